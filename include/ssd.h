@@ -2,8 +2,11 @@
  * ssd.h -- C ABI of libssd: the Mamba-2 state-space-duality (SSD) layer on one
  * AMD Instinct MI355X (gfx950): chunked prefill scan (also over packed batches
  * of different lengths), O(1) cached decode (one step, or many known steps in
- * one launch with the state on-chip), an optional fused step-size prep, and
- * the Gated DeltaNet decode step of the FPGA decode page (ssd_gdn_*).
+ * one launch with the state on-chip), an optional fused step-size prep, the
+ * Gated DeltaNet decode step of the FPGA decode page (ssd_gdn_*), and the two
+ * attention layers of hybrid stacks: linear attention with one decay per head
+ * (ssd_linattn_*) and causal softmax attention (ssd_attn_*), each over prompts
+ * and for single tokens.
  *
  * The operation.  "Compiler-First State Space Duality and Portable O(1)
  * Autoregressive Caching for Inference" (section 2, methodology) describes
@@ -297,6 +300,116 @@ ssd_status ssd_gdn_decode_step(const ssd_gdn_dims *dims, const void *q, const vo
 ssd_status ssd_gdn_decode_steps(const ssd_gdn_dims *dims, int64_t nsteps, const void *q,
                                 const void *k, const void *v, const float *g, const float *beta,
                                 float *state, void *o, void *stream);
+
+/*
+ * Linear attention with one decay per head.  Per sequence and value head j,
+ * with query/key head i = j / (Hv / Hk) (grouped as in ssd_gdn_decode_step) and
+ * lambda = exp(log_decay[j]):
+ *     S_t = lambda S_{t-1} + k[t,i] v[t,j]^T      (S is [dk, dv] fp32)
+ *     o[t,j] = scale S_t^T q[t,i]
+ * ssd_linattn_chunk_scan evaluates it for t = 1..L of every batch row,
+ * ssd_linattn_chunk_scan_varlen over a packed batch (sequence i holds rows
+ * cu_seqlens[i] .. cu_seqlens[i+1] - 1; cu_seqlens is a HOST array of batch + 1
+ * offsets as in ssd_chunk_scan_varlen, and dims->seqlen the rows in all), and
+ * ssd_linattn_decode_step for one more token per sequence.
+ *   q, k [B, L, Hk, dk], v, o [B, L, Hv, dv]  io_dtype (scan)
+ *   q, k [T, Hk, dk],    v, o [T, Hv, dv]     io_dtype (varlen, T = seqlen)
+ *   q, k [B, Hk, dk],    v, o [B, Hv, dv]     io_dtype (decode step)
+ *   log_decay [Hv] fp32, <= 0 (0: nothing is forgotten; -infinity: no memory)
+ *   states [B, Hv, dk, dv] fp32 (initial_state NULL: zero); final_state may be
+ *     initial_state; the decode step updates its state in place
+ * Tokens of q, k and v may lie further apart than their heads need, as in
+ * slices of one projection: {q,k,v}_stride is the distance between consecutive
+ * tokens (rows b L + t of the scan) in elements, 0 for contiguous rows.  o is
+ * contiguous.  A sequence of length 0 hands its state through.
+ * Supported: dk, dv in {64, 128, 256}, strides up to 2^22, io_dtype SSD_F32 or
+ * SSD_BF16.  Scan alignment: q, k, v, o, states and workspace 16 bytes, strides
+ * whole 16 bytes; decode step: state 16 bytes, the rest element-aligned.  o
+ * must not overlap any input, state or the workspace, a final state no input.
+ * Results are deterministic, and a packed batch gives what its sequences give
+ * one by one up to rounding.
+ */
+typedef struct ssd_linattn_dims {
+    int64_t batch;     /* B >= 0 (sequences)                                  */
+    int64_t seqlen;    /* L >= 0; rows in all for varlen; decode: ignored     */
+    int64_t qk_heads;  /* Hk >= 1                                             */
+    int64_t v_heads;   /* Hv >= 1, Hv % Hk == 0                               */
+    int64_t dk, dv;    /* key and value dimensions                            */
+    int64_t q_stride, k_stride, v_stride; /* elements between tokens, 0 = contiguous */
+    float scale;       /* finite                                              */
+    int32_t io_dtype;  /* ssd_dtype of q, k, v, o                             */
+} ssd_linattn_dims;
+
+ssd_status ssd_linattn_chunk_scan_workspace_size(const ssd_linattn_dims *dims, size_t *bytes);
+ssd_status ssd_linattn_chunk_scan(const ssd_linattn_dims *dims, const void *q, const void *k,
+                                  const void *v, const float *log_decay,
+                                  const float *initial_state, void *o, float *final_state,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+ssd_status ssd_linattn_chunk_scan_varlen_workspace_size(const ssd_linattn_dims *dims,
+                                                        const int64_t *cu_seqlens, size_t *bytes);
+ssd_status ssd_linattn_chunk_scan_varlen(const ssd_linattn_dims *dims, const int64_t *cu_seqlens,
+                                         const void *q, const void *k, const void *v,
+                                         const float *log_decay, const float *initial_states,
+                                         void *o, float *final_states, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+ssd_status ssd_linattn_decode_step(const ssd_linattn_dims *dims, const void *q, const void *k,
+                                   const void *v, const float *log_decay, float *state, void *o,
+                                   void *stream);
+
+/*
+ * ssd_attn_prefill -- causal softmax attention over a packed batch of prompts.
+ * Sequence i has the query rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 and the
+ * kv_lens[i] key/value rows from kv_starts[i] on (rows of k and v: a packed
+ * array, or a padded cache [B, M, Hkv, D] taken as B M rows).  Its last query
+ * sees all its keys, the one before it one fewer, and so on: with keys of an
+ * earlier part of the sequence in front, this is the next part of a long
+ * prompt.  Query head h reads key head h / (Hq / Hkv):
+ *     o[t,h] = sum_s softmax_s(scale q[t,h] . k[s,h']) v[s,h']   (visible s)
+ * A query that sees no key (kv_lens[i] < its queries) gets o = 0.  With
+ * kv_starts and kv_lens NULL the keys are the prompts' own rows (kv_rows ==
+ * q_rows).  cu_seqlens, kv_starts and kv_lens are HOST arrays.
+ *   q, o [q_rows, Hq, D], k, v [kv_rows, Hkv, D]  io_dtype
+ * Strides as in ssd_linattn_dims (o contiguous).  Supported: D in {64, 128,
+ * 256}, strides up to 2^22.  Alignment 16 bytes, strides whole 16 bytes.  o must
+ * not overlap an input.  Rows of k and v outside the sequences are not read.
+ */
+typedef struct ssd_attn_dims {
+    int64_t batch;     /* sequences, >= 0                                     */
+    int64_t q_rows;    /* rows of q and o (prefill); decode: ignored          */
+    int64_t kv_rows;   /* rows of k and v (prefill); decode: M, rows of each
+                          sequence's cache                                    */
+    int64_t q_heads;   /* Hq >= 1, Hq % Hkv == 0                              */
+    int64_t kv_heads;  /* Hkv >= 1                                            */
+    int64_t head_dim;  /* D                                                   */
+    int64_t q_stride, k_stride, v_stride; /* elements between rows, 0 = contiguous */
+    float scale;       /* finite                                              */
+    int32_t io_dtype;  /* ssd_dtype of q, k, v, o and the caches              */
+} ssd_attn_dims;
+
+ssd_status ssd_attn_prefill(const ssd_attn_dims *dims, const int64_t *cu_seqlens,
+                            const int64_t *kv_starts, const int64_t *kv_lens, const void *q,
+                            const void *k, const void *v, void *o, void *stream);
+
+/*
+ * ssd_attn_decode_step -- one token per sequence over a padded key/value cache:
+ * k[b] and v[b] are written to row lengths[b] of the caches, and q[b] attends
+ * rows 0 .. lengths[b] (the new one included).  lengths is a DEVICE array that
+ * the call reads and does not change.  A length outside [0, M) marks an unused
+ * slot: o[b] = 0 and its cache stays as it is.  Rows after lengths[b] are not
+ * read.
+ *   q, o [B, Hq, D], k, v [B, Hkv, D], k_cache, v_cache [B, M, Hkv, D] io_dtype
+ *   lengths [B] int32
+ * {q,k,v}_stride: elements between the batch rows of q, k, v (0 = contiguous).
+ * Supported shapes and alignment as for ssd_attn_prefill, M < 2^31 - 4096.  The
+ * caches and o must not overlap an input, each other or the workspace.  The
+ * workspace holds partial results between the call's kernels: one per call that
+ * may run at the same time (also per captured graph that may).
+ */
+ssd_status ssd_attn_decode_workspace_size(const ssd_attn_dims *dims, size_t *bytes);
+ssd_status ssd_attn_decode_step(const ssd_attn_dims *dims, const void *q, const void *k,
+                                const void *v, void *k_cache, void *v_cache,
+                                const int32_t *lengths, void *o, void *workspace,
+                                size_t workspace_bytes, void *stream);
 
 /*
  * ssd_chunk_scan_timed -- measurement entry point: the same computation as

@@ -18,6 +18,12 @@ to pass u instead of dt; the step size is then softplus(u + dt_bias) in the kern
     ssd_chunk_scan_varlen(x, dt, A, B, C, D, cu_seqlens, chunk, ...) -> (y, final_states)
     ssd_gdn_decode_step(q, k, v, g, beta, state, o=None) -> o   (Gated DeltaNet step)
     ssd_gdn_decode_steps(q, k, v, g, beta, state, o=None) -> o  (S steps in one launch)
+and the attention layers of hybrid stacks:
+    ssd_linattn_chunk_scan(q, k, v, log_decay, initial_state=None, ...) -> (o, final_state)
+    ssd_linattn_chunk_scan_varlen(q, k, v, log_decay, cu_seqlens, ...) -> (o, final_states)
+    ssd_linattn_decode_step(q, k, v, log_decay, state, o=None) -> o
+    ssd_attn_prefill(q, k, v, cu_seqlens, kv_starts=None, kv_lens=None, ...) -> o
+    ssd_attn_decode_step(q, k, v, k_cache, v_cache, lengths, ...) -> o  (cache appended in place)
 """
 from __future__ import annotations
 
@@ -37,7 +43,11 @@ STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL", 2: "SSD_ERR_SHAPE", 3: "SSD_ERR_UNSUPP
 EXPORTS = ("ssd_status_string", "ssd_version", "ssd_state_init", "ssd_chunk_scan_workspace_size",
            "ssd_chunk_scan", "ssd_decode_step", "ssd_decode_steps", "ssd_chunk_scan_timed",
            "ssd_chunk_scan_varlen_workspace_size", "ssd_chunk_scan_varlen",
-           "ssd_gdn_decode_step", "ssd_gdn_decode_steps", "ssd_chunk_scan_noalloc")
+           "ssd_gdn_decode_step", "ssd_gdn_decode_steps", "ssd_chunk_scan_noalloc",
+           "ssd_linattn_chunk_scan_workspace_size", "ssd_linattn_chunk_scan",
+           "ssd_linattn_chunk_scan_varlen_workspace_size", "ssd_linattn_chunk_scan_varlen",
+           "ssd_linattn_decode_step", "ssd_attn_prefill", "ssd_attn_decode_workspace_size",
+           "ssd_attn_decode_step")
 NOALLOC_SCRATCH_BYTES = 96 << 20   # SSD_NOALLOC_SCRATCH_BYTES of include/ssd.h
 
 
@@ -106,6 +116,18 @@ def load(path: str | None = None):
     lib.ssd_gdn_decode_step.restype = ctypes.c_int
     lib.ssd_gdn_decode_steps.argtypes = [ctypes.POINTER(SsdGdnDims), ctypes.c_int64] + [vp] * 8
     lib.ssd_gdn_decode_steps.restype = ctypes.c_int
+    lin, att, sz = ctypes.POINTER(SsdLinattnDims), ctypes.POINTER(SsdAttnDims), ctypes.c_size_t
+    for name, args in (
+            ("ssd_linattn_chunk_scan_workspace_size", [lin, i64p]),
+            ("ssd_linattn_chunk_scan", [lin] + [vp] * 8 + [sz, vp]),
+            ("ssd_linattn_chunk_scan_varlen_workspace_size", [lin, cu, i64p]),
+            ("ssd_linattn_chunk_scan_varlen", [lin, cu] + [vp] * 8 + [sz, vp]),
+            ("ssd_linattn_decode_step", [lin] + [vp] * 7),
+            ("ssd_attn_prefill", [att] + [cu] * 3 + [vp] * 5),
+            ("ssd_attn_decode_workspace_size", [att, i64p]),
+            ("ssd_attn_decode_step", [att] + [vp] * 8 + [sz, vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -457,4 +479,253 @@ def ssd_gdn_decode_steps(q, k, v, g, beta, state, o=None, stream=None):
     _check("ssd_gdn_decode_steps", load().ssd_gdn_decode_steps(
         ctypes.byref(d), ctypes.c_int64(nsteps), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
         _ptr(state), _ptr(o), _stream(stream, dev)))
+    return o
+
+
+# --------------------------------------------------------------------------
+# Linear attention and softmax attention
+# --------------------------------------------------------------------------
+class SsdLinattnDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("qk_heads", ctypes.c_int64), ("v_heads", ctypes.c_int64),
+                ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("io_dtype", ctypes.c_int32)]
+
+
+class SsdAttnDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("q_rows", ctypes.c_int64),
+                ("kv_rows", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("io_dtype", ctypes.c_int32)]
+
+
+def _guard(di):
+    """The tensors' device as the current one for a call's launches."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == di else torch.cuda.device(di)
+
+
+def _row_stride(name, t, di, dtype, shape):
+    """Checks a [tokens.., heads, dim] argument whose tokens may lie further apart
+    than its heads need (a slice of one projection), and returns the distance
+    between tokens in elements."""
+    try:
+        ok = t.get_device() == di and t.dtype == dtype and t.shape == shape
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
+    if not ok:
+        _need(name, t, di, dtype)
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    width = shape[-1] * shape[-2]
+    if t.is_contiguous():
+        return width
+    st = t.stride()
+    if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    row = width
+    if len(shape) == 4 and shape[0] > 1 and shape[1] > 1:
+        row = st[1]
+        if st[0] != shape[1] * row:
+            raise ValueError(f"{name}: consecutive tokens must lie evenly spaced over the batch")
+    elif len(shape) == 4:
+        row = st[1] if shape[1] > 1 else st[0] if shape[0] > 1 else width
+    elif shape[0] > 1:
+        row = st[0]
+    if row < width:
+        raise ValueError(f"{name}: tokens overlap")
+    return row
+
+
+def _linattn_dims(q, k, v, lead, dims_of):
+    """(dims, device, state heads/dims) of a linear-attention call whose tokens have
+    `lead` leading dimensions."""
+    dev = _device_of(q)
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        want = {1: ("[T, Hk, dk]", "[T, Hv, dv]"), 2: ("[B, L, Hk, dk]", "[B, L, Hv, dv]")}[lead]
+        raise ValueError(f"q, k must be {want[0]} and v {want[1]}")
+    shp = q.shape
+    Hk, dk = shp[-2:]
+    Hv, dv = v.shape[-2:]
+    qs = _row_stride("q", q, dev, q.dtype, shp)
+    ks = _row_stride("k", k, dev, q.dtype, shp)
+    vs = _row_stride("v", v, dev, q.dtype, shp[:lead] + (Hv, dv))
+    batch, seqlen, scale = dims_of
+    return SsdLinattnDims(batch, seqlen, Hk, Hv, dk, dv, qs, ks, vs, scale, _io_dtype(q)), dev
+
+
+def _linattn_scan(fn, lead, q, k, v, log_decay, cu_seqlens, initial_state, o, final_state, workspace,
+                  scale, stream):
+    lib = load()
+    cu = cup = None
+    if lead == 1:
+        cu, cup = _cu_array(cu_seqlens)
+        if len(cu) < 1:
+            raise ValueError("cu_seqlens must hold at least one offset")
+    nseq = len(cu) - 1 if lead == 1 else q.shape[0]
+    d, dev = _linattn_dims(q, k, v, lead, (nseq, q.shape[lead - 1], scale))
+    f32 = torch.float32
+    state = (nseq, d.v_heads, d.dk, d.dv)
+    _need("log_decay", log_decay, dev, f32, (d.v_heads,))
+    _need("initial_state", initial_state, dev, f32, state, optional=True)
+    _need("o", o, dev, q.dtype, v.shape, optional=True)
+    _need("final_state", final_state, dev, f32, state, optional=True)
+    _need("workspace", workspace, dev, optional=True)
+    args = [ctypes.byref(d)] + ([cup] if lead == 1 else [])
+    n = ctypes.c_size_t(0)
+    _check(fn + "_workspace_size", getattr(lib, fn + "_workspace_size")(*args, ctypes.byref(n)))
+    need = n.value
+    with _guard(dev):
+        with _on(stream):
+            if o is None:
+                o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            if final_state is None:
+                final_state = torch.empty(state, dtype=f32, device=v.device)
+            if workspace is None and need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(fn, getattr(lib, fn)(*args, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                    _ptr(initial_state), _ptr(o), _ptr(final_state),
+                                    _ptr(workspace), ws_bytes, _stream(stream, dev)))
+    return o, final_state
+
+
+def ssd_linattn_chunk_scan_workspace_size(batch, seqlen, qk_heads, v_heads, dk, dv,
+                                          io_dtype=SSD_BF16) -> int:
+    d = SsdLinattnDims(batch, seqlen, qk_heads, v_heads, dk, dv, 0, 0, 0, 1.0, io_dtype)
+    n = ctypes.c_size_t(0)
+    _check("ssd_linattn_chunk_scan_workspace_size",
+           load().ssd_linattn_chunk_scan_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return int(n.value)
+
+
+def ssd_linattn_chunk_scan(q, k, v, log_decay, initial_state=None, o=None, final_state=None,
+                           workspace=None, scale=1.0, stream=None):
+    """Linear attention with one decay per head over prompts: q, k [B, L, Hk, dk],
+    v [B, L, Hv, dv], log_decay [Hv] fp32; returns (o [B, L, Hv, dv], final_state
+    [B, Hv, dk, dv] fp32).  q, k and v may be slices of one projection."""
+    return _linattn_scan("ssd_linattn_chunk_scan", 2, q, k, v, log_decay, None, initial_state, o,
+                         final_state, workspace, scale, stream)
+
+
+def ssd_linattn_chunk_scan_varlen_workspace_size(cu_seqlens, qk_heads, v_heads, dk, dv,
+                                                 io_dtype=SSD_BF16) -> int:
+    cu, cup = _cu_array(cu_seqlens)
+    d = SsdLinattnDims(len(cu) - 1, int(cu[-1]), qk_heads, v_heads, dk, dv, 0, 0, 0, 1.0, io_dtype)
+    n = ctypes.c_size_t(0)
+    _check("ssd_linattn_chunk_scan_varlen_workspace_size",
+           load().ssd_linattn_chunk_scan_varlen_workspace_size(ctypes.byref(d), cup, ctypes.byref(n)))
+    return int(n.value)
+
+
+def ssd_linattn_chunk_scan_varlen(q, k, v, log_decay, cu_seqlens, initial_states=None, o=None,
+                                  final_states=None, workspace=None, scale=1.0, stream=None):
+    """ssd_linattn_chunk_scan of a packed batch: q, k [T, Hk, dk], v [T, Hv, dv];
+    sequence i is tokens cu_seqlens[i] .. cu_seqlens[i+1]-1 (a host sequence of
+    S + 1 offsets).  Returns (o [T, Hv, dv], final_states [S, Hv, dk, dv])."""
+    return _linattn_scan("ssd_linattn_chunk_scan_varlen", 1, q, k, v, log_decay, cu_seqlens,
+                         initial_states, o, final_states, workspace, scale, stream)
+
+
+def ssd_linattn_decode_step(q, k, v, log_decay, state, o=None, scale=1.0, stream=None):
+    """One linear-attention decode step: q, k [B, Hk, dk], v [B, Hv, dv], state
+    [B, Hv, dk, dv] fp32 updated in place; returns o [B, Hv, dv]."""
+    d, dev = _linattn_dims(q, k, v, 1, (q.shape[0], 1, scale))
+    f32 = torch.float32
+    _need("log_decay", log_decay, dev, f32, (d.v_heads,))
+    _need("state", state, dev, f32, (d.batch, d.v_heads, d.dk, d.dv))
+    _need("o", o, dev, q.dtype, v.shape, optional=True)
+    with _guard(dev):
+        if o is None:
+            with _on(stream):
+                o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        _check("ssd_linattn_decode_step", load().ssd_linattn_decode_step(
+            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o),
+            _stream(stream, dev)))
+    return o
+
+
+def ssd_attn_prefill(q, k, v, cu_seqlens, kv_starts=None, kv_lens=None, scale=None, o=None,
+                     stream=None):
+    """Causal softmax attention over packed prompts: q [T, Hq, D], k, v [Tk, Hkv, D];
+    sequence i has queries cu_seqlens[i] .. cu_seqlens[i+1]-1 and, unless kv_starts
+    and kv_lens are None (the prompts' own rows), kv_lens[i] keys from row
+    kv_starts[i] on, the last query seeing them all (host sequences).  scale
+    defaults to 1 / sqrt(D).  Returns o [T, Hq, D]."""
+    dev = _device_of(q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, Hq, D] and k, v [Tk, Hkv, D]")
+    T, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    qs = _row_stride("q", q, dev, q.dtype, q.shape)
+    ks = _row_stride("k", k, dev, q.dtype, (Tk, Hkv, D))
+    vs = _row_stride("v", v, dev, q.dtype, (Tk, Hkv, D))
+    _need("o", o, dev, q.dtype, q.shape, optional=True)
+    cu, cup = _cu_array(cu_seqlens)
+    if len(cu) < 1:
+        raise ValueError("cu_seqlens must hold at least one offset")
+    st, stp = _cu_array(kv_starts) if kv_starts is not None else (None, None)
+    kl, klp = _cu_array(kv_lens) if kv_lens is not None else (None, None)
+    for name, a in (("kv_starts", st), ("kv_lens", kl)):
+        if a is not None and len(a) != len(cu) - 1:
+            raise ValueError(f"{name} must hold one entry per sequence")
+    d = SsdAttnDims(len(cu) - 1, T, Tk, Hq, Hkv, D, qs, ks, vs,
+                    D ** -0.5 if scale is None else scale, _io_dtype(q))
+    with _guard(dev):
+        if o is None:
+            with _on(stream):
+                o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _check("ssd_attn_prefill", load().ssd_attn_prefill(
+            ctypes.byref(d), cup, stp, klp, _ptr(q), _ptr(k), _ptr(v), _ptr(o),
+            _stream(stream, dev)))
+    return o
+
+
+def ssd_attn_decode_workspace_size(batch, cache_rows, q_heads, kv_heads, head_dim,
+                                   io_dtype=SSD_BF16) -> int:
+    d = SsdAttnDims(batch, 0, cache_rows, q_heads, kv_heads, head_dim, 0, 0, 0, 1.0, io_dtype)
+    n = ctypes.c_size_t(0)
+    _check("ssd_attn_decode_workspace_size",
+           load().ssd_attn_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return int(n.value)
+
+
+def ssd_attn_decode_step(q, k, v, k_cache, v_cache, lengths, scale=None, o=None, workspace=None,
+                         stream=None):
+    """One softmax-attention decode step: k, v [B, Hkv, D] are written to row
+    lengths[b] of k_cache, v_cache [B, M, Hkv, D], and q [B, Hq, D] attends rows
+    0 .. lengths[b].  lengths [B] int32 is a device tensor and is left as it is; a
+    length outside [0, M) marks an unused slot (o[b] = 0, cache untouched).
+    Returns o [B, Hq, D]."""
+    dev = _device_of(q)
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [B, Hq, D], k, v [B, Hkv, D] and the caches [B, M, Hkv, D]")
+    B, Hq, D = q.shape
+    Hkv, M = k.shape[1], k_cache.shape[1]
+    qs = _row_stride("q", q, dev, q.dtype, q.shape)
+    ks = _row_stride("k", k, dev, q.dtype, (B, Hkv, D))
+    vs = _row_stride("v", v, dev, q.dtype, (B, Hkv, D))
+    _need("k_cache", k_cache, dev, q.dtype, (B, M, Hkv, D))
+    _need("v_cache", v_cache, dev, q.dtype, (B, M, Hkv, D))
+    _need("lengths", lengths, dev, torch.int32, (B,))
+    _need("o", o, dev, q.dtype, q.shape, optional=True)
+    _need("workspace", workspace, dev, optional=True)
+    lib = load()
+    d = SsdAttnDims(B, 0, M, Hq, Hkv, D, qs, ks, vs, D ** -0.5 if scale is None else scale,
+                    _io_dtype(q))
+    n = ctypes.c_size_t(0)
+    _check("ssd_attn_decode_workspace_size",
+           lib.ssd_attn_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    with _guard(dev):
+        with _on(stream):
+            if o is None:
+                o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if workspace is None and n.value > 0:
+                workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check("ssd_attn_decode_step", lib.ssd_attn_decode_step(
+            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
+            _ptr(lengths), _ptr(o), _ptr(workspace), ws_bytes, _stream(stream, dev)))
     return o

@@ -3,11 +3,13 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 #include <vector>
 
 #include "ssd.h"
+#include "ssd_attn.h"
 #include "ssd_kernels.h"
 
 #define SSD_EXPORT extern "C" __attribute__((visibility("default")))
@@ -893,4 +895,394 @@ SSD_EXPORT ssd_status ssd_gdn_decode_steps(const ssd_gdn_dims *dims, int64_t nst
     return device_status(ssd::launch_gdn_decode_steps(
         dims->io_dtype == SSD_BF16, nsteps, dims->batch, dims->qk_heads, dims->v_heads, dims->dk,
         dims->dv, q, k, v, g, beta, state, o, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Linear attention and softmax attention
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxStride = 1 << 22;   // a 64-row tile's byte offsets stay in 32 bits
+constexpr int64_t kMaxRows = INT32_MAX - 4096;
+
+bool head_size(int64_t d)
+{
+    return d == 64 || d == 128 || d == 256;
+}
+
+// The row stride of a [rows, heads, dim] tensor (0: contiguous rows), and its span.
+struct Rows {
+    int64_t stride, bytes;
+};
+ssd_status rows_of(int64_t stride, int64_t rows, int64_t width, int64_t esz, bool vec, Rows *out)
+{
+    if (stride < 0)
+        return SSD_ERR_SHAPE;
+    out->stride = stride > 0 ? stride : width;
+    if (out->stride < width)
+        return SSD_ERR_SHAPE;
+    if (out->stride > kMaxStride)
+        return SSD_ERR_UNSUPPORTED;
+    if (vec && out->stride * esz % 16 != 0)
+        return SSD_ERR_ALIGNMENT;
+    int64_t t;
+    if (!mul_ok(rows, out->stride, &t) || !mul_ok(t, 4, &t))
+        return SSD_ERR_SHAPE;
+    out->bytes = rows > 0 ? ((rows - 1) * out->stride + width) * esz : 0;
+    return SSD_OK;
+}
+
+struct LinShape {
+    Rows q, k, v;
+    int64_t esz, rows, o_bytes, state_bytes;
+};
+
+ssd_status linattn_dims_check(const ssd_linattn_dims *d, int64_t rows, bool vec, LinShape *sh)
+{
+    if (!d)
+        return SSD_ERR_NULL;
+    if (d->batch < 0 || rows < 0 || d->qk_heads < 1 || d->v_heads < 1 ||
+        d->v_heads % d->qk_heads != 0)
+        return SSD_ERR_SHAPE;
+    if ((d->io_dtype != SSD_F32 && d->io_dtype != SSD_BF16) || !head_size(d->dk) ||
+        !head_size(d->dv) || d->v_heads > kMaxHeads || !std::isfinite(d->scale))
+        return SSD_ERR_UNSUPPORTED;
+    if (d->v_heads * d->dv > kMaxStride)
+        return SSD_ERR_UNSUPPORTED;
+    sh->esz = d->io_dtype == SSD_BF16 ? 2 : 4;
+    sh->rows = rows;
+    ssd_status st;
+    if ((st = rows_of(d->q_stride, rows, d->qk_heads * d->dk, sh->esz, vec, &sh->q)) != SSD_OK ||
+        (st = rows_of(d->k_stride, rows, d->qk_heads * d->dk, sh->esz, vec, &sh->k)) != SSD_OK ||
+        (st = rows_of(d->v_stride, rows, d->v_heads * d->dv, sh->esz, vec, &sh->v)) != SSD_OK)
+        return st;
+    int64_t t;
+    if (!mul_ok(rows, d->v_heads * d->dv * 4, &t) ||
+        !mul_ok(d->batch, d->v_heads * d->dk * d->dv * 4, &t))
+        return SSD_ERR_SHAPE;
+    if (d->batch * d->v_heads * (d->dv / 32) > INT32_MAX)
+        return SSD_ERR_UNSUPPORTED;
+    sh->o_bytes = rows * d->v_heads * d->dv * sh->esz;
+    sh->state_bytes = d->batch * d->v_heads * d->dk * d->dv * 4;
+    return SSD_OK;
+}
+
+// The sequences of a scan call: batch rows of dims->seqlen tokens, or the packed
+// ones of cu.
+ssd_status linattn_seqs(const ssd_linattn_dims *d, const int64_t *cu, bool varlen, LinShape *sh,
+                        std::vector<ssd::LinSeq> *seqs)
+{
+    if (!d || (varlen && !cu))
+        return SSD_ERR_NULL;
+    if (d->batch < 0 || d->seqlen < 0)
+        return SSD_ERR_SHAPE;
+    int64_t rows = d->seqlen;
+    if (!varlen && !mul_ok(d->batch, d->seqlen, &rows))
+        return SSD_ERR_SHAPE;
+    const ssd_status st = linattn_dims_check(d, rows, true, sh);
+    if (st != SSD_OK)
+        return st;
+    if (varlen) {
+        if (cu[0] != 0 || cu[d->batch] != d->seqlen)
+            return SSD_ERR_SHAPE;
+        for (int64_t i = 0; i < d->batch; ++i)
+            if (cu[i + 1] < cu[i])
+                return SSD_ERR_SHAPE;
+    }
+    seqs->resize((size_t)d->batch);
+    for (int64_t i = 0; i < d->batch; ++i) {
+        ssd::LinSeq &s = (*seqs)[(size_t)i];
+        s.tok = varlen ? cu[i] : i * d->seqlen;
+        s.len = varlen ? cu[i + 1] - cu[i] : d->seqlen;
+        if (s.len > kMaxRows)
+            return SSD_ERR_UNSUPPORTED;
+    }
+    return SSD_OK;
+}
+
+ssd_status linattn_plan(const ssd_linattn_dims *d, const std::vector<ssd::LinSeq> &seqs,
+                        ssd::LinPlan *plan)
+{
+    *plan = ssd::plan_linattn(d->io_dtype == SSD_BF16, (int64_t)seqs.size(), seqs.data(),
+                              d->qk_heads, d->v_heads, d->dk, d->dv);
+    return SSD_OK;
+}
+
+ssd_status linattn_workspace(const ssd_linattn_dims *d, const int64_t *cu, bool varlen, size_t *bytes)
+{
+    try {
+        LinShape sh;
+        std::vector<ssd::LinSeq> seqs;
+        ssd::LinPlan plan;
+        ssd_status st = linattn_seqs(d, cu, varlen, &sh, &seqs);
+        if (st == SSD_OK && !bytes)
+            st = SSD_ERR_NULL;
+        if (st == SSD_OK && (st = linattn_plan(d, seqs, &plan)) == SSD_OK)
+            *bytes = plan.ws_bytes;
+        return st;
+    } catch (...) {   // host memory
+        return SSD_ERR_DEVICE;
+    }
+}
+
+ssd_status linattn_scan(const ssd_linattn_dims *d, const int64_t *cu, bool varlen, const void *q,
+                        const void *k, const void *v, const float *g, const float *init, void *o,
+                        float *fin, void *ws, size_t ws_bytes, hipStream_t s)
+{
+    try {
+        LinShape sh;
+        std::vector<ssd::LinSeq> seqs;
+        ssd::LinPlan plan;
+        ssd_status st = linattn_seqs(d, cu, varlen, &sh, &seqs);
+        if (st != SSD_OK)
+            return st;
+        if (d->batch == 0)
+            return SSD_OK;
+        if (!fin || !g || (sh.rows > 0 && (!q || !k || !v || !o)))
+            return SSD_ERR_NULL;
+        if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+            !aligned(fin, 16) || !aligned(init, 16) || !aligned(g, 4))
+            return SSD_ERR_ALIGNMENT;
+        if ((st = linattn_plan(d, seqs, &plan)) != SSD_OK)
+            return st;
+        if (plan.ws_bytes > 0 && (!ws || ws_bytes < plan.ws_bytes))
+            return SSD_ERR_WORKSPACE;
+        if (plan.ws_bytes > 0 && !aligned(ws, 16))
+            return SSD_ERR_ALIGNMENT;
+        const Span so = span(o, sh.o_bytes), sf = span(fin, sh.state_bytes),
+                   si = span(init, init ? sh.state_bytes : 0), sw = span(ws, (int64_t)plan.ws_bytes);
+        const Span ins[] = {span(q, sh.q.bytes), span(k, sh.k.bytes), span(v, sh.v.bytes),
+                            span(g, d->v_heads * 4)};
+        for (const Span &in : ins)
+            if (overlap(so, in) || overlap(sf, in) || overlap(sw, in))
+                return SSD_ERR_ALIAS;
+        if (overlap(so, sf) || overlap(so, si) || overlap(so, sw) || overlap(sw, sf) ||
+            overlap(sw, si) || (init && init != fin && overlap(sf, si)))
+            return SSD_ERR_ALIAS;
+        return device_status(ssd::launch_linattn_scan(
+            d->io_dtype == SSD_BF16, plan, d->batch, seqs.data(), d->qk_heads, d->v_heads, d->dk,
+            d->dv, sh.q.stride, sh.k.stride, sh.v.stride, d->scale, q, k, v, g, init, o, fin, ws, s));
+    } catch (...) {
+        return SSD_ERR_DEVICE;
+    }
+}
+
+struct AttnShape {
+    Rows q, k, v;
+    int64_t esz;
+};
+
+ssd_status attn_dims_check(const ssd_attn_dims *d, int64_t q_rows, int64_t kv_rows, AttnShape *sh)
+{
+    if (!d)
+        return SSD_ERR_NULL;
+    if (d->batch < 0 || q_rows < 0 || kv_rows < 0 || d->q_heads < 1 || d->kv_heads < 1 ||
+        d->q_heads % d->kv_heads != 0)
+        return SSD_ERR_SHAPE;
+    if ((d->io_dtype != SSD_F32 && d->io_dtype != SSD_BF16) || !head_size(d->head_dim) ||
+        d->q_heads > kMaxHeads || !std::isfinite(d->scale))
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t wq = d->q_heads * d->head_dim, wk = d->kv_heads * d->head_dim;
+    if (wq > kMaxStride)
+        return SSD_ERR_UNSUPPORTED;
+    sh->esz = d->io_dtype == SSD_BF16 ? 2 : 4;
+    ssd_status st;
+    if ((st = rows_of(d->q_stride, q_rows, wq, sh->esz, true, &sh->q)) != SSD_OK ||
+        (st = rows_of(d->k_stride, kv_rows, wk, sh->esz, true, &sh->k)) != SSD_OK ||
+        (st = rows_of(d->v_stride, kv_rows, wk, sh->esz, true, &sh->v)) != SSD_OK)
+        return st;
+    int64_t t;
+    if (!mul_ok(q_rows, wq * 4, &t))
+        return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
+// Shape checks of a decode call; *cache: bytes of one cache.
+ssd_status attn_decode_check(const ssd_attn_dims *d, AttnShape *sh, int64_t *cache)
+{
+    if (!d)
+        return SSD_ERR_NULL;
+    const ssd_status st = attn_dims_check(d, d->batch, d->batch, sh);
+    if (st != SSD_OK)
+        return st;
+    if (d->kv_rows < 0)
+        return SSD_ERR_SHAPE;
+    if (d->kv_rows > kMaxRows)
+        return SSD_ERR_UNSUPPORTED;
+    int64_t t;
+    if (!mul_ok(d->batch, d->kv_rows, &t) || !mul_ok(t, d->kv_heads * d->head_dim * sh->esz, &t))
+        return SSD_ERR_SHAPE;
+    *cache = t;
+    const int64_t rtiles = (d->q_heads / d->kv_heads + 31) / 32;
+    if (d->batch * d->q_heads > INT32_MAX / 2 || d->batch * d->kv_heads * rtiles > INT32_MAX / 2)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+}  // namespace
+
+SSD_EXPORT ssd_status ssd_linattn_chunk_scan_workspace_size(const ssd_linattn_dims *dims,
+                                                            size_t *bytes)
+{
+    return linattn_workspace(dims, nullptr, false, bytes);
+}
+
+SSD_EXPORT ssd_status ssd_linattn_chunk_scan_varlen_workspace_size(const ssd_linattn_dims *dims,
+                                                                   const int64_t *cu_seqlens,
+                                                                   size_t *bytes)
+{
+    return linattn_workspace(dims, cu_seqlens, true, bytes);
+}
+
+SSD_EXPORT ssd_status ssd_linattn_chunk_scan(const ssd_linattn_dims *dims, const void *q,
+                                             const void *k, const void *v, const float *log_decay,
+                                             const float *initial_state, void *o,
+                                             float *final_state, void *workspace,
+                                             size_t workspace_bytes, void *stream)
+{
+    return linattn_scan(dims, nullptr, false, q, k, v, log_decay, initial_state, o, final_state,
+                        workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+SSD_EXPORT ssd_status ssd_linattn_chunk_scan_varlen(const ssd_linattn_dims *dims,
+                                                    const int64_t *cu_seqlens, const void *q,
+                                                    const void *k, const void *v,
+                                                    const float *log_decay,
+                                                    const float *initial_states, void *o,
+                                                    float *final_states, void *workspace,
+                                                    size_t workspace_bytes, void *stream)
+{
+    return linattn_scan(dims, cu_seqlens, true, q, k, v, log_decay, initial_states, o,
+                        final_states, workspace, workspace_bytes,
+                        static_cast<hipStream_t>(stream));
+}
+
+SSD_EXPORT ssd_status ssd_linattn_decode_step(const ssd_linattn_dims *dims, const void *q,
+                                              const void *k, const void *v,
+                                              const float *log_decay, float *state, void *o,
+                                              void *stream)
+{
+    LinShape sh;
+    const ssd_status st = linattn_dims_check(dims, dims ? dims->batch : 0, false, &sh);
+    if (st != SSD_OK || dims->batch == 0)
+        return st;
+    if (!q || !k || !v || !log_decay || !state || !o)
+        return SSD_ERR_NULL;
+    if (!aligned(state, 16) || !aligned(q, sh.esz) || !aligned(k, sh.esz) || !aligned(v, sh.esz) ||
+        !aligned(o, sh.esz) || !aligned(log_decay, 4))
+        return SSD_ERR_ALIGNMENT;
+    const Span ss = span(state, sh.state_bytes), so = span(o, sh.o_bytes);
+    const Span ins[] = {span(q, sh.q.bytes), span(k, sh.k.bytes), span(v, sh.v.bytes),
+                        span(log_decay, dims->v_heads * 4)};
+    for (const Span &in : ins)
+        if (overlap(so, in) || overlap(ss, in))
+            return SSD_ERR_ALIAS;
+    if (overlap(so, ss))
+        return SSD_ERR_ALIAS;
+    return device_status(ssd::launch_linattn_decode(
+        dims->io_dtype == SSD_BF16, dims->batch, dims->qk_heads, dims->v_heads, dims->dk, dims->dv,
+        sh.q.stride, sh.k.stride, sh.v.stride, dims->scale, q, k, v, log_decay, state, o,
+        static_cast<hipStream_t>(stream)));
+}
+
+SSD_EXPORT ssd_status ssd_attn_prefill(const ssd_attn_dims *dims, const int64_t *cu_seqlens,
+                                       const int64_t *kv_starts, const int64_t *kv_lens,
+                                       const void *q, const void *k, const void *v, void *o,
+                                       void *stream)
+{
+    try {
+        AttnShape sh;
+        const ssd_status st = attn_dims_check(dims, dims ? dims->q_rows : 0,
+                                              dims ? dims->kv_rows : 0, &sh);
+        if (st != SSD_OK)
+            return st;
+        if (!cu_seqlens || !kv_starts != !kv_lens)
+            return SSD_ERR_NULL;
+        const int64_t S = dims->batch, grp = dims->q_heads / dims->kv_heads;
+        if (cu_seqlens[0] != 0 || cu_seqlens[S] != dims->q_rows ||
+            (!kv_lens && dims->kv_rows != dims->q_rows))
+            return SSD_ERR_SHAPE;
+        std::vector<ssd::AttnSeq> seqs;
+        seqs.reserve((size_t)S);
+        for (int64_t i = 0; i < S; ++i) {
+            const int64_t lq = cu_seqlens[i + 1] - cu_seqlens[i];
+            const int64_t lk = kv_lens ? kv_lens[i] : lq, k0 = kv_lens ? kv_starts[i] : cu_seqlens[i];
+            if (lq < 0 || lk < 0 || k0 < 0 || k0 > dims->kv_rows || lk > dims->kv_rows - k0)
+                return SSD_ERR_SHAPE;
+            if (lq > kMaxRows || lk > kMaxRows || lq > kMaxRows / grp)
+                return SSD_ERR_UNSUPPORTED;
+            if (lq > 0)
+                seqs.push_back(ssd::AttnSeq{cu_seqlens[i], k0, (int32_t)lq, (int32_t)lk});
+        }
+        if (seqs.empty())
+            return SSD_OK;
+        if (!q || !o || (dims->kv_rows > 0 && (!k || !v)))
+            return SSD_ERR_NULL;
+        if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
+            return SSD_ERR_ALIGNMENT;
+        const Span so = span(o, dims->q_rows * dims->q_heads * dims->head_dim * sh.esz);
+        if (overlap(so, span(q, sh.q.bytes)) || overlap(so, span(k, sh.k.bytes)) ||
+            overlap(so, span(v, sh.v.bytes)))
+            return SSD_ERR_ALIAS;
+        return device_status(ssd::launch_attn_prefill(
+            dims->io_dtype == SSD_BF16, (int64_t)seqs.size(), seqs.data(), dims->q_heads,
+            dims->kv_heads, dims->head_dim, sh.q.stride, sh.k.stride, sh.v.stride, dims->scale, q,
+            k, v, o, static_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return SSD_ERR_DEVICE;
+    }
+}
+
+SSD_EXPORT ssd_status ssd_attn_decode_workspace_size(const ssd_attn_dims *dims, size_t *bytes)
+{
+    AttnShape sh;
+    int64_t cache;
+    const ssd_status st = attn_decode_check(dims, &sh, &cache);
+    if (st != SSD_OK)
+        return st;
+    if (!bytes)
+        return SSD_ERR_NULL;
+    *bytes = ssd::attn_decode_workspace(dims->batch, dims->kv_rows, dims->q_heads, dims->kv_heads,
+                                        dims->head_dim);
+    return SSD_OK;
+}
+
+SSD_EXPORT ssd_status ssd_attn_decode_step(const ssd_attn_dims *dims, const void *q,
+                                           const void *k, const void *v, void *k_cache,
+                                           void *v_cache, const int32_t *lengths, void *o,
+                                           void *workspace, size_t workspace_bytes, void *stream)
+{
+    AttnShape sh;
+    int64_t cache;
+    const ssd_status st = attn_decode_check(dims, &sh, &cache);
+    if (st != SSD_OK || dims->batch == 0)
+        return st;
+    if (!q || !k || !v || !lengths || !o || (cache > 0 && (!k_cache || !v_cache)))
+        return SSD_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(lengths, 4))
+        return SSD_ERR_ALIGNMENT;
+    const size_t need = ssd::attn_decode_workspace(dims->batch, dims->kv_rows, dims->q_heads,
+                                                   dims->kv_heads, dims->head_dim);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return SSD_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 16))
+        return SSD_ERR_ALIGNMENT;
+    const Span outs[] = {span(o, dims->batch * dims->q_heads * dims->head_dim * sh.esz),
+                         span(k_cache, cache), span(v_cache, cache),
+                         span(workspace, (int64_t)need)};
+    const Span ins[] = {span(q, sh.q.bytes), span(k, sh.k.bytes), span(v, sh.v.bytes),
+                        span(lengths, dims->batch * 4)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Span &in : ins)
+            if (overlap(outs[i], in))
+                return SSD_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j]))
+                return SSD_ERR_ALIAS;
+    }
+    return device_status(ssd::launch_attn_decode(
+        dims->io_dtype == SSD_BF16, dims->batch, dims->kv_rows, dims->q_heads, dims->kv_heads,
+        dims->head_dim, sh.q.stride, sh.k.stride, sh.v.stride, dims->scale, q, k, v, k_cache,
+        v_cache, lengths, o, workspace, static_cast<hipStream_t>(stream)));
 }

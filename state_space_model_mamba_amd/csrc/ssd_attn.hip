@@ -1,0 +1,691 @@
+// Causal softmax attention on gfx950: packed prompts (prefill) and one decode
+// token per sequence over a padded key/value cache.
+//
+// For query token t of a sequence with lq queries and lk keys, query head h and
+// key head h / (Hq / Hkv), keys s <= t + lk - lq being visible:
+//     a_s = scale q_t . k_s,   o_t = sum_s exp(a_s - m) v_s / sum_s exp(a_s - m)
+// for any m; a row that sees no key is 0.  One pass over the keys carries
+// (m, l = sum exp(a_s - m), acc = sum exp(a_s - m) v_s) per row in fp32: when m
+// grows by more than kSlack (log2 units) l and acc are rescaled, otherwise the
+// old m is kept -- the result does not depend on m, and exp(a - m) <= 2^kSlack
+// stays far from overflow -- so that the rescaling pass over acc is rare.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "ssd_attn.h"
+#include "ssd_mma.h"
+
+namespace ssd {
+namespace {
+
+using namespace mx;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;
+constexpr float kNoMax = -1e30f;   // m before the first visible key (finite: m - m is 0)
+// A scale of 0 weights all visible keys alike; it is kept off 0 so that a masked
+// score (-inf) times it stays -inf.
+constexpr float kTinyScale = 1.17549435e-38f;
+
+// ---------------------------------------------------------------------------
+// Prefill
+// ---------------------------------------------------------------------------
+// Rows of a sequence are its (token, head of the group) pairs, token-major, so
+// that all query heads of a key head share its K and V tiles and short prompts
+// still fill the 32-row blocks.  A work-group takes kRows consecutive rows, one
+// 32-row block per wave and qb; the scores are formed transposed (keys x rows):
+// a lane then holds one row, its statistics are per-lane scalars, and the
+// probabilities are the second product's operand as they stand.
+struct SeqTab {
+    static constexpr int kMax = 120;          // sequences per launch (kernel arguments: 4 KB)
+    AttnSeq seq[kMax];
+    int32_t pre[128];                         // first work item of each sequence; then INT32_MAX
+};
+
+struct PrefillArgs {
+    SeqTab tab;
+    const void *q, *k, *v;
+    void *o;
+    int64_t q_stride, k_stride, v_stride;     // elements between rows
+    int Hq, Hkv, grp;
+    float c;                                  // |scale| log2 e
+    int neg;                                  // scale < 0: the queries' signs are flipped
+};
+
+typedef const __attribute__((address_space(4))) PrefillArgs *PrefillArgsPtr;
+
+template <typename T> __device__ __forceinline__ typename Piece<T>::V flip(typename Piece<T>::V v);
+template <> __device__ __forceinline__ bf16x8 flip<__bf16>(bf16x8 v)
+{
+    u32x4 u = __builtin_bit_cast(u32x4, v);
+    return __builtin_bit_cast(bf16x8, u ^ 0x80008000u);
+}
+template <> __device__ __forceinline__ f32x4 flip<float>(f32x4 v)
+{
+    return -v;
+}
+
+template <typename T, int D, int NW, int QB>
+__global__ __launch_bounds__(64 * NW, QB == 1 && D <= 128 ? 2 : 1) void attn_prefill_kernel(
+    PrefillArgs args_in_kernarg)
+{
+    constexpr int KT = sizeof(T) == 2 ? 64 : 32;      // keys per tile
+    constexpr int KB = KT / 32, DB = D / 32;
+    constexpr int E = Piece<T>::E;
+    constexpr int PC = 16 / E * 2 / 2;                // pieces per 32-key block of P
+    constexpr int kRows = 32 * QB * NW;
+    typedef Tile<T, D> TL;
+    typedef typename Piece<T>::V V;
+    static_assert(PC * 2 * E == 32, "pieces of a 32-row block");
+    constexpr int kTileBytes = KT * TL::kPitch;
+    extern __shared__ __align__(1024) unsigned char smem[];   // [2][K tile, V tile]
+
+    const PrefillArgsPtr a = (PrefillArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
+    const int cl = lane & 31, hh = lane >> 5;
+
+    // heads of one row block next to each other: with 8 key heads each XCD
+    // keeps one head's K and V in its L2
+    const int Hkv = a->Hkv, grp = a->grp;
+    const int item = (int)(blockIdx.x / (unsigned)Hkv), hk = (int)(blockIdx.x % (unsigned)Hkv);
+    const int below = __popcll(__ballot(a->tab.pre[lane] <= item)) +
+                      __popcll(__ballot(a->tab.pre[64 + lane] <= item));
+    const int si = uniform_int(below - 1);
+    const int lq = a->tab.seq[si].lq, lk = a->tab.seq[si].lk;
+    const int64_t nrow = (int64_t)lq * grp;
+    const int nblk = (int)((nrow + kRows - 1) / kRows);
+    // the last rows see the most keys: they start first
+    const int blk = nblk - 1 - (item - a->tab.pre[si]);
+    const int64_t row0 = (int64_t)blk * kRows;
+    const T *kp = (const T *)a->k + a->tab.seq[si].k0 * a->k_stride + (int64_t)hk * D;
+    const T *vp = (const T *)a->v + a->tab.seq[si].k0 * a->v_stride + (int64_t)hk * D;
+
+    int64_t orow[QB];         // the lane's output row, in units of D elements
+    bool valid[QB];
+    int lim[QB];              // keys the lane's row sees
+    V qf[QB][TL::kPieces];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        const int64_t r = row0 + (w * QB + b) * 32 + cl;
+        valid[b] = r < nrow;
+        const unsigned rr = (unsigned)(valid[b] ? r : nrow - 1);
+        const unsigned t = rr / (unsigned)grp, h = hk * grp + rr % (unsigned)grp;
+        const int64_t qt = a->tab.seq[si].q0 + t;
+        orow[b] = qt * a->Hq + h;
+        lim[b] = valid[b] ? std::max(0, lk - lq + (int)t + 1) : 0;
+        const T *qp = (const T *)a->q + qt * a->q_stride + (int64_t)h * D;
+#pragma unroll
+        for (int p = 0; p < TL::kPieces; ++p) {
+            qf[b][p] = *reinterpret_cast<const V *>(qp + (2 * p + hh) * E);
+            if (a->neg)
+                qf[b][p] = flip<T>(qf[b][p]);
+        }
+    }
+    // keys that any / every row of the wave sees, and any row of the work-group
+    const int64_t wlast = std::min<int64_t>(nrow, row0 + (w + 1) * 32 * QB) - 1;
+    const int64_t wfirst = row0 + (int64_t)w * 32 * QB;
+    const int wmax = wfirst >= nrow ? 0 : std::max(0, lk - lq + (int)((unsigned)wlast / (unsigned)grp) + 1);
+    const int wmin = std::max(0, lk - lq + (int)((unsigned)wfirst / (unsigned)grp) + 1);
+    const int64_t glast = std::min<int64_t>(nrow, row0 + kRows) - 1;
+    const int gmax = std::max(0, lk - lq + (int)((unsigned)glast / (unsigned)grp) + 1);
+    const int ntile = uniform_int((gmax + KT - 1) / KT);
+    const float c = a->c;
+
+    f32x16 acc[DB][QB] = {};
+    float m[QB], l[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        m[b] = kNoMax;
+        l[b] = 0.f;
+    }
+
+    const unsigned lds0 = lds_addr(smem);
+    auto issue = [&](int n) {
+        const unsigned dst = lds0 + (n & 1) * 2 * kTileBytes;
+        TileLoad<T, D, KT, NW>::issue(dst, kp, a->k_stride, (int64_t)n * KT, lk, w, lane);
+        TileLoad<T, D, KT, NW>::issue(dst + kTileBytes, vp, a->v_stride, (int64_t)n * KT, lk, w, lane);
+    };
+    if (ntile > 0)
+        issue(0);
+
+    for (int n = 0; n < ntile; ++n) {
+        wait_vmcnt<0>();      // this wave's share of tile n has landed
+        lds_barrier();        // everyone's has, and tile n - 1 has been read
+        if (n + 1 < ntile)
+            issue(n + 1);
+        if (n * KT >= wmax)
+            continue;
+        const unsigned char *Kt = smem + (n & 1) * 2 * kTileBytes, *Vt = Kt + kTileBytes;
+
+        f32x16 s[KB][QB] = {};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int p = 0; p < TL::kPieces; ++p) {
+                const V kf = TL::row_nat(Kt, kb * 32 + cl, p, hh);
+#pragma unroll
+                for (int b = 0; b < QB; ++b)
+                    s[kb][b] = mma(kf, qf[b][p], s[kb][b]);
+            }
+        if ((n + 1) * KT > wmin) {
+#pragma unroll
+            for (int b = 0; b < QB; ++b) {
+                const int see = lim[b] - n * KT - 4 * hh;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (32 * kb + 8 * (r >> 2) + (r & 3) >= see)
+                            s[kb][b][r] = -__builtin_inff();
+            }
+        }
+        V pf[KB * PC][QB];
+#pragma unroll
+        for (int b = 0; b < QB; ++b) {
+            float t = s[0][b][0];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    t = fmaxf(t, s[kb][b][r]);
+            t = half_max(t) * c;
+            if (__any(t > m[b] + kSlack)) {
+                const float mn = fmaxf(m[b], t);
+                const float al = exp2_fast(m[b] - mn);
+                m[b] = mn;
+                l[b] *= al;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        acc[d][b][r] *= al;
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float e = exp2_fast(__builtin_fmaf(s[kb][b][r], c, -m[b]));
+                    l[b] += e;
+                    s[kb][b][r] = e;
+                }
+                // the probabilities are rounded to the operand type once, unnormalised
+#pragma unroll
+                for (int p = 0; p < PC; ++p)
+                    pf[kb * PC + p][b] = acc_piece(s[kb][b], p, (const T *)nullptr);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < KB * PC; ++p)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const V vf = TL::col_acc(Vt, p, 32 * d, lane);
+#pragma unroll
+                for (int b = 0; b < QB; ++b)
+                    acc[d][b] = mma(vf, pf[p][b], acc[d][b]);
+            }
+    }
+
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        const float tot = half_sum(l[b]);
+        const float inv = tot > 0.f ? 1.f / tot : 0.f;
+        T *op = (T *)a->o + orow[b] * D;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                acc[d][b][r] *= inv;
+            store_row(op, 32 * d, hh, valid[b], acc[d][b]);
+        }
+    }
+}
+
+template <typename T, int D, int NW, int QB>
+hipError_t prefill(PrefillArgs &args, int64_t nseq, const AttnSeq *seqs, hipStream_t s)
+{
+    constexpr int kRows = 32 * QB * NW;
+    constexpr int KT = sizeof(T) == 2 ? 64 : 32;
+    constexpr unsigned kSmem = 4u * KT * D * sizeof(T);
+    hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void *>(&attn_prefill_kernel<T, D, NW, QB>),
+        hipFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != hipSuccess)
+        return e;
+    // launches of at most SeqTab::kMax sequences and 2^31 - 1 work-groups,
+    // the sequences with the most work per row block first
+    for (int64_t at = 0; at < nseq;) {
+        int n = 0;
+        int64_t items = 0;
+        const int64_t most = INT32_MAX / args.Hkv;
+        while (at < nseq && n < SeqTab::kMax) {
+            const int64_t blocks = (seqs[at].lq * (int64_t)args.grp + kRows - 1) / kRows;
+            if (blocks > most - items)
+                break;
+            if (blocks > 0)
+                args.tab.seq[n++] = seqs[at];
+            items += blocks;
+            ++at;
+        }
+        if (n == 0)
+            break;
+        std::stable_sort(args.tab.seq, args.tab.seq + n,
+                         [](const AttnSeq &x, const AttnSeq &y) { return x.lk > y.lk; });
+        items = 0;
+        for (int i = 0; i < n; ++i) {
+            args.tab.pre[i] = (int32_t)items;
+            items += (args.tab.seq[i].lq * (int64_t)args.grp + kRows - 1) / kRows;
+        }
+        for (int i = n; i < 128; ++i)
+            args.tab.pre[i] = INT32_MAX;
+        attn_prefill_kernel<T, D, NW, QB>
+            <<<dim3((unsigned)(items * args.Hkv)), dim3(64 * NW), kSmem, s>>>(args);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+
+// ---------------------------------------------------------------------------
+// One decode token per sequence
+// ---------------------------------------------------------------------------
+// The new token's k and v go to row `at` = lengths[b] of the cache and rows
+// 0 .. at are attended.  The rows are cut into chunks of a fixed size (so that
+// every work-group does about the same work whatever the lengths are, which
+// the host does not know); a work-group takes one chunk of one key head, its
+// waves every kWaves-th 32-key tile of it, each with its own running (m, l,
+// acc), double-buffered in a part of the LDS that only it touches.  The query
+// heads of the group are the columns of the score block.  Chunks are joined by
+// a second small kernel.
+struct DecodeArgs {
+    const void *q, *k, *v;
+    void *kc, *vc;
+    const int32_t *lengths;
+    void *o;
+    float *part;                              // [item][split][rows][D] accumulators
+    float2 *ml;                               // [item][split][rows] (m, l)
+    int64_t q_stride, k_stride, v_stride;
+    int64_t M;
+    int Hq, Hkv, grp, rtiles;                 // rtiles: 32-row tiles of a group
+    int chunk, nsplit;
+    float c;
+    int neg;
+};
+
+template <typename T, int D> struct DecodeGeom {
+    static constexpr int kPitch = Tile<T, D>::kPitch;
+    static constexpr int kWaves = kPitch <= 256 ? 4 : kPitch == 512 ? 2 : 1;
+    static constexpr int kTileBytes = 32 * kPitch;
+    static constexpr unsigned kWaveSmem = 4u * kTileBytes;          // two slots of K and V
+    static constexpr unsigned kSmem = kWaves * kWaveSmem;
+};
+
+// Rows first .. 31 of a wave's K (or V) tile become the new token's.
+template <typename T, int D>
+__device__ __forceinline__ void put_rows(unsigned char *tile, const T *src, int first, int lane)
+{
+    typedef Tile<T, D> TL;
+    for (int i = lane; i < (32 - first) * TL::kChunks; i += 64) {
+        const int row = first + i / TL::kChunks, ch = i % TL::kChunks;
+        *reinterpret_cast<uint4 *>(tile + TL::off(row, ch)) =
+            *reinterpret_cast<const uint4 *>(src + ch * (16 / (int)sizeof(T)));
+    }
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__((64 * DecodeGeom<T, D>::kWaves), 1) void attn_decode_kernel(DecodeArgs a)
+{
+    typedef DecodeGeom<T, D> GM;
+    typedef Tile<T, D> TL;
+    typedef typename Piece<T>::V V;
+    constexpr int E = Piece<T>::E, NW = GM::kWaves, DB = D / 32, PC = 16 / E;
+    constexpr int kLoads = 2 * TileLoad<T, D, 32, 1>::kPer;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ float sm[NW][32], sl[NW][32];
+
+    const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
+    const int cl = lane & 31, hh = lane >> 5;
+    // (sequence, key head, row tile) fastest: the chunks of long sequences, which
+    // are few in a mixed batch, spread over the launch
+    const int items = gridDim.x / a.nsplit;
+    const int item = blockIdx.x % items, split = blockIdx.x / items;
+    const int rt = item % a.rtiles, hk = (item / a.rtiles) % a.Hkv;
+    const int64_t b = item / (a.rtiles * a.Hkv);
+    const int at = uniform_int(a.lengths[b]);
+    const int rows = std::min(32, a.grp - 32 * rt);       // query heads of this tile
+    const int64_t h0 = (int64_t)hk * a.grp + 32 * rt;
+    T *op = (T *)a.o + (b * a.Hq + h0) * D;
+
+    if (at < 0 || at >= a.M) {                            // inactive slot
+        if (a.nsplit == 1)
+            for (int i = tid; i < rows * D; i += 64 * NW)
+                op[i] = (T)0.f;
+        return;
+    }
+    const int64_t kbeg = (int64_t)split * a.chunk;
+    if (kbeg > at)
+        return;
+    const int kend = (int)std::min<int64_t>(kbeg + a.chunk, (int64_t)at + 1);   // keys [kbeg, kend)
+
+    V qf[TL::kPieces];
+    const T *qp = (const T *)a.q + b * a.q_stride + (h0 + std::min(cl, rows - 1)) * D;
+#pragma unroll
+    for (int p = 0; p < TL::kPieces; ++p) {
+        qf[p] = *reinterpret_cast<const V *>(qp + (2 * p + hh) * E);
+        if (a.neg)
+            qf[p] = flip<T>(qf[p]);
+    }
+    const T *kn = (const T *)a.k + b * a.k_stride + (int64_t)hk * D;
+    const T *vn = (const T *)a.v + b * a.v_stride + (int64_t)hk * D;
+    const int64_t cstride = (int64_t)a.Hkv * D;
+    T *kc = (T *)a.kc + b * a.M * cstride + (int64_t)hk * D;
+    T *vc = (T *)a.vc + b * a.M * cstride + (int64_t)hk * D;
+    if (kend == at + 1 && rt == 0) {                      // the chunk that holds the new row stores it
+        for (int i = tid; i < TL::kChunks; i += 64 * NW) {
+            *reinterpret_cast<uint4 *>((unsigned char *)(kc + at * cstride) + 16 * i) =
+                *reinterpret_cast<const uint4 *>((const unsigned char *)kn + 16 * i);
+            *reinterpret_cast<uint4 *>((unsigned char *)(vc + at * cstride) + 16 * i) =
+                *reinterpret_cast<const uint4 *>((const unsigned char *)vn + 16 * i);
+        }
+    }
+
+    unsigned char *mine = smem + w * GM::kWaveSmem;
+    const unsigned lds0 = lds_addr(mine);
+    // rows of the tile at key t0 that are in the cache already: those before `at`
+    auto issue = [&](int t0, int slot) {
+        if (t0 >= at)
+            return;
+        const unsigned dst = lds0 + slot * 2 * GM::kTileBytes;
+        TileLoad<T, D, 32, 1>::issue(dst, kc, cstride, t0, at, 0, lane);
+        TileLoad<T, D, 32, 1>::issue(dst + GM::kTileBytes, vc, cstride, t0, at, 0, lane);
+    };
+
+    f32x16 acc[DB] = {};
+    float m = kNoMax, l = 0.f;
+    int t0 = (int)kbeg + 32 * w;
+    if (t0 < kend)
+        issue(t0, 0);
+    for (int n = 0; t0 < kend; ++n, t0 += 32 * NW) {
+        const int tn = t0 + 32 * NW;
+        // the slot issued next was read by this wave before: its reads are done
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (tn < kend && tn < at) {
+            issue(tn, (n + 1) & 1);
+            wait_vmcnt<(kLoads < 63 ? kLoads : 63)>();
+        } else {
+            wait_vmcnt<0>();
+        }
+        unsigned char *Kt = mine + (n & 1) * 2 * GM::kTileBytes, *Vt = Kt + GM::kTileBytes;
+        if (t0 + 32 > at) {
+            // the new token, and after it (masked rows) its copies
+            put_rows<T, D>(Kt, kn, at - t0, lane);
+            put_rows<T, D>(Vt, vn, at - t0, lane);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        f32x16 s = {};
+#pragma unroll
+        for (int p = 0; p < TL::kPieces; ++p)
+            s = mma(TL::row_nat(Kt, cl, p, hh), qf[p], s);
+        if (t0 + 32 > kend) {
+            const int see = kend - t0 - 4 * hh;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (8 * (r >> 2) + (r & 3) >= see)
+                    s[r] = -__builtin_inff();
+        }
+        float t = s[0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r)
+            t = fmaxf(t, s[r]);
+        t = half_max(t) * a.c;
+        if (__any(t > m + kSlack)) {
+            const float mn = fmaxf(m, t), al = exp2_fast(m - mn);
+            m = mn;
+            l *= al;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc[d][r] *= al;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            s[r] = exp2_fast(__builtin_fmaf(s[r], a.c, -m));
+            l += s[r];
+        }
+#pragma unroll
+        for (int p = 0; p < PC; ++p) {
+            const V pf = acc_piece(s, p, (const T *)nullptr);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                acc[d] = mma(TL::col_acc(Vt, p, 32 * d, lane), pf, acc[d]);
+        }
+    }
+    l = half_sum(l);
+
+    // join the waves: each scales its sums to the common m and leaves them in
+    // its part of the LDS as [row][D]
+    if (hh == 0) {
+        sm[w][cl] = m;
+        sl[w][cl] = l;
+    }
+    __syncthreads();
+    float mt = sm[0][cl];
+#pragma unroll
+    for (int i = 1; i < NW; ++i)
+        mt = fmaxf(mt, sm[i][cl]);
+    const float f = exp2_fast(m - mt);
+    float *wp = reinterpret_cast<float *>(mine);
+    if (cl < rows)
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4 *>(wp + cl * D + 32 * d + 8 * g + 4 * hh) =
+                    f32x4{acc[d][4 * g] * f, acc[d][4 * g + 1] * f, acc[d][4 * g + 2] * f,
+                          acc[d][4 * g + 3] * f};
+    __syncthreads();
+    const int64_t slot = ((int64_t)item * a.nsplit + split) * 32;
+    for (int i = 4 * tid; i < rows * D; i += 4 * 64 * NW) {
+        const int row = i / D;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(smem + i * 4);
+#pragma unroll
+        for (int j = 1; j < NW; ++j)
+            v += *reinterpret_cast<const f32x4 *>(smem + j * GM::kWaveSmem + i * 4);
+        float mr = sm[0][row];
+#pragma unroll
+        for (int j = 1; j < NW; ++j)
+            mr = fmaxf(mr, sm[j][row]);
+        float lr = 0.f;
+#pragma unroll
+        for (int j = 0; j < NW; ++j)
+            lr += sl[j][row] * exp2_fast(sm[j][row] - mr);
+        if (a.nsplit == 1) {
+            const float inv = 1.f / lr;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                op[i + e] = (T)(v[e] * inv);
+        } else {
+            *reinterpret_cast<f32x4 *>(a.part + slot * D + i) = v;
+            if (i % D == 0)
+                a.ml[slot + row] = make_float2(mr, lr);
+        }
+    }
+}
+
+// Joins the chunks of one query head: o = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a)
+{
+    constexpr int LPR = D / 4, G = 256 / LPR;             // lanes per row, chunk groups
+    __shared__ float4 sacc[G][LPR];
+    __shared__ float sl[G], smax[4];
+    const int tid = threadIdx.x, g = tid / LPR, d4 = tid % LPR;
+    const int64_t b = blockIdx.x / a.Hq;
+    const int h = blockIdx.x % a.Hq;
+    const int at = a.lengths[b];
+    const int ns = at < 0 || at >= a.M ? 0 : at / a.chunk + 1;
+    const int hk = h / a.grp, rt = (h % a.grp) / 32, row = h % a.grp % 32;
+    const int64_t slot = (((b * a.Hkv + hk) * a.rtiles + rt) * a.nsplit) * 32 + row;
+    float mx = kNoMax;
+    for (int i = tid; i < ns; i += 256)
+        mx = fmaxf(mx, a.ml[slot + i * 32].x);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+    if ((tid & 63) == 0)
+        smax[tid >> 6] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int i = g; i < ns; i += G) {
+        const float2 ml = a.ml[slot + i * 32];
+        const float f = exp2_fast(ml.x - mx);
+        const float4 p = *reinterpret_cast<const float4 *>(a.part + (slot + i * 32) * D + 4 * d4);
+        v.x += f * p.x; v.y += f * p.y; v.z += f * p.z; v.w += f * p.w;
+        l += f * ml.y;
+    }
+    sacc[g][d4] = v;
+    if (d4 == 0)
+        sl[g] = l;
+    __syncthreads();
+    if (tid < LPR) {
+        for (int i = 1; i < G; ++i) {
+            const float4 p = sacc[i][d4];
+            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+            l += sl[i];
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        T *op = (T *)a.o + (b * a.Hq + h) * D + 4 * d4;
+        op[0] = (T)(v.x * inv);
+        op[1] = (T)(v.y * inv);
+        op[2] = (T)(v.z * inv);
+        op[3] = (T)(v.w * inv);
+    }
+}
+
+// Keys per work-group: about 2048 work-groups when the cache is full (eight
+// rounds of the chip, so that unequal lengths even out), 128 keys at least.
+int64_t decode_chunk(int64_t B, int64_t M, int64_t Hkv, int64_t rtiles)
+{
+    const int64_t want = (M * B * Hkv * rtiles + 2047) / 2048;
+    return std::max<int64_t>(128, (want + 127) / 128 * 128);
+}
+
+template <typename T, int D> hipError_t decode(const DecodeArgs &a, int64_t B, hipStream_t s)
+{
+    typedef DecodeGeom<T, D> GM;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attn_decode_kernel<T, D>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)GM::kSmem);
+    if (e != hipSuccess)
+        return e;
+    const unsigned grid = (unsigned)(B * a.Hkv * a.rtiles * a.nsplit);
+    attn_decode_kernel<T, D><<<dim3(grid), dim3(64 * GM::kWaves), GM::kSmem, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess || a.nsplit == 1)
+        return e;
+    attn_join_kernel<T, D><<<dim3((unsigned)(B * a.Hq)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_prefill(int bf16, int64_t nseq, const AttnSeq *seqs, int64_t Hq, int64_t Hkv,
+                               int64_t D, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               float scale, const void *q, const void *k, const void *v, void *o,
+                               hipStream_t s)
+{
+    PrefillArgs args = {};
+    args.q = q;
+    args.k = k;
+    args.v = v;
+    args.o = o;
+    args.q_stride = q_stride;
+    args.k_stride = k_stride;
+    args.v_stride = v_stride;
+    args.Hq = (int)Hq;
+    args.Hkv = (int)Hkv;
+    args.grp = (int)(Hq / Hkv);
+    args.c = std::max(std::abs(scale) * kLog2e, kTinyScale);
+    args.neg = scale < 0.f;
+    if (bf16) {
+        switch (D) {
+        case 64: return prefill<__bf16, 64, 8, 1>(args, nseq, seqs, s);
+        case 128: return prefill<__bf16, 128, 8, 1>(args, nseq, seqs, s);
+        case 256: return prefill<__bf16, 256, 4, 1>(args, nseq, seqs, s);
+        }
+    } else {
+        switch (D) {
+        case 64: return prefill<float, 64, 4, 1>(args, nseq, seqs, s);
+        case 128: return prefill<float, 128, 4, 1>(args, nseq, seqs, s);
+        case 256: return prefill<float, 256, 4, 1>(args, nseq, seqs, s);
+        }
+    }
+    return hipErrorInvalidValue;
+}
+
+
+int64_t attn_decode_splits(int64_t B, int64_t M, int64_t Hq, int64_t Hkv)
+{
+    const int64_t rtiles = (Hq / Hkv + 31) / 32;
+    const int64_t chunk = decode_chunk(B, M, Hkv, rtiles);
+    return (M + chunk - 1) / chunk;
+}
+
+size_t attn_decode_workspace(int64_t B, int64_t M, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    if (B == 0 || M == 0)
+        return 0;
+    const int64_t ns = attn_decode_splits(B, M, Hq, Hkv);
+    if (ns <= 1)
+        return 0;
+    const int64_t slots = B * Hkv * ((Hq / Hkv + 31) / 32) * ns * 32;
+    return (size_t)(slots * (D * 4 + 8));
+}
+
+hipError_t launch_attn_decode(int bf16, int64_t B, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                              const void *q, const void *k, const void *v, void *k_cache,
+                              void *v_cache, const int32_t *lengths, void *o, void *ws,
+                              hipStream_t s)
+{
+    DecodeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.lengths = lengths;
+    a.o = o;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.M = M;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.grp = (int)(Hq / Hkv);
+    a.rtiles = (a.grp + 31) / 32;
+    a.chunk = (int)decode_chunk(B, M, Hkv, a.rtiles);
+    a.nsplit = (int)attn_decode_splits(B, M, Hq, Hkv);
+    a.c = std::max(std::abs(scale) * kLog2e, kTinyScale);
+    a.neg = scale < 0.f;
+    a.part = static_cast<float *>(ws);
+    a.ml = reinterpret_cast<float2 *>(a.part + B * Hkv * a.rtiles * (int64_t)a.nsplit * 32 * D);
+    if (bf16) {
+        switch (D) {
+        case 64: return decode<__bf16, 64>(a, B, s);
+        case 128: return decode<__bf16, 128>(a, B, s);
+        case 256: return decode<__bf16, 256>(a, B, s);
+        }
+    } else {
+        switch (D) {
+        case 64: return decode<float, 64>(a, B, s);
+        case 128: return decode<float, 128>(a, B, s);
+        case 256: return decode<float, 256>(a, B, s);
+        }
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace ssd
