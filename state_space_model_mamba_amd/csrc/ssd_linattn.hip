@@ -24,6 +24,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ssd_attn.h"
 #include "ssd_mma.h"
@@ -34,7 +35,9 @@ namespace {
 using namespace mx;
 
 constexpr double kLog2e = 1.4426950408889634;
-constexpr float kEpoch = 24.f;
+constexpr float kEpoch = 60.f;
+constexpr int kEpochTiles = 8;
+constexpr float kForget = 4.f;
 
 struct LinTab {
     static constexpr int kMax = 96;           // sequences per launch (kernel arguments: 4 KB)
@@ -70,30 +73,50 @@ __device__ __forceinline__ float pow_of(double g2, double n)
     return __builtin_ldexpf(exp2_fast((float)(x - r)), (int)r);
 }
 
-template <typename T> struct LinGeom {
-    static constexpr int C = sizeof(T) == 2 ? 64 : 32;    // tokens per tile
-};
-
 template <typename T, int DK, int NW> struct LinSmem {
-    static constexpr int C = LinGeom<T>::C, CT = 32 * NW;
+    static constexpr int C = 32, CT = 32 * NW;   // tokens per tile, value columns
     static constexpr int kK = C * DK * (int)sizeof(T), kV = C * CT * (int)sizeof(T);
     static constexpr int kP = C * C * (int)sizeof(T);
     static constexpr int kScanSlot = 2 * kK + kV, kStateSlot = kK + kV;
-    static constexpr int kScan = 2 * kScanSlot + kP, kState = 2 * kStateSlot;
+    // tiles in LDS: in use, landed, on its way.  Work-groups of two waves do without
+    // the one between, so that three instead of two share a CU (8 x 2048 tokens of 24
+    // heads of 128 x 64 in bf16: 75 us against 94), as does whatever has no room for it.
+    static constexpr int kRing = 3 * (kScanSlot + kP) <= 158 * 1024 && NW == 4 ? 3 : 2;
+    static constexpr int kScan = kRing * (kScanSlot + kP), kState = kRing * kStateSlot;
+    static constexpr int kTables = ((kEpochTiles + 1) * C + kEpochTiles + 1) * 4;
 };
 
-// v * u, rounded to fp32, as the sum of three bf16 numbers.
-__device__ __forceinline__ void weigh(bf16x8 v, const f32x4 &u0, const f32x4 &u1, bf16x8 (&x)[3])
+// The state row (of a 32-row block) that register r of lane half hh holds.
+template <typename T> __device__ __forceinline__ int state_row(int r, int hh)
 {
+    if constexpr (sizeof(T) == 2)
+        return 16 * (r >> 3) + 8 * hh + (r & 7);
+    else
+        return 8 * (r >> 2) + 4 * hh + (r & 3);
+}
+
+// v * u as the sum of kTerms bf16 numbers (three hold an fp32 product whole).
+template <int kTerms>
+__device__ __forceinline__ void weigh(bf16x8 v, const f32x4 &u0, const f32x4 &u1, bf16x8 (&x)[kTerms])
+{
+    const u32x4 vb = __builtin_bit_cast(u32x4, v);
+    u32x4 xb[kTerms];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float p = (float)v[e] * (e < 4 ? u0[e & 3] : u1[e & 3]);
+    for (int j = 0; j < 4; ++j) {
+        float p = __builtin_bit_cast(float, vb[j] << 16) * (j < 2 ? u0[2 * j] : u1[2 * j - 4]);
+        float q = __builtin_bit_cast(float, vb[j] & 0xffff0000u) * (j < 2 ? u0[2 * j + 1] : u1[2 * j - 3]);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            x[i][e] = (__bf16)p;
-            p -= (float)x[i][e];
+        for (int i = 0; i < kTerms; ++i) {
+            xb[i][j] = pack_bf16(p, q);
+            if (i + 1 == kTerms)
+                break;
+            p -= __builtin_bit_cast(float, xb[i][j] << 16);
+            q -= __builtin_bit_cast(float, xb[i][j] & 0xffff0000u);
         }
     }
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i)
+        x[i] = __builtin_bit_cast(bf16x8, xb[i]);
 }
 
 // The work of one segment of one (sequence, value head, column tile): with
@@ -106,19 +129,28 @@ __device__ __forceinline__ void weigh(bf16x8 v, const f32x4 &u0, const f32x4 &u1
 // through LDS.  Outputs are formed transposed (columns x tokens): a lane holds
 // one token, so its power of lambda is one per-lane factor.
 template <typename T, int DK, int NW, bool kScan>
-__global__ __launch_bounds__(64 * NW) void lin_scan_kernel(LinArgs args_in_kernarg)
+__global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void lin_scan_kernel(LinArgs args_in_kernarg)
 {
     typedef LinSmem<T, DK, NW> SM;
-    constexpr int C = SM::C, TB = C / 32, CT = SM::CT, DB = DK / 32;
+    constexpr int C = SM::C, CT = SM::CT, DB = DK / 32;
+    static_assert(C == 32, "a tile is one 32-token block");
     constexpr int E = Piece<T>::E, PB = 16 / E;           // pieces per 32-row block
     constexpr int PT = C / (2 * E);                       // pieces over a tile's tokens
     typedef Tile<T, DK> TK;
     typedef Tile<T, CT> TV;
     typedef Tile<T, C> TP;
+    typedef LaneBase<T, DK> BK;
+    typedef LaneBase<T, CT> BV;
+    typedef LaneBase<T, C> BP;
     typedef typename Piece<T>::V V;
-    constexpr int kStores = kScan ? TB * (sizeof(T) == 2 ? 2 : 4) : 0;   // per wave and tile
+    constexpr int kStores = kScan ? (sizeof(T) == 2 ? 2 : 4) : 0;   // per wave and tile
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(16) float su[NW][C];             // the tokens' update weights
+    // after the ring: update weights of an epoch's tokens, lambda^-(i C + s + 1)
+    // (direct: those of a tile, lambda^(C-1-s); the last C: a ragged tile's), and
+    // lambda^(i C).  (All of it dynamic, so that the ring starts at LDS address 0 and
+    // its offsets are immediates.)
+    float *su = reinterpret_cast<float *>(smem + (kScan ? SM::kScan : SM::kState));
+    float *spow = su + (kEpochTiles + 1) * C;
 
     const LinArgsPtr a = (LinArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
     const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
@@ -190,7 +222,7 @@ __global__ __launch_bounds__(64 * NW) void lin_scan_kernel(LinArgs args_in_kerna
             for (int d = 0; d < DB; ++d)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    R[d][r] = a->init[sbase + (int64_t)(32 * d + 8 * (r >> 2) + 4 * hh + (r & 3)) * dv];
+                    R[d][r] = a->init[sbase + (int64_t)(32 * d + state_row<T>(r, hh)) * dv];
         }
         if (!kScan && a->copy_init)
             to_ws(nseg - 1, 1.f);
@@ -207,8 +239,10 @@ __global__ __launch_bounds__(64 * NW) void lin_scan_kernel(LinArgs args_in_kerna
 
     const unsigned lds0 = lds_addr(smem);
     constexpr int kSlot = kScan ? SM::kScanSlot : SM::kStateSlot;
+    constexpr int kRing = SM::kRing;
+    constexpr bool kAhead = kRing == 3;                   // scores are formed a tile ahead
     auto issue = [&](int t0, int slot) {
-        unsigned dst = lds0 + slot * kSlot;
+        const unsigned dst = lds0 + slot * kSlot;
         TileLoad<T, DK, C, NW>::issue(dst, kp, a->k_stride, t0, end, w, lane);
         TileLoad<T, CT, C, NW>::issue(dst + SM::kK, vp, a->v_stride, t0, end, w, lane);
         if constexpr (kScan)
@@ -216,180 +250,306 @@ __global__ __launch_bounds__(64 * NW) void lin_scan_kernel(LinArgs args_in_kerna
     };
 
     const bool direct = -g2f * (float)C > kEpoch || g2f > 0.f;   // scaled every tile
+    const int epoch = direct ? 0 : std::min(kEpochTiles, (int)(kEpoch / (1e-9f - g2f * (float)C)));
+    // what R is multiplied by when it is rescaled, to more than fp32
+    const double fd = exp2(g2 * (double)(C * (direct ? 1 : epoch)));
+    const float fhi = (float)fd, flo = (float)(fd - (double)fhi);
     const float scale = a->scale;
-    int e = 0;                                            // S = lambda^e R
-    if (beg < end)
-        issue(beg, 0);
-    bool first = true;
-    for (int t0 = beg, n = 0; t0 < end; t0 += C, ++n) {
-        const int rows = std::min(C, end - t0);
-        // this wave's share of the tile has landed (the last tile's stores, issued
-        // after its loads, may still be on their way), then everyone's has
-        if (first)
-            wait_vmcnt<0>();
-        else
-            wait_vmcnt<kStores>();
-        first = false;
-        lds_barrier();
-        if (t0 + C < end)
-            issue(t0 + C, (n + 1) & 1);
-        const unsigned char *Kt = smem + (n & 1) * kSlot, *Vt = Kt + SM::kK, *Qt = Vt + SM::kV;
-        unsigned char *Pt = smem + 2 * SM::kScanSlot;
+    for (int i = tid; i < kEpochTiles * C; i += 64 * NW)
+        su[i] = pow_of(g2, direct ? C - 1 - i : -(i + 1));
+    if (tid <= kEpochTiles)
+        spow[tid] = direct ? 1.f : pow_of(g2, tid * C);
+    const float ft = scale * pow_of(g2, cl + 1);          // scale lambda^(t+1), the lane's token t
+    // the wave's 16 x 16 blocks of a tile's masked scores (transposed: s x t): factors
+    // scale lambda^(t-s), and the scores of the tile in `slot` into its P buffer
+    constexpr int kBlk = 4 / NW;
+    const int c16 = lane & 15, g16 = lane >> 4;
+    float fp[kBlk][4];
+    if constexpr (kScan) {
+#pragma unroll
+        for (int j = 0; j < kBlk; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tb = (w * kBlk + j) >> 1, sb = (w * kBlk + j) & 1;
+                const int d = 16 * (tb - sb) + c16 - 4 * g16 - i;   // t - s
+                fp[j][i] = d < 0 ? 0.f : scale * exp2_fast(g2f * (float)d);
+            }
+    }
+    constexpr int kSp = TK::kChunks / 4;                  // pieces of a 16-row operand
+    const unsigned bsk = BK::row16(c16, g16);             // the lane's offsets of each operand
+    const unsigned bq = BK::row32(cl, hh), bk = BK::template col<true>(lane);
+    const unsigned bv = BV::template col<false>(lane) ^ (sizeof(T) == 2 ? (unsigned)w << 6 : (unsigned)w << 7);
+    const unsigned bp = BP::row32(cl, hh);
+    struct ScoreIn {
+        V k[kSp], q[kSp];
+    };
+    const int tb = (w * kBlk) >> 1;                       // the blocks' tokens t
+    auto score_load_k = [&](int slot, int j, ScoreIn &in) {
+        const unsigned b =
+            opaque(bsk) + (unsigned)(slot * kSlot) + (((unsigned)(w * kBlk + j) & 1) * 16u) * TK::kPitch;
+#pragma unroll
+        for (int i = 0; i < kSp; ++i)
+            in.k[i] = BK::piece16(0, b, i);
+    };
+    auto score_load = [&](int slot, ScoreIn &in) {
+        const unsigned b = opaque(bsk) + (unsigned)(slot * kSlot) + (unsigned)tb * 16u * TK::kPitch;
+#pragma unroll
+        for (int i = 0; i < kSp; ++i)
+            in.q[i] = BK::piece16(SM::kK + SM::kV, b, i);
+        score_load_k(slot, 0, in);
+    };
+    auto score_store = [&](int slot, ScoreIn &in) {
+        unsigned char *Pt = smem + kRing * kSlot + slot * SM::kP;
+#pragma unroll
+        for (int j = 0; j < kBlk; ++j) {
+            const int sb = (w * kBlk + j) & 1;
+            f32x4 p = {};
+#pragma unroll
+            for (int i = 0; i < kSp; ++i)
+                p = mma16(in.k[i], in.q[i], p);
+            if (j + 1 < kBlk)
+                score_load_k(slot, j + 1, in);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)                   // (a masked score may be infinite: no 0 times it)
+                p[i] = fp[j][i] == 0.f ? 0.f : p[i] * fp[j][i];
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<uint2 *>(Pt + TP::off(16 * tb + c16, 2 * sb + (g16 >> 1)) + 8 * (g16 & 1)) =
+                    make_uint2(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]));
+            else
+                *reinterpret_cast<f32x4 *>(Pt + TP::off(16 * tb + c16, 4 * sb + g16)) = p;
+        }
+    };
 
-        if (!direct && e > 0 && -g2f * (float)(e + C) > kEpoch) {
-            const float f = pow_of(g2, e);
+    if (beg < end) {
+        issue(beg, 0);
+        if (kAhead && beg + C < end)
+            issue(beg + C, 1);
+        wait_vmcnt<0>();
+        if constexpr (kScan && kAhead) {
+            lds_barrier();                                // (the tables are written, too)
+            ScoreIn in;
+            score_load(0, in);
+            score_store(0, in);
+        }
+    }
+    T *const out = (T *)a->o;
+    int n = 0, ep = 0, e = 0;                             // tiles done; S = lambda^e R, ep = e / C
+    int64_t orow = ((a->tab.tok[si] + beg) * Hv + head) * (int64_t)dv + col0;
+    const unsigned ostride = (unsigned)(Hv * dv * (int)sizeof(T));
+    const unsigned olane = (unsigned)cl * ostride + (sizeof(T) == 2 ? 16u : 16u) * (unsigned)hh;
+
+    // one tile; mode 0: the head is scaled every tile, else the bf16 terms of the
+    // update's weighted values
+    int slot = 0;
+    auto tile = [&](auto mode) {
+        constexpr int kMode = decltype(mode)::value;
+        constexpr bool kDirect = kMode == 0;
+        constexpr int kTerms = kDirect ? 3 : kMode;
+        const int next = slot == kRing - 1 ? 0 : slot + 1, last = slot == 0 ? kRing - 1 : slot - 1;
+        const int t0 = beg + n * C, rows = std::min(C, end - t0);
+        // the next tile's loads of this wave have landed (this tile's were waited for
+        // before; the last tile's stores, issued after them, may still be on their
+        // way), then everyone's have, the last tile has been read and this one's
+        // scores are there
+        if (n > 0)
+            wait_vmcnt<kStores>();
+        lds_barrier();
+        if (t0 + (kRing - 1) * C < end)
+            issue(t0 + (kRing - 1) * C, last);
+        const unsigned ring = (unsigned)(slot * kSlot), pring = (unsigned)(slot * SM::kP);
+        if (!kDirect && ep == epoch) {
+            if (epoch == kEpochTiles) {
+                // a slowly forgetting head: the factor to more than fp32, since its
+                // rounding would be repeated over many epochs
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+                for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    R[d][r] *= f;
+                    for (int r = 0; r < 16; ++r)
+                        R[d][r] = __builtin_fmaf(R[d][r], fhi, R[d][r] * flo);
+            } else {
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        R[d][r] *= fhi;
+            }
+            ep = 0;
             e = 0;
         }
-        // update weights of the tile's tokens (lane = token), 0 past the end
-        if (lane < C)
-            su[w][lane] = lane < rows ? (direct ? pow_of(g2, rows - 1 - lane) : pow_of(g2, -(e + lane + 1)))
-                                      : 0.f;
-
-        V vf[PT];
-        if constexpr (kScan) {
-            // masked scores (transposed: s x t): one 32 x 32 block per wave
-            constexpr int kBlocks = TB * (TB + 1) / 2;
-            for (int blk = w; blk < kBlocks; blk += NW) {
-                const int tb = blk == 0 ? 0 : 1, sb = blk == 2 ? 1 : 0;
-                f32x16 p = {};
-#pragma unroll
-                for (int i = 0; i < TK::kPieces; ++i)
-                    p = mma(TK::row_nat(Kt, 32 * sb + cl, i, hh), TK::row_nat(Qt, 32 * tb + cl, i, hh), p);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int d = 32 * (tb - sb) + cl - (8 * (r >> 2) + 4 * hh + (r & 3));   // t - s
-                    p[r] = d < 0 ? 0.f : p[r] * (scale * exp2_fast(g2f * (float)d));
-                }
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    unsigned char *dst = Pt + TP::off(32 * tb + cl, (32 * sb + 8 * g) * (int)sizeof(T) / 16);
-                    if constexpr (sizeof(T) == 2)
-                        *reinterpret_cast<uint2 *>(dst + 8 * hh) =
-                            make_uint2(pack_bf16(p[4 * g], p[4 * g + 1]), pack_bf16(p[4 * g + 2], p[4 * g + 3]));
-                    else
-                        *reinterpret_cast<f32x4 *>(
-                            Pt + TP::off(32 * tb + cl, (32 * sb + 8 * g + 4 * hh) / 4)) =
-                            f32x4{p[4 * g], p[4 * g + 1], p[4 * g + 2], p[4 * g + 3]};
-                }
-            }
-            // the state's part
-            f32x16 y[TB] = {};
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int i = 0; i < PB; ++i) {
-                    const V rf = acc_piece(R[d], i, (const T *)nullptr);
-#pragma unroll
-                    for (int tb = 0; tb < TB; ++tb)
-                        y[tb] = mma(rf, TK::row_acc(Qt, 32 * tb + cl, d * PB + i, hh), y[tb]);
-                }
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb) {
-                const float f = scale * pow_of(g2, (direct ? 0 : e) + 32 * tb + cl + 1);
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    y[tb][r] *= f;
-            }
-#pragma unroll
-            for (int i = 0; i < PT; ++i)
-                vf[i] = TV::col_acc(Vt, i, 32 * w, lane);
-            lds_barrier();                                // the scores are there
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                for (int i = 0; i < (tb + 1) * PB; ++i)
-                    y[tb] = mma(vf[i], TP::row_acc(Pt, 32 * tb + cl, i, hh), y[tb]);
-            // stores through a descriptor that ends at the segment's last row: always the
-            // same number of store instructions (see the wait above)
-            T *ob = (T *)a->o + ((a->tab.tok[si] + t0) * Hv + head) * (int64_t)dv + col0;
-            const unsigned ostride = (unsigned)(Hv * dv * (int)sizeof(T));
-            const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
-                ob, (short)0, (int)((unsigned)(rows - 1) * ostride + 32 * (unsigned)sizeof(T)), 0x00020000);
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb) {
-                // a row past the last lies past the descriptor's end whatever the column
-                const unsigned ro = (unsigned)(32 * tb + cl) * ostride;
-                if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                    for (int g = 0; g < 4; g += 2) {
-                        unsigned out[4];
-#pragma unroll
-                        for (int h2 = 0; h2 < 2; ++h2) {
-                            const auto sw = __builtin_amdgcn_permlane32_swap(
-                                pack_bf16(y[tb][4 * g + 2 * h2], y[tb][4 * g + 2 * h2 + 1]),
-                                pack_bf16(y[tb][4 * g + 4 + 2 * h2], y[tb][4 * g + 5 + 2 * h2]), false, false);
-                            out[h2] = sw[0];
-                            out[2 + h2] = sw[1];
-                        }
-                        __builtin_amdgcn_raw_buffer_store_b128(u32x4{out[0], out[1], out[2], out[3]}, orr,
-                                                               ro + (unsigned)(8 * g + 8 * hh) * 2u, 0, 0);
-                    }
-                } else {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        __builtin_amdgcn_raw_buffer_store_b128(
-                            __builtin_bit_cast(u32x4, f32x4{y[tb][4 * g], y[tb][4 * g + 1], y[tb][4 * g + 2],
-                                                            y[tb][4 * g + 3]}),
-                            orr, ro + (unsigned)(8 * g + 4 * hh) * 4u, 0, 0);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < PT; ++i)
-                vf[i] = TV::col_acc(Vt, i, 32 * w, lane);
+        int ub = ep * C;
+        if (rows < C) {   // the tokens past the end weigh 0 (every wave writes the same)
+            ub = kEpochTiles * C;
+            if (lane < C)
+                su[ub + lane] = lane < rows ? su[ep * C + lane + (kDirect ? C - rows : 0)] : 0.f;
+            lds_barrier();
         }
 
-        // the state update
-        if (direct) {
-            const float f = pow_of(g2, rows);
+        // The LDS reads of a step are issued together ahead of the products (one at a
+        // time before its product, as the compiler would have them, each costs its
+        // latency); for fp32 and 256 keys there are not the registers for it.
+        constexpr bool kBatch = sizeof(T) == 2 && DK <= 128 && NW == 4;
+        auto step = [] {
+            if constexpr (kBatch)
+                __builtin_amdgcn_sched_barrier(0);
+        };
+        V vf[PT], kf[DB];
+        f32x4 uw[E / 4];
+        V pf[PT];
+        f32x16 y = {};
+        float f = 0.f;
+        const unsigned bvo = opaque(bv) + ring;
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+            vf[i] = BV::col_piece(SM::kK, bvo, i, 0);
+        auto load_k = [&](int i) {
+            const unsigned b = opaque(bk) + ring;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                kf[d] = BK::col_piece(0, b, i, d);
+        };
+        auto load_u = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < E / 4; ++j)
+                uw[j] = *reinterpret_cast<const f32x4 *>(su + ub + 2 * E * i + E * hh + 4 * j);
+        };
+        if constexpr (kScan) {
+            // the (next) tile's scores (past the last tile: of whatever is there, not
+            // used) and the state's part
+            ScoreIn in;
+            score_load(kAhead ? next : slot, in);
+            constexpr bool kHold = DK <= 128;
+            V qf[kHold ? TK::kPieces : 1];
+            const unsigned bqo = opaque(bq) + ring;
+            if constexpr (kHold)
+#pragma unroll
+                for (int i = 0; i < TK::kPieces; ++i)
+                    qf[i] = BK::piece32(SM::kK + SM::kV, bqo, i);
+            f = ft * spow[ep];
+            step();
+            score_store(kAhead ? next : slot, in);
+            load_u(0);
+            load_k(0);
+            if constexpr (!kAhead)
+                lds_barrier();
+#pragma unroll
+            for (int i = 0; i < PT; ++i)
+                pf[i] = BP::piece32(kRing * kSlot, opaque(bp) + pring, i);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+                    y = mma(acc_piece(R[d], i, (const T *)nullptr),
+                            kHold ? qf[kHold ? d * PB + i : 0] : BK::piece32(SM::kK + SM::kV, bqo, d * PB + i), y);
+            step();
+        } else {
+            load_u(0);
+            load_k(0);
+        }
+
+        // the state update (issued ahead of the other wave of the SIMD)
+        __builtin_amdgcn_s_setprio(1);
+        if constexpr (kDirect) {
+            const float fd = rows < C ? su[C - 1 - rows] : fhi;   // lambda^rows
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    R[d][r] *= f;
-        } else {
-            e += rows;
+                    R[d][r] *= fd;
         }
 #pragma unroll
         for (int i = 0; i < PT; ++i) {
             if constexpr (sizeof(T) == 2) {
-                const f32x4 u0 = *reinterpret_cast<const f32x4 *>(&su[w][16 * i + 4 * hh]);
-                const f32x4 u1 = *reinterpret_cast<const f32x4 *>(&su[w][16 * i + 8 + 4 * hh]);
-                V x[3];
-                weigh(vf[i], u0, u1, x);
+                V x[kTerms];
+                weigh(vf[i], uw[0], uw[1], x);
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const V kf = TK::col_acc(Kt, i, 32 * d, lane);
+                for (int j = 0; j < kTerms; ++j)
 #pragma unroll
-                    for (int j = 0; j < 3; ++j)
-                        R[d] = mma(kf, x[j], R[d]);
-                }
+                    for (int d = 0; d < DB; ++d)
+                        R[d] = mma(kf[d], x[j], R[d]);
             } else {
-                const f32x4 u = *reinterpret_cast<const f32x4 *>(&su[w][8 * i + 4 * hh]);
-                const V x = vf[i] * u;
+                const V x = vf[i] * uw[0];
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
-                    R[d] = mma(TK::col_acc(Kt, i, 32 * d, lane), x, R[d]);
+                    R[d] = mma(kf[d], x, R[d]);
+            }
+            if (i + 1 < PT) {
+                load_u(i + 1);
+                load_k(i + 1);
             }
         }
+
+        if constexpr (kScan) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                y[r] *= f;
+#pragma unroll
+            for (int i = 0; i < PT; ++i)
+                y = mma(vf[i], pf[i], y);
+            // stores through a descriptor that ends at the segment's last row: always the
+            // same number of store instructions (see the wait above); a row past the last
+            // lies past the descriptor's end whatever the column
+            const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
+                out + orow, (short)0, (int)((unsigned)(rows - 1) * ostride + 32 * (unsigned)sizeof(T)),
+                0x00020000);
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int g = 0; g < 4; g += 2) {
+                    unsigned out[4];
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        const auto sw = __builtin_amdgcn_permlane32_swap(
+                            pack_bf16(y[4 * g + 2 * h2], y[4 * g + 2 * h2 + 1]),
+                            pack_bf16(y[4 * g + 4 + 2 * h2], y[4 * g + 5 + 2 * h2]), false, false);
+                        out[h2] = sw[0];
+                        out[2 + h2] = sw[1];
+                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{out[0], out[1], out[2], out[3]}, orr,
+                                                           olane + 16u * (unsigned)g, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        __builtin_bit_cast(u32x4, f32x4{y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]}),
+                        orr, olane + 32u * (unsigned)g, 0, 0);
+            }
+            orow += (int64_t)C * Hv * dv;
+        }
+        __builtin_amdgcn_s_setprio(0);
+        if constexpr (!kDirect) {
+            ++ep;
+            e += rows;
+        }
+        slot = next;
+        ++n;
+    };
+    const int ntile = (end - beg + C - 1) / C;
+    auto tiles = [&](auto mode, int upto) {
+        while (n < upto)
+            tile(mode);
+    };
+    if (direct) {
+        tiles(std::integral_constant<int, 0>(), ntile);
+    } else {
+        // tokens that the end of the segment's state has forgotten below 2^-kForget
+        // take two terms
+        const int keep = kScan && seg < nseg - 1 ? 0 : (int)std::min(1e6f, kForget / (1e-9f - g2f * (float)C)) + 1;
+        if constexpr (sizeof(T) == 2)
+            tiles(std::integral_constant<int, 2>(), ntile - keep);
+        tiles(std::integral_constant<int, 3>(), ntile);
     }
+    const float fe = pow_of(g2, e);
 
     if constexpr (kScan) {
         if (seg == nseg - 1) {
-            const float f = pow_of(g2, e);
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    a->fin[sbase + (int64_t)(32 * d + 8 * (r >> 2) + 4 * hh + (r & 3)) * dv] = R[d][r] * f;
+                    a->fin[sbase + (int64_t)(32 * d + state_row<T>(r, hh)) * dv] = R[d][r] * fe;
         }
     } else {
-        to_ws(seg, pow_of(g2, e));
+        to_ws(seg, fe);
     }
 }
 
@@ -397,8 +557,8 @@ template <typename T, int DK, int NW, bool kScan>
 hipError_t launch_part(const LinArgs &args, int64_t items, hipStream_t s)
 {
     typedef LinSmem<T, DK, NW> SM;
-    constexpr int kSmem = kScan ? SM::kScan : SM::kState;
-    static_assert(kSmem + NW * SM::C * 4 <= 160 * 1024, "LDS of a CU");
+    constexpr int kSmem = (kScan ? SM::kScan : SM::kState) + SM::kTables;
+    static_assert(kSmem <= 160 * 1024, "LDS of a CU");
     const hipError_t e = hipFuncSetAttribute(
         reinterpret_cast<const void *>(&lin_scan_kernel<T, DK, NW, kScan>),
         hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -577,29 +737,72 @@ hipError_t step(int64_t B, int64_t Hk, int64_t Hv, int64_t dv, int64_t qs, int64
 
 }  // namespace
 
+// Segment length and column tile by a model of the two launches.  A work-group's
+// 32-token tile takes at least `chain` us (its own dependent steps), and with the
+// chip's slots full at least slots x `rate` us (memory: the bytes of a tile at
+// 4.8 TB/s, q and k once per head group; or the matrix and vector work).  A launch
+// runs in rounds of `slots` work-groups; a chained state costs its reader about
+// 2.5 us.  Measured at 4 x 8192 tokens (32 heads of 128 x 128, bf16, 512 slots): 262
+// us with 4 segments per sequence (one round of the scan) against 295 with 8 and
+// 326 with 2; at 8 x 2048 (24 heads of 128 x 64, 768 slots): 75 us with 4 against
+// 97 with 2, 92 with 8, 102 unsplit.
 LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int64_t Hv, int64_t dk,
                      int64_t dv)
 {
-    LinPlan p = {};
-    p.cols = dv % 128 == 0 && dk <= 128 ? 128 : 64;
-    const int64_t heads = Hv * (dv / p.cols);
-    int64_t total = 0, longest = 0;
-    for (int64_t i = 0; i < nseq; ++i) {
-        total += seqs[i].len;
+    int64_t longest = 0;
+    for (int64_t i = 0; i < nseq; ++i)
         longest = std::max(longest, seqs[i].len);
+    LinPlan best = {};
+    double best_us = 1e300;
+    const int64_t esz = bf16 ? 2 : 4;
+    const int64_t kmax = std::max<int64_t>(1, std::min<int64_t>(nseq > 256 ? 16 : 64, (longest + 95) / 96));
+    for (int cols = dv % 128 == 0 && dk <= 128 ? 128 : 64; cols >= 64; cols /= 2) {
+        const int64_t heads = Hv * (dv / cols);
+        // work-groups of a CU: by LDS, and by registers (8 waves; 4 of the large heads
+        // and of fp32)
+        const int64_t nw = cols / 32, slot_b = 32 * esz * (2 * dk + cols), p_b = 32 * 32 * esz;
+        const int64_t ring = nw == 4 && 3 * (slot_b + p_b) <= 158 * 1024 ? 3 : 2;
+        const int64_t per_cu = std::max<int64_t>(
+            1, std::min((bf16 && dk <= 128 ? 8 : 4) / nw, 160 * 1024 / (ring * (slot_b + p_b) + 1280)));
+        const double slots = 256.0 * per_cu, w = dk / 128.0, waves = (double)nw;
+        const double chain = !bf16 ? 1.8 + 4.6 * w : dk <= 128 ? 0.6 + 0.9 * w : 5.8;
+        const double chain_state = !bf16 ? 0.7 + 2.4 * w : dk <= 128 ? 0.4 + 0.6 * w : 3.5;
+        const double shared = (double)dk * Hk / Hv;       // q (or k) columns a work-group pays for
+        const double us_byte = 1.0 / 4.8e6;
+        const double rate = std::max(32 * esz * (2 * shared + 2 * cols) * us_byte,
+                                     (bf16 ? 0.9e-3 : 4e-3) * waves * w);
+        const double rate_state = std::max(32 * esz * (shared + cols) * us_byte,
+                                           (bf16 ? 0.7e-3 : 2e-3) * waves * w);
+        for (int64_t k = 1; k <= kmax; ++k) {
+            const int64_t T0 = std::max<int64_t>(32, ((longest + k - 1) / k + 31) / 32 * 32);
+            int64_t segs = 0, slot = 0;
+            for (int64_t i = 0; i < nseq; ++i) {
+                const int64_t ns = std::max<int64_t>(1, (seqs[i].len + T0 - 1) / T0);
+                segs += ns;
+                slot += ns > 1 ? ns : 0;
+            }
+            // rounds of a launch of n work-groups of at most T0 tokens (a partly filled
+            // one gains about half of what it leaves free)
+            auto launch = [&](double n, double ch, double rt) {
+                const double tiles = T0 / 32.0, full = (double)(int64_t)(n / slots);
+                const double rest = n - full * slots;
+                return tiles * (full * std::max(ch, slots * rt) +
+                                (rest > 0 ? std::max(ch, 0.5 * (slots + rest) * rt) : 0.0));
+            };
+            double us = launch((double)(segs * heads), chain, rate);
+            if (segs > nseq)
+                us += 4.0 + launch((double)((segs - nseq) * heads), chain_state, rate_state) +
+                      2.5 * (double)((longest + T0 - 1) / T0 - 1);
+            if (us < best_us) {
+                best_us = us;
+                best.seg_tokens = T0;
+                best.nslot = slot;
+                best.cols = cols;
+            }
+        }
     }
-    const int64_t tile = bf16 ? 64 : 32;
-    // work-groups wanted: one per CU
-    int64_t T0 = total * heads / 256;
-    T0 = std::max<int64_t>(4 * tile, (T0 + tile - 1) / tile * tile);
-    T0 = std::min(T0, (std::max<int64_t>(longest, 1) + tile - 1) / tile * tile);
-    p.seg_tokens = T0;
-    for (int64_t i = 0; i < nseq; ++i) {
-        const int64_t ns = (seqs[i].len + T0 - 1) / T0;
-        p.nslot += ns > 1 ? ns : 0;
-    }
-    p.ws_bytes = (size_t)(p.nslot * Hv * dk * dv * 4);
-    return p;
+    best.ws_bytes = (size_t)(best.nslot * Hv * dk * dv * 4);
+    return best;
 }
 
 hipError_t launch_linattn_scan(int bf16, const LinPlan &plan, int64_t nseq, const LinSeq *seqs,

@@ -53,6 +53,20 @@ __device__ __forceinline__ f32x16 mma(f32x4 a, f32x4 b, f32x16 c)
     return c;
 }
 
+// 16 x 16 blocks: lane l = c + 16 g holds row c of A (column c of B), natural
+// order over the four lane groups, and D[4 g + i][c] in register i.
+__device__ __forceinline__ f32x4 mma16(bf16x8 a, bf16x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma16(f32x4 a, f32x4 b, f32x4 c)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+
 // Piece p of a 32-row result block as an operand (accumulator order), rounded
 // once to the operand type.
 __device__ __forceinline__ bf16x8 acc_piece(const f32x16 &d, int p, const __bf16 *)
@@ -76,14 +90,16 @@ template <typename T, int D> struct Tile {
     static constexpr int kPitch = D * (int)sizeof(T);
     static constexpr int kChunks = kPitch / 16;
     static constexpr int kPieces = kPitch / 32;      // pieces of a row as an operand
-    static_assert(kChunks >= 8, "a row is half the banks or more");
+    static_assert(kChunks >= 4, "a row is a quarter of the banks or more");
 
     static __device__ __forceinline__ int swz(int row)
     {
         if constexpr (kChunks >= 16)
             return ((row & 3) << 2) | ((row >> 2) & 3);
-        else   // two rows per 256 bytes: row bit 0 is the upper half already
+        else if constexpr (kChunks == 8)   // two rows per 256 bytes: row bit 0 is the upper half already
             return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+        else
+            return (row >> 2) & 3;
     }
     static __device__ __forceinline__ int off(int row, int chunk)
     {
@@ -133,6 +149,99 @@ template <typename T, int D> struct Tile {
         }
     }
 };
+
+// A lane's byte offset into a tile, from which an operand's pieces follow by an
+// XOR with a constant (the chunk permutation is an XOR itself) and a constant
+// row offset: one register per operand instead of one per read.  opaque() keeps
+// the XORs where they are used.
+__device__ __forceinline__ unsigned opaque(unsigned v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+template <typename T, int D> struct LaneBase {
+    typedef Tile<T, D> TL;
+    typedef typename Piece<T>::V V;
+    // (t: the tile's LDS address, a constant, which ends up in the instruction)
+    static __device__ __forceinline__ V at(unsigned t, unsigned off)
+    {
+        return *(const __attribute__((address_space(3))) V *)(uintptr_t)(t + off);
+    }
+    // 32-row operand over the columns, natural order: piece p of row `row`
+    static __device__ __forceinline__ unsigned row32(int row, int hh)
+    {
+        return (unsigned)TL::off(row, hh);
+    }
+    static __device__ __forceinline__ V piece32(unsigned t, unsigned base, int p)
+    {
+        return at(t, base ^ ((unsigned)p << 5));
+    }
+    // 16-row operand
+    static __device__ __forceinline__ unsigned row16(int row, int g)
+    {
+        return (unsigned)TL::off(row, g);
+    }
+    static __device__ __forceinline__ V piece16(unsigned t, unsigned base, int p)
+    {
+        return at(t, base ^ ((unsigned)p << 6));
+    }
+    // transposed operand (see col_nat): block d of 32 columns, piece p of the rows
+    template <bool kPerm> static __device__ __forceinline__ unsigned col(int lane)
+    {
+        if constexpr (sizeof(T) == 4) {
+            const int c = lane & 31;
+            return (unsigned)(TL::off(4 * (lane >> 5), c >> 2) + (c & 3) * 4);
+        } else {
+            const int q = lane & 3, g4 = kPerm ? ((q & 1) << 1) | (q >> 1) : q;
+            const int c = 16 * ((lane >> 4) & 1) + 4 * g4;
+            return (unsigned)(TL::off(8 * (lane >> 5) + ((lane >> 2) & 3), c >> 3) + (c & 7) * 2);
+        }
+    }
+    static __device__ __forceinline__ V col_piece(unsigned t, unsigned base, int p, int d)
+    {
+        if constexpr (sizeof(T) == 4) {
+            // rows 8 p + 4 hh + e: e changes the permutation's upper two bits, 8 p its lower
+            V v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 8 * p + e;
+                v[e] = *(const __attribute__((address_space(3))) float *)(uintptr_t)(
+                    (base ^ (unsigned)((d << 7) ^ (TL::swz(r) << 4))) + (t + (unsigned)(r * TL::kPitch)));
+            }
+            return v;
+        } else {
+            const unsigned a = base ^ ((unsigned)d << 6);
+            const unsigned x = a + (t + 16u * p * TL::kPitch), y = (a ^ 16u) + (t + (16u * p + 4) * TL::kPitch);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)x);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)y);
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+};
+
+// Transposed operands in the natural order, for bf16: rows 16 p + 8 hh + e of
+// column col0 + lane % 32, or with kPerm of the column that makes a result's
+// register 8 j + i of lane half hh stand for column 16 j + 8 hh + i (so that the
+// result, as an operand, meets a natural-order operand: in each 16 columns the
+// middle two groups of four trade places).  fp32: the accumulator order is the
+// natural one, and the register r stands for column 8 (r / 4) + 4 hh + r % 4.
+template <typename T, int D, bool kPerm>
+__device__ __forceinline__ typename Piece<T>::V col_nat(const unsigned char *t, int p, int col0, int lane)
+{
+    typedef Tile<T, D> TL;
+    if constexpr (sizeof(T) == 4) {
+        return TL::col_acc(t, p, col0, lane);
+    } else {
+        const int row = 16 * p + 8 * (lane >> 5) + ((lane >> 2) & 3);
+        const int q = lane & 3, g4 = kPerm ? ((q & 1) << 1) | (q >> 1) : q;
+        const int col = col0 + 16 * ((lane >> 4) & 1) + 4 * g4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(t + TL::off(row, col >> 3) + (col & 7) * 2));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(t + TL::off(row + 4, col >> 3) + (col & 7) * 2));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+}
 
 __device__ __forceinline__ float exp2_fast(float v)
 {
@@ -224,10 +333,10 @@ __device__ __forceinline__ u32x4 buffer_words(const void *base, unsigned bytes)
 // assembly because the compiler waits for every such load before any LDS read;
 // the reader waits with wait_vmcnt and a barrier instead.  (One wait state
 // between writing m0 and the load that reads it.)
-__device__ __forceinline__ void lds_load16(unsigned dst, u32x4 rsrc, unsigned voff)
+__device__ __forceinline__ void lds_load16(unsigned dst, u32x4 rsrc, unsigned voff, unsigned soff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(dst), "v"(voff), "s"(rsrc) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(uniform_int((int)dst)), "v"(voff), "s"(rsrc), "s"(uniform_int((int)soff)) : "memory", "m0");
 }
 
 template <int n> __device__ __forceinline__ void wait_vmcnt()
@@ -263,9 +372,24 @@ template <typename T, int D, int kRows, int kWaves> struct TileLoad {
     static __device__ __forceinline__ void issue(unsigned dst, const T *base, int64_t stride,
                                                  int64_t row0, int64_t nrows, int w, int lane)
     {
-        const int rows = (int)(nrows - row0 < kRows ? nrows - row0 : kRows);   // >= 1
-        const unsigned sb = (unsigned)stride * (unsigned)sizeof(T);
+        const int rows = uniform_int((int)(nrows - row0 < kRows ? nrows - row0 : kRows));   // >= 1
+        const unsigned sb = (unsigned)uniform_int((int)((unsigned)stride * (unsigned)sizeof(T)));
         const u32x4 rs = buffer_words(base + row0 * stride, (unsigned)(rows - 1) * sb + TL::kPitch);
+        constexpr int kBlkRows = TL::kPitch >= 1024 ? 1 : 1024 / TL::kPitch;   // rows of a 1 KB block
+        if (TL::kPitch <= 1024 && rows == kRows) {
+            // whole: block b's rows are kBlkRows b further on, a scalar offset, and only
+            // the chunk permutation differs
+            const int row = 16 * lane / TL::kPitch, chunk = 16 * lane % TL::kPitch / 16;
+            const unsigned lo = (unsigned)row * sb;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int b = w * kPer + i;
+                lds_load16(dst + 1024u * (unsigned)b, rs,
+                           lo + (unsigned)((chunk ^ TL::swz(row + b * kBlkRows)) << 4),
+                           (unsigned)(b * kBlkRows) * sb);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int b = w * kPer + i;
@@ -273,7 +397,7 @@ template <typename T, int D, int kRows, int kWaves> struct TileLoad {
             const int chunk = ((b * 1024 + 16 * lane) % TL::kPitch) / 16;
             const int src = row < rows ? row : rows - 1;
             lds_load16(dst + 1024u * (unsigned)b, rs,
-                       (unsigned)src * sb + (unsigned)((chunk ^ TL::swz(row)) << 4));
+                       (unsigned)src * sb + (unsigned)((chunk ^ TL::swz(row)) << 4), 0);
         }
     }
 };
