@@ -512,16 +512,19 @@ def _row_stride(name, t, di, dtype, shape):
     """Checks a [tokens.., heads, dim] argument whose tokens may lie further apart
     than its heads need (a slice of one projection), and returns the distance
     between tokens in elements."""
+    width = shape[-1] * shape[-2]
     try:
         ok = t.get_device() == di and t.dtype == dtype and t.shape == shape
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
-    if not ok:
-        _need(name, t, di, dtype)
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    width = shape[-1] * shape[-2]
-    if t.is_contiguous():
+    if ok and t.is_contiguous():
         return width
+    if not ok:
+        if t.get_device() != di:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{di}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     st = t.stride()
     if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -539,33 +542,38 @@ def _row_stride(name, t, di, dtype, shape):
     return row
 
 
-def _linattn_dims(q, k, v, lead, dims_of):
-    """(dims, device, state heads/dims) of a linear-attention call whose tokens have
-    `lead` leading dimensions."""
-    dev = _device_of(q)
+def _empty_rows(t):
+    """An uninitialised contiguous tensor like `t` (which may be a strided slice)."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(
+        t, memory_format=torch.contiguous_format)
+
+
+def _linattn_dims(q, k, v, lead, batch, seqlen, scale, dev):
+    """dims of a linear-attention call whose tokens have `lead` leading dimensions."""
     if q.dim() != lead + 2 or v.dim() != lead + 2:
-        want = {1: ("[T, Hk, dk]", "[T, Hv, dv]"), 2: ("[B, L, Hk, dk]", "[B, L, Hv, dv]")}[lead]
+        want = (("[T, Hk, dk]", "[T, Hv, dv]"), ("[B, L, Hk, dk]", "[B, L, Hv, dv]"))[lead - 1]
         raise ValueError(f"q, k must be {want[0]} and v {want[1]}")
-    shp = q.shape
-    Hk, dk = shp[-2:]
-    Hv, dv = v.shape[-2:]
-    qs = _row_stride("q", q, dev, q.dtype, shp)
-    ks = _row_stride("k", k, dev, q.dtype, shp)
-    vs = _row_stride("v", v, dev, q.dtype, shp[:lead] + (Hv, dv))
-    batch, seqlen, scale = dims_of
-    return SsdLinattnDims(batch, seqlen, Hk, Hv, dk, dv, qs, ks, vs, scale, _io_dtype(q)), dev
+    shp, vshp, dtype = q.shape, v.shape, q.dtype
+    if vshp[:lead] != shp[:lead]:
+        raise ValueError(f"v has shape {tuple(vshp)}, which does not go with q {tuple(shp)}")
+    return SsdLinattnDims(batch, seqlen, shp[-2], vshp[-2], shp[-1], vshp[-1],
+                          _row_stride("q", q, dev, dtype, shp),
+                          _row_stride("k", k, dev, dtype, shp),
+                          _row_stride("v", v, dev, dtype, vshp), scale, _io_dtype(q))
 
 
 def _linattn_scan(fn, lead, q, k, v, log_decay, cu_seqlens, initial_state, o, final_state, workspace,
                   scale, stream):
     lib = load()
-    cu = cup = None
+    dev = _device_of(q)
     if lead == 1:
         cu, cup = _cu_array(cu_seqlens)
         if len(cu) < 1:
             raise ValueError("cu_seqlens must hold at least one offset")
-    nseq = len(cu) - 1 if lead == 1 else q.shape[0]
-    d, dev = _linattn_dims(q, k, v, lead, (nseq, q.shape[lead - 1], scale))
+        nseq = len(cu) - 1
+    else:
+        nseq = q.shape[0]
+    d = _linattn_dims(q, k, v, lead, nseq, q.shape[lead - 1], scale, dev)
     f32 = torch.float32
     state = (nseq, d.v_heads, d.dk, d.dv)
     _need("log_decay", log_decay, dev, f32, (d.v_heads,))
@@ -573,22 +581,26 @@ def _linattn_scan(fn, lead, q, k, v, log_decay, cu_seqlens, initial_state, o, fi
     _need("o", o, dev, q.dtype, v.shape, optional=True)
     _need("final_state", final_state, dev, f32, state, optional=True)
     _need("workspace", workspace, dev, optional=True)
-    args = [ctypes.byref(d)] + ([cup] if lead == 1 else [])
-    n = ctypes.c_size_t(0)
-    _check(fn + "_workspace_size", getattr(lib, fn + "_workspace_size")(*args, ctypes.byref(n)))
-    need = n.value
+    args = (ctypes.byref(d),) if lead == 2 else (ctypes.byref(d), cup)
+    need = 0
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        _check(fn + "_workspace_size", getattr(lib, fn + "_workspace_size")(*args, ctypes.byref(n)))
+        need = n.value
     with _guard(dev):
-        with _on(stream):
-            if o is None:
-                o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-            if final_state is None:
-                final_state = torch.empty(state, dtype=f32, device=v.device)
-            if workspace is None and need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+        if o is None or final_state is None or need > 0:
+            with _on(stream):
+                if o is None:
+                    o = _empty_rows(v)
+                if final_state is None:
+                    final_state = log_decay.new_empty(state)
+                if need > 0:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(fn, getattr(lib, fn)(*args, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                    _ptr(initial_state), _ptr(o), _ptr(final_state),
-                                    _ptr(workspace), ws_bytes, _stream(stream, dev)))
+        _check(fn, getattr(lib, fn)(*args, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                    log_decay.data_ptr(), _ptr(initial_state), o.data_ptr(),
+                                    final_state.data_ptr(), _ptr(workspace), ws_bytes,
+                                    _stream(stream, dev)))
     return o, final_state
 
 
@@ -632,7 +644,8 @@ def ssd_linattn_chunk_scan_varlen(q, k, v, log_decay, cu_seqlens, initial_states
 def ssd_linattn_decode_step(q, k, v, log_decay, state, o=None, scale=1.0, stream=None):
     """One linear-attention decode step: q, k [B, Hk, dk], v [B, Hv, dv], state
     [B, Hv, dk, dv] fp32 updated in place; returns o [B, Hv, dv]."""
-    d, dev = _linattn_dims(q, k, v, 1, (q.shape[0], 1, scale))
+    dev = _device_of(q)
+    d = _linattn_dims(q, k, v, 1, q.shape[0], 1, scale, dev)
     f32 = torch.float32
     _need("log_decay", log_decay, dev, f32, (d.v_heads,))
     _need("state", state, dev, f32, (d.batch, d.v_heads, d.dk, d.dv))
@@ -640,10 +653,10 @@ def ssd_linattn_decode_step(q, k, v, log_decay, state, o=None, scale=1.0, stream
     with _guard(dev):
         if o is None:
             with _on(stream):
-                o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+                o = _empty_rows(v)
         _check("ssd_linattn_decode_step", load().ssd_linattn_decode_step(
-            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o),
-            _stream(stream, dev)))
+            ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+            state.data_ptr(), o.data_ptr(), _stream(stream, dev)))
     return o
 
 
@@ -676,7 +689,7 @@ def ssd_attn_prefill(q, k, v, cu_seqlens, kv_starts=None, kv_lens=None, scale=No
     with _guard(dev):
         if o is None:
             with _on(stream):
-                o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                o = _empty_rows(q)
         _check("ssd_attn_prefill", load().ssd_attn_prefill(
             ctypes.byref(d), cup, stp, klp, _ptr(q), _ptr(k), _ptr(v), _ptr(o),
             _stream(stream, dev)))
@@ -715,15 +728,19 @@ def ssd_attn_decode_step(q, k, v, k_cache, v_cache, lengths, scale=None, o=None,
     lib = load()
     d = SsdAttnDims(B, 0, M, Hq, Hkv, D, qs, ks, vs, D ** -0.5 if scale is None else scale,
                     _io_dtype(q))
-    n = ctypes.c_size_t(0)
-    _check("ssd_attn_decode_workspace_size",
-           lib.ssd_attn_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    need = 0
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        _check("ssd_attn_decode_workspace_size",
+               lib.ssd_attn_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+        need = n.value
     with _guard(dev):
-        with _on(stream):
-            if o is None:
-                o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            if workspace is None and n.value > 0:
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+        if o is None or need > 0:
+            with _on(stream):
+                if o is None:
+                    o = _empty_rows(q)
+                if need > 0:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check("ssd_attn_decode_step", lib.ssd_attn_decode_step(
             ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),

@@ -6,7 +6,26 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace ssd {
+
+// Lets `kernel` be launched with `bytes` of dynamic LDS, once per device (`done`:
+// a bit per device, one word for each kernel).
+inline hipError_t allow_lds(const void *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess)
+        return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if ((done.load(std::memory_order_acquire) & bit) != 0)
+        return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess)
+        done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // One packed sequence of an attention launch.
 struct AttnSeq {

@@ -247,9 +247,9 @@ hipError_t prefill(PrefillArgs &args, int64_t nseq, const AttnSeq *seqs, hipStre
     constexpr int kRows = 32 * QB * NW;
     constexpr int KT = sizeof(T) == 2 ? 64 : 32;
     constexpr unsigned kSmem = 4u * KT * D * sizeof(T);
-    hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(&attn_prefill_kernel<T, D, NW, QB>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    hipError_t e = allow_lds(reinterpret_cast<const void *>(&attn_prefill_kernel<T, D, NW, QB>), (int)kSmem,
+                             allowed);
     if (e != hipSuccess)
         return e;
     // launches of at most SeqTab::kMax sequences and 2^31 - 1 work-groups,
@@ -530,7 +530,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a)
     const int64_t slot = (((b * a.Hkv + hk) * a.rtiles + rt) * a.nsplit) * 32 + row;
     float mx = kNoMax;
     for (int i = tid; i < ns; i += 256)
-        mx = fmaxf(mx, a.ml[slot + i * 32].x);
+        mx = fmaxf(mx, a.ml[slot + (int64_t)i * 32].x);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
         mx = fmaxf(mx, __shfl_xor(mx, off, 64));
@@ -540,12 +540,24 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a)
     mx = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-    for (int i = g; i < ns; i += G) {
-        const float2 ml = a.ml[slot + i * 32];
-        const float f = exp2_fast(ml.x - mx);
-        const float4 p = *reinterpret_cast<const float4 *>(a.part + (slot + i * 32) * D + 4 * d4);
-        v.x += f * p.x; v.y += f * p.y; v.z += f * p.z; v.w += f * p.w;
-        l += f * ml.y;
+    // eight chunks in flight per lane (their loads are independent, and few
+    // work-groups run)
+    constexpr int U = 8;
+    for (int i0 = g; i0 < ns; i0 += G * U) {
+        float2 ml[U];
+        float4 p[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = std::min(i0 + u * G, ns - 1);
+            ml[u] = a.ml[slot + (int64_t)i * 32];
+            p[u] = *reinterpret_cast<const float4 *>(a.part + (slot + (int64_t)i * 32) * D + 4 * d4);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = i0 + u * G < ns ? exp2_fast(ml[u].x - mx) : 0.f;
+            v.x += f * p[u].x; v.y += f * p[u].y; v.z += f * p[u].z; v.w += f * p[u].w;
+            l += f * ml[u].y;
+        }
     }
     sacc[g][d4] = v;
     if (d4 == 0)
@@ -577,8 +589,8 @@ int64_t decode_chunk(int64_t B, int64_t M, int64_t Hkv, int64_t rtiles)
 template <typename T, int D> hipError_t decode(const DecodeArgs &a, int64_t B, hipStream_t s)
 {
     typedef DecodeGeom<T, D> GM;
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attn_decode_kernel<T, D>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)GM::kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    hipError_t e = allow_lds(reinterpret_cast<const void *>(&attn_decode_kernel<T, D>), (int)GM::kSmem, allowed);
     if (e != hipSuccess)
         return e;
     const unsigned grid = (unsigned)(B * a.Hkv * a.rtiles * a.nsplit);

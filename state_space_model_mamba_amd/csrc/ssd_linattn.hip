@@ -188,7 +188,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     f32x16 R[DB];
     // ---- the state entering the segment ----
     const bool use_init = a->init != nullptr;
-    auto from_ws = [&](int j, float f) {                  // R = f R + slot j
+    auto add_ws = [&](int j, float f) {                   // R += f times slot j
         const float *p = wsp + j * wslot;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
                 const f32x4 z = *reinterpret_cast<const f32x4 *>(p + (d * 4 + g) * 256);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    R[d][4 * g + e] = __builtin_fmaf(R[d][4 * g + e], f, z[e]);
+                    R[d][4 * g + e] = __builtin_fmaf(z[e], f, R[d][4 * g + e]);
             }
     };
     auto to_ws = [&](int j, float f) {
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
             R[d][r] = 0.f;
     if (seg == 0) {
         if (kScan && a->copy_init && nseg > 1) {
-            from_ws(nseg - 1, 0.f);
+            add_ws(nseg - 1, 1.f);
         } else if (use_init) {
 #pragma unroll
             for (int d = 0; d < DB; ++d)
@@ -229,12 +229,11 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     } else if (kScan) {
         // slot 0 holds the state after segment 0 (the initial one included), slot
         // j segment j's from zero; those forgotten below 2^-150 are left out
-        const float fT = pow_of(g2, T0);
         int j = 0;
         while (j < seg - 1 && g2f * (float)T0 * (float)(seg - 1 - j) < -150.f)
             ++j;
         for (; j < seg; ++j)
-            from_ws(j, fT);
+            add_ws(j, pow_of(g2, (double)T0 * (seg - 1 - j)));
     }
 
     const unsigned lds0 = lds_addr(smem);
@@ -252,8 +251,12 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     const bool direct = -g2f * (float)C > kEpoch || g2f > 0.f;   // scaled every tile
     const int epoch = direct ? 0 : std::min(kEpochTiles, (int)(kEpoch / (1e-9f - g2f * (float)C)));
     // what R is multiplied by when it is rescaled, to more than fp32
-    const double fd = exp2(g2 * (double)(C * (direct ? 1 : epoch)));
-    const float fhi = (float)fd, flo = (float)(fd - (double)fhi);
+    float fhi = pow_of(g2, C * (direct ? 1 : epoch)), flo = 0.f;
+    if (epoch == kEpochTiles) {
+        const double fd = exp2(g2 * (double)(C * epoch));
+        fhi = (float)fd;
+        flo = (float)(fd - (double)fhi);
+    }
     const float scale = a->scale;
     for (int i = tid; i < kEpochTiles * C; i += 64 * NW)
         su[i] = pow_of(g2, direct ? C - 1 - i : -(i + 1));
@@ -559,9 +562,9 @@ hipError_t launch_part(const LinArgs &args, int64_t items, hipStream_t s)
     typedef LinSmem<T, DK, NW> SM;
     constexpr int kSmem = (kScan ? SM::kScan : SM::kState) + SM::kTables;
     static_assert(kSmem <= 160 * 1024, "LDS of a CU");
-    const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(&lin_scan_kernel<T, DK, NW, kScan>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    const hipError_t e =
+        allow_lds(reinterpret_cast<const void *>(&lin_scan_kernel<T, DK, NW, kScan>), kSmem, allowed);
     if (e != hipSuccess)
         return e;
     const int64_t grid = items * args.Hv * (args.dv / (32 * NW));
