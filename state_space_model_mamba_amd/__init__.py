@@ -503,6 +503,14 @@ class SsdAttnDims(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32)]
 
 
+def _offsets(name, x, n=None):
+    """A host sequence of offsets or lengths as int64: (array, pointer)."""
+    a, p = _cu_array(x)
+    if a.ndim != 1 or (len(a) < 1 if n is None else len(a) != n):
+        raise ValueError(f"{name} must hold " + ("S + 1 offsets" if n is None else "one entry per sequence"))
+    return a, p
+
+
 def _guard(di):
     """The tensors' device as the current one for a call's launches."""
     return contextlib.nullcontext() if torch.cuda.current_device() == di else torch.cuda.device(di)
@@ -567,9 +575,7 @@ def _linattn_scan(fn, lead, q, k, v, log_decay, cu_seqlens, initial_state, o, fi
     lib = load()
     dev = _device_of(q)
     if lead == 1:
-        cu, cup = _cu_array(cu_seqlens)
-        if len(cu) < 1:
-            raise ValueError("cu_seqlens must hold at least one offset")
+        cu, cup = _offsets("cu_seqlens", cu_seqlens)
         nseq = len(cu) - 1
     else:
         nseq = q.shape[0]
@@ -676,14 +682,9 @@ def ssd_attn_prefill(q, k, v, cu_seqlens, kv_starts=None, kv_lens=None, scale=No
     ks = _row_stride("k", k, dev, q.dtype, (Tk, Hkv, D))
     vs = _row_stride("v", v, dev, q.dtype, (Tk, Hkv, D))
     _need("o", o, dev, q.dtype, q.shape, optional=True)
-    cu, cup = _cu_array(cu_seqlens)
-    if len(cu) < 1:
-        raise ValueError("cu_seqlens must hold at least one offset")
-    st, stp = _cu_array(kv_starts) if kv_starts is not None else (None, None)
-    kl, klp = _cu_array(kv_lens) if kv_lens is not None else (None, None)
-    for name, a in (("kv_starts", st), ("kv_lens", kl)):
-        if a is not None and len(a) != len(cu) - 1:
-            raise ValueError(f"{name} must hold one entry per sequence")
+    cu, cup = _offsets("cu_seqlens", cu_seqlens)
+    st, stp = (None, None) if kv_starts is None else _offsets("kv_starts", kv_starts, len(cu) - 1)
+    kl, klp = (None, None) if kv_lens is None else _offsets("kv_lens", kv_lens, len(cu) - 1)
     d = SsdAttnDims(len(cu) - 1, T, Tk, Hq, Hkv, D, qs, ks, vs,
                     D ** -0.5 if scale is None else scale, _io_dtype(q))
     with _guard(dev):

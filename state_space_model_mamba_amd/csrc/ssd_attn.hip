@@ -28,6 +28,117 @@ constexpr float kNoMax = -1e30f;   // m before the first visible key (finite: m 
 // score (-inf) times it stays -inf.
 constexpr float kTinyScale = 1.17549435e-38f;
 
+// A 32-key tile in a wave's own LDS, for 32 rows (score columns): updates (m, l,
+// acc).  Keys from `see` (per lane) on are masked if `masked` (wave-uniform).
+template <typename T, int D>
+__device__ __forceinline__ void tile32(const unsigned char *Kt, const unsigned char *Vt,
+                                       const typename Piece<T>::V (&qf)[Tile<T, D>::kPieces], bool masked,
+                                       int see, float c,
+                                       int lane, float &m, float &l, f32x16 (&acc)[D / 32])
+{
+    typedef Tile<T, D> TL;
+    constexpr int DB = D / 32, PC = 16 / Piece<T>::E;
+    const int cl = lane & 31, hh = lane >> 5;
+    f32x16 s = {};
+#pragma unroll
+    for (int p = 0; p < TL::kPieces; ++p)
+        s = mma(TL::row_nat(Kt, cl, p, hh), qf[p], s);
+    if (masked) {
+        const int lim = see - 4 * hh;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (8 * (r >> 2) + (r & 3) >= lim)
+                s[r] = -__builtin_inff();
+    }
+    float t = s[0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r)
+        t = fmaxf(t, s[r]);
+    t = half_max(t) * c;
+    if (__any(t > m + kSlack)) {
+        const float mn = fmaxf(m, t), al = exp2_fast(m - mn);
+        m = mn;
+        l *= al;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                acc[d][r] *= al;
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        s[r] = exp2_fast(__builtin_fmaf(s[r], c, -m));
+        l += s[r];
+    }
+#pragma unroll
+    for (int p = 0; p < PC; ++p) {
+        const typename Piece<T>::V pf = acc_piece(s, p, (const T *)nullptr);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+            acc[d] = mma(TL::col_acc(Vt, p, 32 * d, lane), pf, acc[d]);
+    }
+}
+
+// The LDS of kernels whose waves work on tiles of their own: two slots of a K and a
+// V tile per wave, as many waves as fit.
+template <typename T, int D> struct WaveTiles {
+    static constexpr int kPitch = Tile<T, D>::kPitch;
+    static constexpr int kWaves = kPitch <= 256 ? 4 : kPitch == 512 ? 2 : 1;
+    static constexpr int kTileBytes = 32 * kPitch;
+    static constexpr unsigned kWaveSmem = 4u * kTileBytes;
+    static constexpr unsigned kSmem = kWaves * kWaveSmem;
+};
+
+// Joins the waves' results for the same 32 rows: each scales its sums to the common
+// m and leaves them in its part of the LDS as [row][D]; then out(i, v, m, l) is
+// called with four consecutive sums of the work-group for each i = row D + d.
+template <typename T, int D, typename Out>
+__device__ __forceinline__ void join_waves(unsigned char *smem, float (&sm)[WaveTiles<T, D>::kWaves][32],
+                                           float (&sl)[WaveTiles<T, D>::kWaves][32], int w, int lane, int rows,
+                                           float m, float l, const f32x16 (&acc)[D / 32], Out out)
+{
+    typedef WaveTiles<T, D> GM;
+    constexpr int NW = GM::kWaves, DB = D / 32;
+    const int cl = lane & 31, hh = lane >> 5;
+    l = half_sum(l);
+    if (hh == 0) {
+        sm[w][cl] = m;
+        sl[w][cl] = l;
+    }
+    __syncthreads();
+    float mt = sm[0][cl];
+#pragma unroll
+    for (int i = 1; i < NW; ++i)
+        mt = fmaxf(mt, sm[i][cl]);
+    const float f = exp2_fast(m - mt);
+    float *wp = reinterpret_cast<float *>(smem + w * GM::kWaveSmem);
+    if (cl < rows)
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4 *>(wp + cl * D + 32 * d + 8 * g + 4 * hh) =
+                    f32x4{acc[d][4 * g] * f, acc[d][4 * g + 1] * f, acc[d][4 * g + 2] * f,
+                          acc[d][4 * g + 3] * f};
+    __syncthreads();
+    for (int i = 4 * (64 * w + lane); i < rows * D; i += 4 * 64 * NW) {
+        const int row = i / D;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(smem + i * 4);
+#pragma unroll
+        for (int j = 1; j < NW; ++j)
+            v += *reinterpret_cast<const f32x4 *>(smem + j * GM::kWaveSmem + i * 4);
+        float mr = sm[0][row];
+#pragma unroll
+        for (int j = 1; j < NW; ++j)
+            mr = fmaxf(mr, sm[j][row]);
+        float lr = 0.f;
+#pragma unroll
+        for (int j = 0; j < NW; ++j)
+            lr += sl[j][row] * exp2_fast(sm[j][row] - mr);
+        out(i, v, mr, lr);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Prefill
 // ---------------------------------------------------------------------------
@@ -241,15 +352,97 @@ __global__ __launch_bounds__(64 * NW, QB == 1 && D <= 128 ? 2 : 1) void attn_pre
     }
 }
 
-template <typename T, int D, int NW, int QB>
-hipError_t prefill(PrefillArgs &args, int64_t nseq, const AttnSeq *seqs, hipStream_t s)
+// Few rows (short prompts, or few heads): 32 rows per work-group, the waves taking
+// every kWaves-th 32-key tile of them, each with its own running (m, l, acc), joined
+// at the end.  A work-group then walks its keys in a quarter of the steps, and eight
+// times as many share the chip.
+template <typename T, int D>
+__global__ __launch_bounds__((64 * WaveTiles<T, D>::kWaves), 1) void attn_prefill_few_kernel(
+    PrefillArgs args_in_kernarg)
 {
-    constexpr int kRows = 32 * QB * NW;
-    constexpr int KT = sizeof(T) == 2 ? 64 : 32;
-    constexpr unsigned kSmem = 4u * KT * D * sizeof(T);
-    static std::atomic<uint64_t> allowed{0};
-    hipError_t e = allow_lds(reinterpret_cast<const void *>(&attn_prefill_kernel<T, D, NW, QB>), (int)kSmem,
-                             allowed);
+    typedef WaveTiles<T, D> GM;
+    typedef Tile<T, D> TL;
+    typedef typename Piece<T>::V V;
+    constexpr int E = Piece<T>::E, NW = GM::kWaves, DB = D / 32;
+    constexpr int kLoads = 2 * TileLoad<T, D, 32, 1>::kPer;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ float sm[NW][32], sl[NW][32];
+    __shared__ int64_t srow[32];
+
+    const PrefillArgsPtr a = (PrefillArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
+    const int cl = lane & 31, hh = lane >> 5;
+    const int Hkv = a->Hkv, grp = a->grp;
+    const int item = (int)(blockIdx.x / (unsigned)Hkv), hk = (int)(blockIdx.x % (unsigned)Hkv);
+    const int below = __popcll(__ballot(a->tab.pre[lane] <= item)) +
+                      __popcll(__ballot(a->tab.pre[64 + lane] <= item));
+    const int si = uniform_int(below - 1);
+    const int lq = a->tab.seq[si].lq, lk = a->tab.seq[si].lk;
+    const int64_t nrow = (int64_t)lq * grp;
+    const int blk = (int)((nrow + 31) / 32) - 1 - (item - a->tab.pre[si]);
+    const int64_t row0 = (int64_t)blk * 32;
+    const int rows = (int)std::min<int64_t>(32, nrow - row0);
+    const T *kp = (const T *)a->k + a->tab.seq[si].k0 * a->k_stride + (int64_t)hk * D;
+    const T *vp = (const T *)a->v + a->tab.seq[si].k0 * a->v_stride + (int64_t)hk * D;
+
+    const unsigned rr = (unsigned)(row0 + std::min(cl, rows - 1));
+    const unsigned tok = rr / (unsigned)grp, head = hk * grp + rr % (unsigned)grp;
+    const int64_t qt = a->tab.seq[si].q0 + tok;
+    if (w == 0 && hh == 0)
+        srow[cl] = (qt * a->Hq + head) * D;
+    const int lim = std::max(0, lk - lq + (int)tok + 1);
+    V qf[TL::kPieces];
+    const T *qp = (const T *)a->q + qt * a->q_stride + (int64_t)head * D;
+#pragma unroll
+    for (int p = 0; p < TL::kPieces; ++p) {
+        qf[p] = *reinterpret_cast<const V *>(qp + (2 * p + hh) * E);
+        if (a->neg)
+            qf[p] = flip<T>(qf[p]);
+    }
+    const int kend = uniform_int(std::max(0, lk - lq + (int)((unsigned)(row0 + rows - 1) / (unsigned)grp) + 1));
+    const int kall = uniform_int(std::max(0, lk - lq + (int)((unsigned)row0 / (unsigned)grp) + 1));
+
+    unsigned char *mine = smem + w * GM::kWaveSmem;
+    const unsigned lds0 = lds_addr(mine);
+    auto issue = [&](int t0, int slot) {
+        const unsigned dst = lds0 + slot * 2 * GM::kTileBytes;
+        TileLoad<T, D, 32, 1>::issue(dst, kp, a->k_stride, t0, lk, 0, lane);
+        TileLoad<T, D, 32, 1>::issue(dst + GM::kTileBytes, vp, a->v_stride, t0, lk, 0, lane);
+    };
+    f32x16 acc[DB] = {};
+    float m = kNoMax, l = 0.f;
+    int t0 = 32 * w;
+    if (t0 < kend)
+        issue(t0, 0);
+    for (int n = 0; t0 < kend; ++n, t0 += 32 * NW) {
+        const int tn = t0 + 32 * NW;
+        // the slot issued next was read by this wave before: its reads are done
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (tn < kend) {
+            issue(tn, (n + 1) & 1);
+            wait_vmcnt<(kLoads < 63 ? kLoads : 63)>();
+        } else {
+            wait_vmcnt<0>();
+        }
+        const unsigned char *Kt = mine + (n & 1) * 2 * GM::kTileBytes, *Vt = Kt + GM::kTileBytes;
+        tile32<T, D>(Kt, Vt, qf, t0 + 32 > kall, lim - t0, a->c, lane, m, l, acc);
+    }
+    T *o = (T *)a->o;
+    join_waves<T, D>(smem, sm, sl, w, lane, rows, m, l, acc, [&](int i, f32x4 v, float, float lr) {
+        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        T *op = o + srow[i / D] + i % D;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            op[e] = (T)(v[e] * inv);
+    });
+}
+
+// Launches `kernel` with work-groups of `rows` rows.
+hipError_t prefill_launch(void (*kernel)(PrefillArgs), int64_t rows, int threads, unsigned smem,
+                          std::atomic<uint64_t> &allowed, PrefillArgs &args, int64_t nseq, const AttnSeq *seqs,
+                          hipStream_t s)
+{
+    hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), (int)smem, allowed);
     if (e != hipSuccess)
         return e;
     // launches of at most SeqTab::kMax sequences and 2^31 - 1 work-groups,
@@ -259,33 +452,50 @@ hipError_t prefill(PrefillArgs &args, int64_t nseq, const AttnSeq *seqs, hipStre
         int64_t items = 0;
         const int64_t most = INT32_MAX / args.Hkv;
         while (at < nseq && n < SeqTab::kMax) {
-            const int64_t blocks = (seqs[at].lq * (int64_t)args.grp + kRows - 1) / kRows;
+            const int64_t blocks = (seqs[at].lq * (int64_t)args.grp + rows - 1) / rows;
             if (blocks > most - items)
                 break;
-            if (blocks > 0)
-                args.tab.seq[n++] = seqs[at];
+            args.tab.seq[n++] = seqs[at++];
             items += blocks;
-            ++at;
         }
         if (n == 0)
-            break;
+            return hipErrorInvalidValue;                  // one sequence alone is too much
         std::stable_sort(args.tab.seq, args.tab.seq + n,
                          [](const AttnSeq &x, const AttnSeq &y) { return x.lk > y.lk; });
         items = 0;
         for (int i = 0; i < n; ++i) {
             args.tab.pre[i] = (int32_t)items;
-            items += (args.tab.seq[i].lq * (int64_t)args.grp + kRows - 1) / kRows;
+            items += (args.tab.seq[i].lq * (int64_t)args.grp + rows - 1) / rows;
         }
         for (int i = n; i < 128; ++i)
             args.tab.pre[i] = INT32_MAX;
-        attn_prefill_kernel<T, D, NW, QB>
-            <<<dim3((unsigned)(items * args.Hkv)), dim3(64 * NW), kSmem, s>>>(args);
+        kernel<<<dim3((unsigned)(items * args.Hkv)), dim3(threads), smem, s>>>(args);
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
     }
     return hipSuccess;
 }
 
+template <typename T, int D, int NW>
+hipError_t prefill(PrefillArgs &args, int64_t nseq, const AttnSeq *seqs, hipStream_t s)
+{
+    static std::atomic<uint64_t> allowed{0}, allowed_few{0};
+    constexpr int64_t kRows = 32 * NW;
+    // Few rows go to the kernel of 32-row work-groups.  Measured (us, few against
+    // many; work-groups of 32 rows in brackets): bf16, 32 heads over 8 of 128, 64
+    // queries on 4000 cached keys 40 against 103 [64], 256 on 4000 46 against 108
+    // [256], a prompt of 500 18.9 against 18.6 [504], of 1000 43 against 31 [1000]; fp32,
+    // 8 heads of 128, 1000 tokens 86 against 189 [252], 2000 tokens 180 against 367
+    // [504].
+    int64_t blocks = 0;
+    for (int64_t i = 0; i < nseq && blocks < (int64_t(1) << 32); ++i)
+        blocks += (seqs[i].lq * (int64_t)args.grp + 31) / 32;
+    if (blocks * args.Hkv <= (sizeof(T) == 2 ? 512 : 1024))
+        return prefill_launch(&attn_prefill_few_kernel<T, D>, 32, 64 * WaveTiles<T, D>::kWaves,
+                              WaveTiles<T, D>::kSmem, allowed_few, args, nseq, seqs, s);
+    constexpr unsigned kSmem = 4u * (sizeof(T) == 2 ? 64 : 32) * D * sizeof(T);
+    return prefill_launch(&attn_prefill_kernel<T, D, NW, 1>, kRows, 64 * NW, kSmem, allowed, args, nseq, seqs, s);
+}
 
 // ---------------------------------------------------------------------------
 // One decode token per sequence
@@ -313,14 +523,6 @@ struct DecodeArgs {
     int neg;
 };
 
-template <typename T, int D> struct DecodeGeom {
-    static constexpr int kPitch = Tile<T, D>::kPitch;
-    static constexpr int kWaves = kPitch <= 256 ? 4 : kPitch == 512 ? 2 : 1;
-    static constexpr int kTileBytes = 32 * kPitch;
-    static constexpr unsigned kWaveSmem = 4u * kTileBytes;          // two slots of K and V
-    static constexpr unsigned kSmem = kWaves * kWaveSmem;
-};
-
 // Rows first .. 31 of a wave's K (or V) tile become the new token's.
 template <typename T, int D>
 __device__ __forceinline__ void put_rows(unsigned char *tile, const T *src, int first, int lane)
@@ -334,12 +536,12 @@ __device__ __forceinline__ void put_rows(unsigned char *tile, const T *src, int 
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__((64 * DecodeGeom<T, D>::kWaves), 1) void attn_decode_kernel(DecodeArgs a)
+__global__ __launch_bounds__((64 * WaveTiles<T, D>::kWaves), 1) void attn_decode_kernel(DecodeArgs a)
 {
-    typedef DecodeGeom<T, D> GM;
+    typedef WaveTiles<T, D> GM;
     typedef Tile<T, D> TL;
     typedef typename Piece<T>::V V;
-    constexpr int E = Piece<T>::E, NW = GM::kWaves, DB = D / 32, PC = 16 / E;
+    constexpr int E = Piece<T>::E, NW = GM::kWaves, DB = D / 32;
     constexpr int kLoads = 2 * TileLoad<T, D, 32, 1>::kPer;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float sm[NW][32], sl[NW][32];
@@ -423,84 +625,10 @@ __global__ __launch_bounds__((64 * DecodeGeom<T, D>::kWaves), 1) void attn_decod
             put_rows<T, D>(Vt, vn, at - t0, lane);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
-        f32x16 s = {};
-#pragma unroll
-        for (int p = 0; p < TL::kPieces; ++p)
-            s = mma(TL::row_nat(Kt, cl, p, hh), qf[p], s);
-        if (t0 + 32 > kend) {
-            const int see = kend - t0 - 4 * hh;
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (8 * (r >> 2) + (r & 3) >= see)
-                    s[r] = -__builtin_inff();
-        }
-        float t = s[0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r)
-            t = fmaxf(t, s[r]);
-        t = half_max(t) * a.c;
-        if (__any(t > m + kSlack)) {
-            const float mn = fmaxf(m, t), al = exp2_fast(m - mn);
-            m = mn;
-            l *= al;
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    acc[d][r] *= al;
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            s[r] = exp2_fast(__builtin_fmaf(s[r], a.c, -m));
-            l += s[r];
-        }
-#pragma unroll
-        for (int p = 0; p < PC; ++p) {
-            const V pf = acc_piece(s, p, (const T *)nullptr);
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-                acc[d] = mma(TL::col_acc(Vt, p, 32 * d, lane), pf, acc[d]);
-        }
+        tile32<T, D>(Kt, Vt, qf, t0 + 32 > kend, kend - t0, a.c, lane, m, l, acc);
     }
-    l = half_sum(l);
-
-    // join the waves: each scales its sums to the common m and leaves them in
-    // its part of the LDS as [row][D]
-    if (hh == 0) {
-        sm[w][cl] = m;
-        sl[w][cl] = l;
-    }
-    __syncthreads();
-    float mt = sm[0][cl];
-#pragma unroll
-    for (int i = 1; i < NW; ++i)
-        mt = fmaxf(mt, sm[i][cl]);
-    const float f = exp2_fast(m - mt);
-    float *wp = reinterpret_cast<float *>(mine);
-    if (cl < rows)
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<f32x4 *>(wp + cl * D + 32 * d + 8 * g + 4 * hh) =
-                    f32x4{acc[d][4 * g] * f, acc[d][4 * g + 1] * f, acc[d][4 * g + 2] * f,
-                          acc[d][4 * g + 3] * f};
-    __syncthreads();
     const int64_t slot = ((int64_t)item * a.nsplit + split) * 32;
-    for (int i = 4 * tid; i < rows * D; i += 4 * 64 * NW) {
-        const int row = i / D;
-        f32x4 v = *reinterpret_cast<const f32x4 *>(smem + i * 4);
-#pragma unroll
-        for (int j = 1; j < NW; ++j)
-            v += *reinterpret_cast<const f32x4 *>(smem + j * GM::kWaveSmem + i * 4);
-        float mr = sm[0][row];
-#pragma unroll
-        for (int j = 1; j < NW; ++j)
-            mr = fmaxf(mr, sm[j][row]);
-        float lr = 0.f;
-#pragma unroll
-        for (int j = 0; j < NW; ++j)
-            lr += sl[j][row] * exp2_fast(sm[j][row] - mr);
+    join_waves<T, D>(smem, sm, sl, w, lane, rows, m, l, acc, [&](int i, f32x4 v, float mr, float lr) {
         if (a.nsplit == 1) {
             const float inv = 1.f / lr;
 #pragma unroll
@@ -509,9 +637,9 @@ __global__ __launch_bounds__((64 * DecodeGeom<T, D>::kWaves), 1) void attn_decod
         } else {
             *reinterpret_cast<f32x4 *>(a.part + slot * D + i) = v;
             if (i % D == 0)
-                a.ml[slot + row] = make_float2(mr, lr);
+                a.ml[slot + i / D] = make_float2(mr, lr);
         }
-    }
+    });
 }
 
 // Joins the chunks of one query head: o = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i.
@@ -588,7 +716,7 @@ int64_t decode_chunk(int64_t B, int64_t M, int64_t Hkv, int64_t rtiles)
 
 template <typename T, int D> hipError_t decode(const DecodeArgs &a, int64_t B, hipStream_t s)
 {
-    typedef DecodeGeom<T, D> GM;
+    typedef WaveTiles<T, D> GM;
     static std::atomic<uint64_t> allowed{0};
     hipError_t e = allow_lds(reinterpret_cast<const void *>(&attn_decode_kernel<T, D>), (int)GM::kSmem, allowed);
     if (e != hipSuccess)
@@ -623,15 +751,15 @@ hipError_t launch_attn_prefill(int bf16, int64_t nseq, const AttnSeq *seqs, int6
     args.neg = scale < 0.f;
     if (bf16) {
         switch (D) {
-        case 64: return prefill<__bf16, 64, 8, 1>(args, nseq, seqs, s);
-        case 128: return prefill<__bf16, 128, 8, 1>(args, nseq, seqs, s);
-        case 256: return prefill<__bf16, 256, 4, 1>(args, nseq, seqs, s);
+        case 64: return prefill<__bf16, 64, 8>(args, nseq, seqs, s);
+        case 128: return prefill<__bf16, 128, 8>(args, nseq, seqs, s);
+        case 256: return prefill<__bf16, 256, 4>(args, nseq, seqs, s);
         }
     } else {
         switch (D) {
-        case 64: return prefill<float, 64, 4, 1>(args, nseq, seqs, s);
-        case 128: return prefill<float, 128, 4, 1>(args, nseq, seqs, s);
-        case 256: return prefill<float, 256, 4, 1>(args, nseq, seqs, s);
+        case 64: return prefill<float, 64, 4>(args, nseq, seqs, s);
+        case 128: return prefill<float, 128, 4>(args, nseq, seqs, s);
+        case 256: return prefill<float, 256, 4>(args, nseq, seqs, s);
         }
     }
     return hipErrorInvalidValue;
@@ -642,7 +770,7 @@ int64_t attn_decode_splits(int64_t B, int64_t M, int64_t Hq, int64_t Hkv)
 {
     const int64_t rtiles = (Hq / Hkv + 31) / 32;
     const int64_t chunk = decode_chunk(B, M, Hkv, rtiles);
-    return (M + chunk - 1) / chunk;
+    return std::max<int64_t>(1, (M + chunk - 1) / chunk);
 }
 
 size_t attn_decode_workspace(int64_t B, int64_t M, int64_t Hq, int64_t Hkv, int64_t D)

@@ -41,6 +41,35 @@ def test_head_layouts(io, hq, hkv, d):
     check(io, o, q[1], k[1], v[1], d ** -0.5, f"{hq}/{hkv} x {d}")
 
 
+@pytest.mark.parametrize("io,hq,hkv,d", [("bf16", 32, 32, 64), ("bf16", 66, 22, 128), ("bf16", 32, 32, 256),
+                                         ("f32", 48, 48, 64), ("f32", 96, 24, 128), ("f32", 48, 48, 256)])
+def test_many_rows(io, hq, hkv, d):
+    """Enough rows for the kernel of large row blocks (the small cases take the
+    one that splits the keys): several sequences, some on cached prefixes, one that
+    sees nothing at first, ragged everywhere."""
+    lq, lk = [300, 1, 64, 33, 150, 129], [300, 50, 64, 97, 100, 129]
+    starts = [0, 300, 350, 414, 511, 611]
+    cu = np.concatenate([[0], np.cumsum(lq)])
+    q, k, v = prompt(hq + d, io, int(cu[-1]), 740, hq, hkv, d, sliced=True)
+    o = ssd.ssd_attn_prefill(q[0], k[0], v[0], cu, kv_starts=starts, kv_lens=lk)
+    for i in range(len(lq)):
+        s = slice(starts[i], starts[i] + lk[i])
+        check(io, o[cu[i]:cu[i + 1]], q[1][cu[i]:cu[i + 1]], k[1][s], v[1][s], d ** -0.5, f"seq {i}")
+
+
+def test_many_rows_growing_scores():
+    """The large-block kernel's running maximum over 10 tiles."""
+    L, h, d = 600, 32, 64
+    q, k, v = prompt(5, "bf16", L, L, h, h, d)
+    kk = (torch.ones(L, h, d) * torch.arange(L)[:, None, None] / 8).to(torch.bfloat16)
+    qq = torch.ones(L, h, d, dtype=torch.bfloat16)
+    for kx in (kk, kk.flip(0).contiguous()):
+        o = ssd.ssd_attn_prefill(qq.cuda(), kx.cuda(), v[0], [0, L])
+        for j in (0, h - 1):
+            check("bf16", o[:, j:j + 1], qq[:, :1].double().numpy(), kx[:, j:j + 1].double().numpy(),
+                  v[1][:, j:j + 1], d ** -0.5, f"head {j}")
+
+
 @pytest.mark.parametrize("scale", [0.0, 1e-40, -0.3, 2.0])
 def test_scales(scale):
     q, k, v = prompt(3, "f32", 70, 70, 2, 2, 64)
@@ -161,6 +190,41 @@ def test_step_short_capacities():
     for M in (1, 5, 128, 129):
         q, k, v, kc, vc = step_inputs(M, "bf16", 3, M, 2, 1, 64)
         check_step("bf16", q, k, v, kc, vc, [M - 1, 0, M])
+
+
+def test_step_without_capacity():
+    q, k, v, _, _ = step_inputs(3, "bf16", 2, 1, 4, 2, 64)
+    c = torch.empty((2, 0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    n = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    assert not ssd.ssd_attn_decode_step(q[0], k[0], v[0], c, c.clone(), n).any()
+
+
+def test_step_offsets_past_32_bits():
+    """A cache of more than 2^31 elements: the last sequence's rows lie past it."""
+    B, M, hkv, d = 3, 1 << 20, 8, 128                     # 3 x 2^30 elements
+    gen = torch.Generator().manual_seed(5)
+    q, k, v = (randn(gen, B, h, d, io="bf16") for h in (16, hkv, hkv))
+    kc = torch.zeros(B, M, hkv, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    at = M - 2
+    kt, vt = randn(gen, 40, hkv, d, io="bf16"), randn(gen, 40, hkv, d, io="bf16")
+    kc[2, at - 40:at], vc[2, at - 40:at] = kt[0] * 4, vt[0]
+    # the zero keys before score 0 and have value 0: they only add to the sum
+    n = torch.tensor([-1, 3, at], dtype=torch.int32, device="cuda")
+    o = ssd.ssd_attn_decode_step(q[0], k[0], v[0], kc, vc, n)
+    assert torch.equal(kc[2, at], k[0][2]) and torch.equal(vc[2, at], v[0][2])
+    assert not kc[2, at + 1:].any() and not kc[0].any() and not o[0].any()
+    kk = np.concatenate([host(kc[2, at - 40:at]), k[1][2:3]])
+    vv = np.concatenate([vt[1], v[1][2:3]])
+    for h in (0, 15):
+        a = d ** -0.5 * (kk[:, h // 2] @ q[1][2, h])
+        p = np.exp(a - a.max())
+        rest = (at - 40) * np.exp(-a.max())
+        want = p @ vv[:, h // 2] / (p.sum() + rest)
+        size = p @ np.abs(vv[:, h // 2]) / (p.sum() + rest)
+        # bf16 roundings as in attn_bound; a sum of 2^20 equal terms in fp32 over 4096
+        # partial sums of 256 each is off by some 2^-15 at most
+        assert (np.abs(host(o[2, h]) - want) <= 2.0 ** -8 * (np.abs(want) + 1.01 * size) + 2.0 ** -12 * size).all()
 
 
 def test_step_long_cache():

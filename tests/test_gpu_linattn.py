@@ -93,6 +93,22 @@ def test_packed(io):
             check(io, o[a:b], fin[i], q[1][a:b], k[1][a:b], v[1][a:b], g[1], S0[1][i], -1.5, f"seq {i}")
 
 
+@pytest.mark.parametrize("io,dk,dv", [("bf16", 128, 128), ("bf16", 128, 64), ("bf16", 256, 256), ("f32", 64, 64),
+                                      ("f32", 256, 64)])
+def test_slow_decays_over_many_tiles(io, dk, dv):
+    """Heads that hardly forget over thousands of tokens (many epochs and segments
+    between rescales) and ones that forget at every speed, the state to fp32."""
+    L, hv = 3001, 4
+    g = [-1e-5, -0.004, -0.02, -0.9]
+    q, k, v, gg, S0 = inputs(dk + dv, io, (1, L), 2, hv, dk, dv, 1, g=g)
+    o, fin = ssd.ssd_linattn_chunk_scan(q[0], k[0], v[0], gg[0], initial_state=S0[0])
+    check(io, o[0], fin[0], q[1][0], k[1][0], v[1][0], gg[1], S0[1][0], 1.0, "slow decays")
+    _, rS, _, _ = att.linattn(q[1][0], k[1][0], v[1][0], gg[1], S0[1][0])
+    for h in range(hv):      # sums of thousands of fp32 roundings of either sign: 1e-6 of the norm
+        e = np.linalg.norm(host(fin[0, h]) - rS[h]) / np.linalg.norm(rS[h])
+        assert e < 2e-6, f"head {h}: state off by {e:.2e} of its norm"
+
+
 def test_many_sequences():
     """More sequences than one launch takes."""
     lens = [(7 * i) % 5 for i in range(250)]
@@ -181,6 +197,20 @@ def test_deterministic_on_another_stream_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, o) and torch.equal(end, eager)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight at once, each with its own workspace."""
+    cases = [inputs(50 + i, "bf16", (1, 1500), 2, 4, 128, 128, 1) for i in range(2)]
+    want = [ssd.ssd_linattn_chunk_scan(c[0][0], c[1][0], c[2][0], c[3][0], initial_state=c[4][0]) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[ssd.ssd_linattn_chunk_scan(c[0][0], c[1][0], c[2][0], c[3][0], initial_state=c[4][0], stream=s)
+            for c, s in zip(cases, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for g in got:
+        for (o, f), (wo, wf) in zip(g, want):
+            assert torch.equal(o, wo) and torch.equal(f, wf)
 
 
 def test_refusals():
