@@ -82,7 +82,8 @@ template <typename T, int DK, int NW> struct LinSmem {
     // the one between, so that three instead of two share a CU (8 x 2048 tokens of 24
     // heads of 128 x 64 in bf16: 75 us against 94), as does whatever has no room for it.
     static constexpr int kRing = 3 * (kScanSlot + kP) <= 158 * 1024 && NW == 4 ? 3 : 2;
-    static constexpr int kScan = kRing * (kScanSlot + kP), kState = kRing * kStateSlot;
+    static constexpr int kScan = kRing * (kScanSlot + kP);
+    static constexpr int kStateRing = 3 * kStateSlot <= 159 * 1024 ? 3 : 2, kState = kStateRing * kStateSlot;
     static constexpr int kTables = ((kEpochTiles + 1) * C + kEpochTiles + 1) * 4;
 };
 
@@ -119,16 +120,210 @@ __device__ __forceinline__ void weigh(bf16x8 v, const f32x4 &u0, const f32x4 &u1
         x[i] = __builtin_bit_cast(bf16x8, xb[i]);
 }
 
-// The work of one segment of one (sequence, value head, column tile): with
-// kScan, o over the segment (and the end state for a sequence's last segment);
-// without, its end state into the workspace.
+// What a work-group of either kernel works on.
+struct Work {
+    int si, seg, head, ct, hk;                // sequence, segment, value head, column tile, query/key head
+    int len, nseg, beg, end;                  // the sequence's tokens and segments, the segment's tokens
+};
+template <int CT> __device__ __forceinline__ Work work_of(LinArgsPtr a, int lane)
+{
+    // value heads of a query/key head, and their column tiles, next to each other
+    // on one XCD: they read the same q and k
+    const unsigned nb = gridDim.x, per = nb / 8;
+    const unsigned bid = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
+    const int Hv = a->Hv, nct = a->dv / CT, hc = Hv * nct;
+    const int item = (int)(bid / (unsigned)hc), hx = (int)(bid % (unsigned)hc);
+    const int below = __popcll(__ballot(a->tab.pre[lane] <= item)) +
+                      __popcll(__ballot(a->tab.pre[64 + lane] <= item));
+    Work k;
+    k.si = uniform_int(below - 1);
+    k.seg = item - a->tab.pre[k.si];
+    k.head = hx / nct;
+    k.ct = hx % nct;
+    k.hk = k.head / (Hv / a->Hk);
+    k.len = a->tab.len[k.si];
+    k.nseg = std::max(1, (k.len + a->seg_tokens - 1) / a->seg_tokens);
+    k.beg = k.seg * a->seg_tokens;
+    k.end = std::min(k.len, k.beg + a->seg_tokens);
+    return k;
+}
+
+// A wave's 32 columns of a state: element (row, column) of the [dk][dv] matrix of
+// init and fin, and its slot in the workspace (fragment order: coalesced).
+template <typename T, int DK>
+__device__ __forceinline__ void load_state(f32x16 (&R)[DK / 32], const float *p, int dv, int hh)
+{
+#pragma unroll
+    for (int d = 0; d < DK / 32; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            R[d][r] = p[(int64_t)(32 * d + state_row<T>(r, hh)) * dv];
+}
+template <int DK> __device__ __forceinline__ void store_slot(float *p, const f32x16 (&R)[DK / 32])
+{
+#pragma unroll
+    for (int d = 0; d < DK / 32; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<f32x4 *>(p + (d * 4 + g) * 256) =
+                f32x4{R[d][4 * g], R[d][4 * g + 1], R[d][4 * g + 2], R[d][4 * g + 3]};
+}
+template <int DK> __device__ __forceinline__ void add_slot(f32x16 (&R)[DK / 32], const float *p, float f)
+{
+#pragma unroll
+    for (int d = 0; d < DK / 32; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 z = *reinterpret_cast<const f32x4 *>(p + (d * 4 + g) * 256);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                R[d][4 * g + e] = __builtin_fmaf(z[e], f, R[d][4 * g + e]);
+        }
+}
+
+// A tile's update of the wave's state columns, from its K tile in LDS (lane offset
+// `bk` included) and its V operands: R += sum_s u_s k_s v_s^T, u being the lane's
+// weights of the tokens (u4(i, j): four of piece i).
+template <typename T, int DK, int kTerms, typename U>
+__device__ __forceinline__ void update(f32x16 (&R)[DK / 32], unsigned bk,
+                                       const typename Piece<T>::V (&vf)[16 / Piece<T>::E],
+                                       typename Piece<T>::V (&kf)[DK / 32], U u4)
+{
+    typedef LaneBase<T, DK> BK;
+    constexpr int DB = DK / 32, PT = 16 / Piece<T>::E;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+        if constexpr (sizeof(T) == 2) {
+            bf16x8 x[kTerms];
+            weigh(vf[i], u4(i, 0), u4(i, 1), x);
+#pragma unroll
+            for (int j = 0; j < kTerms; ++j)
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    R[d] = mma(kf[d], x[j], R[d]);
+        } else {
+            const f32x4 x = vf[i] * u4(i, 0);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                R[d] = mma(kf[d], x, R[d]);
+        }
+        if (i + 1 < PT)
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                kf[d] = BK::col_piece(0, bk, i + 1, d);
+    }
+}
+
+// The end state of a segment (every segment but its sequence's last, so a whole
+// number of tiles) into its slot: sum_t lambda^(T-1-t) k_t v_t^T, with the first
+// segment's initial state.  The tiles are walked from the end: the weights then
+// only shrink, R needs no rescaling, the walk ends where lambda^(T-1-t) is 0 in
+// fp32, and the tokens read last are those the scan reads first.
+template <typename T, int DK, int NW>
+__global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void lin_state_kernel(
+    LinArgs args_in_kernarg)
+{
+    typedef LinSmem<T, DK, NW> SM;
+    constexpr int C = SM::C, CT = SM::CT, DB = DK / 32, PT = 16 / Piece<T>::E, E = Piece<T>::E;
+    typedef typename Piece<T>::V V;
+    typedef LaneBase<T, DK> BK;
+    typedef LaneBase<T, CT> BV;
+    typedef TileLoad<T, DK, C, NW> LK;
+    typedef TileLoad<T, CT, C, NW> LV;
+    constexpr int kLoads = LK::kPer + LV::kPer, kSlot = SM::kStateSlot, kRing = SM::kStateRing;
+    extern __shared__ __align__(1024) unsigned char smem[];   // the ring, then lambda^(C-1-s)
+    float *su = reinterpret_cast<float *>(smem + SM::kState);
+
+    const LinArgsPtr a = (LinArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6), hh = lane >> 5;
+    const Work k = work_of<CT>(a, lane);
+    const int dv = a->dv, Hv = a->Hv, ntile = (k.end - k.beg) / C;
+    const double g2 = std::max(a->g[k.head] * kLog2e, -1e5);
+    const float g2f = (float)g2;
+    const T *kp = (const T *)a->k + a->tab.tok[k.si] * a->k_stride + (int64_t)k.hk * DK;
+    const T *vp = (const T *)a->v + a->tab.tok[k.si] * a->v_stride + (int64_t)k.head * dv + k.ct * CT;
+    float *slot0 = a->ws + (((int64_t)a->tab.slot[k.si] * Hv + k.head) * (dv / CT) + k.ct) * ((int64_t)DK * CT) +
+                   w * (DK * 32) + lane * 4;
+    const int64_t wslot = (int64_t)Hv * DK * dv;          // floats between slots
+
+    if (tid < C)
+        su[tid] = pow_of(g2, C - 1 - tid);
+    // tiles that count: lambda^(n C) >= 2^-150
+    const int cnt = g2f * (float)C * (float)ntile > -150.f ? ntile : std::min(ntile, (int)(-150.f / (g2f * (float)C)) + 1);
+    f32x16 R[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            R[d][r] = 0.f;
+    if (k.seg == 0 && a->init) {
+        load_state<T, DK>(R, a->init + (a->tab.id[k.si] * (int64_t)Hv + k.head) * DK * dv + k.ct * CT + 32 * w +
+                                 (lane & 31), dv, hh);
+        if (a->copy_init)
+            store_slot<DK>(slot0 + (k.nseg - 1) * wslot, R);
+        const float f = pow_of(g2, k.end - k.beg);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                R[d][r] *= f;
+    }
+
+    const unsigned lds0 = lds_addr(smem);
+    auto issue = [&](int n) {                             // the n-th tile from the end
+        const unsigned dst = lds0 + (n % kRing) * kSlot;
+        const int t0 = k.end - (n + 1) * C;
+        LK::issue(dst, kp, a->k_stride, t0, k.end, w, lane);
+        LV::issue(dst + SM::kK, vp, a->v_stride, t0, k.end, w, lane);
+    };
+    const unsigned bk = lds0 + BK::template col<true>(lane);
+    const unsigned bv = lds0 + (BV::template col<false>(lane) ^ (sizeof(T) == 2 ? (unsigned)w << 6 : (unsigned)w << 7));
+    auto tile = [&](int n, auto terms) {
+        // this wave's share of the tile has landed (the next one's loads are on their
+        // way), then everyone's has, and the tile before has been read
+        if (kRing == 3 && n + 1 < cnt)
+            wait_vmcnt<kRing == 3 ? kLoads : 0>();
+        else
+            wait_vmcnt<0>();
+        lds_barrier();
+        if (n + kRing - 1 < cnt)
+            issue(n + kRing - 1);
+        const unsigned ring = (unsigned)(n % kRing) * kSlot, b = opaque(bk) + ring, c = opaque(bv) + ring;
+        V vf[PT], kf[DB];
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+            vf[i] = BV::col_piece(SM::kK, c, i, 0);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+            kf[d] = BK::col_piece(0, b, 0, d);
+        const float f = pow_of(g2, (double)n * C);
+        update<T, DK, decltype(terms)::value>(R, b, vf, kf, [&](int i, int j) {
+            return f * *reinterpret_cast<const f32x4 *>(su + 2 * E * i + E * hh + 4 * j);
+        });
+    };
+    if (cnt > 0)
+        issue(0);
+    if (kRing == 3 && cnt > 1)
+        issue(1);
+    // tokens that the segment's end has forgotten below 2^-kForget take two terms
+    const int keep = sizeof(T) == 2 ? std::min(cnt, (int)std::min(1e6f, kForget / (1e-9f - g2f * (float)C)) + 1) : cnt;
+    int n = 0;
+    for (; n < keep; ++n)
+        tile(n, std::integral_constant<int, 3>());
+    for (; n < cnt; ++n)
+        tile(n, std::integral_constant<int, 2>());
+    store_slot<DK>(slot0 + k.seg * wslot, R);
+}
+
+// o over one segment of one (sequence, value head, column tile), and the end state
+// for a sequence's last segment.
 //
 // A wave owns 32 value columns: its dk x 32 slice of R stays in the result
 // registers and is the operand of the state product as it stands (contraction
 // over its rows), and the scores of a tile, the same for all columns, are shared
 // through LDS.  Outputs are formed transposed (columns x tokens): a lane holds
 // one token, so its power of lambda is one per-lane factor.
-template <typename T, int DK, int NW, bool kScan>
+template <typename T, int DK, int NW>
 __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void lin_scan_kernel(LinArgs args_in_kernarg)
 {
     typedef LinSmem<T, DK, NW> SM;
@@ -137,115 +332,69 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     constexpr int E = Piece<T>::E, PB = 16 / E;           // pieces per 32-row block
     constexpr int PT = C / (2 * E);                       // pieces over a tile's tokens
     typedef Tile<T, DK> TK;
-    typedef Tile<T, CT> TV;
     typedef Tile<T, C> TP;
     typedef LaneBase<T, DK> BK;
     typedef LaneBase<T, CT> BV;
     typedef LaneBase<T, C> BP;
     typedef typename Piece<T>::V V;
-    constexpr int kStores = kScan ? (sizeof(T) == 2 ? 2 : 4) : 0;   // per wave and tile
+    constexpr int kStores = sizeof(T) == 2 ? 2 : 4;       // per wave and tile
     extern __shared__ __align__(1024) unsigned char smem[];
     // after the ring: update weights of an epoch's tokens, lambda^-(i C + s + 1)
     // (direct: those of a tile, lambda^(C-1-s); the last C: a ragged tile's), and
     // lambda^(i C).  (All of it dynamic, so that the ring starts at LDS address 0 and
     // its offsets are immediates.)
-    float *su = reinterpret_cast<float *>(smem + (kScan ? SM::kScan : SM::kState));
+    float *su = reinterpret_cast<float *>(smem + SM::kScan);
     float *spow = su + (kEpochTiles + 1) * C;
 
     const LinArgsPtr a = (LinArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
     const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
     const int cl = lane & 31, hh = lane >> 5;
-
-    // value heads of a query/key head, and their column tiles, next to each other
-    // on one XCD: they read the same q and k
-    const unsigned nb = gridDim.x, per = nb / 8;
-    const unsigned bid = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
-    const int Hv = a->Hv, nct = a->dv / CT, hc = Hv * nct;
-    const int item = (int)(bid / (unsigned)hc), hx = (int)(bid % (unsigned)hc);
-    const int head = hx / nct, ct = hx % nct, hk = head / (Hv / a->Hk);
-    const int below = __popcll(__ballot(a->tab.pre[lane] <= item)) +
-                      __popcll(__ballot(a->tab.pre[64 + lane] <= item));
-    const int si = uniform_int(below - 1);
-    const int seg = item - a->tab.pre[si];
-    const int len = a->tab.len[si], T0 = a->seg_tokens;
-    const int nseg = std::max(1, (len + T0 - 1) / T0);
-    const int beg = seg * T0, end = std::min(len, beg + T0);
-    const int64_t sid = a->tab.id[si];
+    const Work k = work_of<CT>(a, lane);
+    const int seg = k.seg, nseg = k.nseg, beg = k.beg, end = k.end, head = k.head, T0 = a->seg_tokens;
+    const int Hv = a->Hv, dv = a->dv;
     const double g2 = std::max(a->g[head] * kLog2e, -1e5);
     const float g2f = (float)g2;
-    const int col0 = ct * CT + 32 * w;                    // the wave's first column of dv
-    const int dv = a->dv;
+    const int col0 = k.ct * CT + 32 * w;                  // the wave's first column of dv
 
-    const T *qp = (const T *)a->q + a->tab.tok[si] * a->q_stride + (int64_t)hk * DK;
-    const T *kp = (const T *)a->k + a->tab.tok[si] * a->k_stride + (int64_t)hk * DK;
-    const T *vp = (const T *)a->v + a->tab.tok[si] * a->v_stride + (int64_t)head * dv + ct * CT;
-    const int64_t sbase = (sid * Hv + head) * (int64_t)DK * dv + col0 + cl;   // of init and fin
-    const int64_t frag = (int64_t)DK * CT;                // floats of a slot's (head, column tile)
-    float *wsp = a->ws + (((int64_t)a->tab.slot[si] * Hv + head) * nct + ct) * frag +
-                 w * (DK * 32) + lane * 4;
-    const int64_t wslot = (int64_t)Hv * nct * frag;
+    const int64_t tok0 = a->tab.tok[k.si];
+    const T *qp = (const T *)a->q + tok0 * a->q_stride + (int64_t)k.hk * DK;
+    const T *kp = (const T *)a->k + tok0 * a->k_stride + (int64_t)k.hk * DK;
+    const T *vp = (const T *)a->v + tok0 * a->v_stride + (int64_t)head * dv + k.ct * CT;
+    const int64_t sbase = (a->tab.id[k.si] * (int64_t)Hv + head) * DK * dv + col0 + cl;   // of init and fin
+    const float *slot0 = a->ws + (((int64_t)a->tab.slot[k.si] * Hv + head) * (dv / CT) + k.ct) * ((int64_t)DK * CT) +
+                         w * (DK * 32) + lane * 4;
+    const int64_t wslot = (int64_t)Hv * DK * dv;          // floats between slots
 
-    f32x16 R[DB];
     // ---- the state entering the segment ----
-    const bool use_init = a->init != nullptr;
-    auto add_ws = [&](int j, float f) {                   // R += f times slot j
-        const float *p = wsp + j * wslot;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4 z = *reinterpret_cast<const f32x4 *>(p + (d * 4 + g) * 256);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    R[d][4 * g + e] = __builtin_fmaf(z[e], f, R[d][4 * g + e]);
-            }
-    };
-    auto to_ws = [&](int j, float f) {
-        float *p = wsp + j * wslot;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<f32x4 *>(p + (d * 4 + g) * 256) =
-                    f32x4{R[d][4 * g] * f, R[d][4 * g + 1] * f, R[d][4 * g + 2] * f, R[d][4 * g + 3] * f};
-    };
+    f32x16 R[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             R[d][r] = 0.f;
     if (seg == 0) {
-        if (kScan && a->copy_init && nseg > 1) {
-            add_ws(nseg - 1, 1.f);
-        } else if (use_init) {
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    R[d][r] = a->init[sbase + (int64_t)(32 * d + state_row<T>(r, hh)) * dv];
-        }
-        if (!kScan && a->copy_init)
-            to_ws(nseg - 1, 1.f);
-    } else if (kScan) {
+        if (a->copy_init && nseg > 1)
+            add_slot<DK>(R, slot0 + (nseg - 1) * wslot, 1.f);
+        else if (a->init)
+            load_state<T, DK>(R, a->init + sbase, dv, hh);
+    } else {
         // slot 0 holds the state after segment 0 (the initial one included), slot
         // j segment j's from zero; those forgotten below 2^-150 are left out
         int j = 0;
         while (j < seg - 1 && g2f * (float)T0 * (float)(seg - 1 - j) < -150.f)
             ++j;
         for (; j < seg; ++j)
-            add_ws(j, pow_of(g2, (double)T0 * (seg - 1 - j)));
+            add_slot<DK>(R, slot0 + j * wslot, pow_of(g2, (double)T0 * (seg - 1 - j)));
     }
 
     const unsigned lds0 = lds_addr(smem);
-    constexpr int kSlot = kScan ? SM::kScanSlot : SM::kStateSlot;
-    constexpr int kRing = SM::kRing;
+    constexpr int kSlot = SM::kScanSlot, kRing = SM::kRing;
     constexpr bool kAhead = kRing == 3;                   // scores are formed a tile ahead
     auto issue = [&](int t0, int slot) {
         const unsigned dst = lds0 + slot * kSlot;
         TileLoad<T, DK, C, NW>::issue(dst, kp, a->k_stride, t0, end, w, lane);
         TileLoad<T, CT, C, NW>::issue(dst + SM::kK, vp, a->v_stride, t0, end, w, lane);
-        if constexpr (kScan)
-            TileLoad<T, DK, C, NW>::issue(dst + SM::kK + SM::kV, qp, a->q_stride, t0, end, w, lane);
+        TileLoad<T, DK, C, NW>::issue(dst + SM::kK + SM::kV, qp, a->q_stride, t0, end, w, lane);
     };
 
     const bool direct = -g2f * (float)C > kEpoch || g2f > 0.f;   // scaled every tile
@@ -268,16 +417,14 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     constexpr int kBlk = 4 / NW;
     const int c16 = lane & 15, g16 = lane >> 4;
     float fp[kBlk][4];
-    if constexpr (kScan) {
 #pragma unroll
-        for (int j = 0; j < kBlk; ++j)
+    for (int j = 0; j < kBlk; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tb = (w * kBlk + j) >> 1, sb = (w * kBlk + j) & 1;
-                const int d = 16 * (tb - sb) + c16 - 4 * g16 - i;   // t - s
-                fp[j][i] = d < 0 ? 0.f : scale * exp2_fast(g2f * (float)d);
-            }
-    }
+        for (int i = 0; i < 4; ++i) {
+            const int tb = (w * kBlk + j) >> 1, sb = (w * kBlk + j) & 1;
+            const int d = 16 * (tb - sb) + c16 - 4 * g16 - i;       // t - s
+            fp[j][i] = d < 0 ? 0.f : scale * exp2_fast(g2f * (float)d);
+        }
     constexpr int kSp = TK::kChunks / 4;                  // pieces of a 16-row operand
     const unsigned bsk = BK::row16(c16, g16);             // the lane's offsets of each operand
     const unsigned bq = BK::row32(cl, hh), bk = BK::template col<true>(lane);
@@ -328,7 +475,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
         if (kAhead && beg + C < end)
             issue(beg + C, 1);
         wait_vmcnt<0>();
-        if constexpr (kScan && kAhead) {
+        if constexpr (kAhead) {
             lds_barrier();                                // (the tables are written, too)
             ScoreIn in;
             score_load(0, in);
@@ -337,7 +484,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     }
     T *const out = (T *)a->o;
     int n = 0, ep = 0, e = 0;                             // tiles done; S = lambda^e R, ep = e / C
-    int64_t orow = ((a->tab.tok[si] + beg) * Hv + head) * (int64_t)dv + col0;
+    int64_t orow = ((tok0 + beg) * Hv + head) * (int64_t)dv + col0;
     const unsigned ostride = (unsigned)(Hv * dv * (int)sizeof(T));
     const unsigned olane = (unsigned)cl * ostride + (sizeof(T) == 2 ? 16u : 16u) * (unsigned)hh;
 
@@ -399,55 +546,46 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
         f32x4 uw[E / 4];
         V pf[PT];
         f32x16 y = {};
-        float f = 0.f;
         const unsigned bvo = opaque(bv) + ring;
 #pragma unroll
         for (int i = 0; i < PT; ++i)
             vf[i] = BV::col_piece(SM::kK, bvo, i, 0);
-        auto load_k = [&](int i) {
-            const unsigned b = opaque(bk) + ring;
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-                kf[d] = BK::col_piece(0, b, i, d);
+        const unsigned bko = opaque(bk) + ring;
+        auto weight4 = [&](int i, int j) {
+            return *reinterpret_cast<const f32x4 *>(su + ub + 2 * E * i + E * hh + 4 * j);
         };
-        auto load_u = [&](int i) {
+        // the (next) tile's scores (past the last tile: of whatever is there, not
+        // used) and the state's part
+        ScoreIn in;
+        score_load(kAhead ? next : slot, in);
+        constexpr bool kHold = DK <= 128 && NW == 4;
+        V qf[kHold ? TK::kPieces : 1];
+        const unsigned bqo = opaque(bq) + ring;
+        if constexpr (kHold)
 #pragma unroll
-            for (int j = 0; j < E / 4; ++j)
-                uw[j] = *reinterpret_cast<const f32x4 *>(su + ub + 2 * E * i + E * hh + 4 * j);
-        };
-        if constexpr (kScan) {
-            // the (next) tile's scores (past the last tile: of whatever is there, not
-            // used) and the state's part
-            ScoreIn in;
-            score_load(kAhead ? next : slot, in);
-            constexpr bool kHold = DK <= 128;
-            V qf[kHold ? TK::kPieces : 1];
-            const unsigned bqo = opaque(bq) + ring;
-            if constexpr (kHold)
+            for (int i = 0; i < TK::kPieces; ++i)
+                qf[i] = BK::piece32(SM::kK + SM::kV, bqo, i);
+        const float f = ft * spow[ep];
+        step();
+        score_store(kAhead ? next : slot, in);
 #pragma unroll
-                for (int i = 0; i < TK::kPieces; ++i)
-                    qf[i] = BK::piece32(SM::kK + SM::kV, bqo, i);
-            f = ft * spow[ep];
-            step();
-            score_store(kAhead ? next : slot, in);
-            load_u(0);
-            load_k(0);
-            if constexpr (!kAhead)
-                lds_barrier();
+        for (int j = 0; j < E / 4; ++j)
+            uw[j] = weight4(0, j);
 #pragma unroll
-            for (int i = 0; i < PT; ++i)
-                pf[i] = BP::piece32(kRing * kSlot, opaque(bp) + pring, i);
+        for (int d = 0; d < DB; ++d)
+            kf[d] = BK::col_piece(0, bko, 0, d);
+        if constexpr (!kAhead)
+            lds_barrier();
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+        for (int i = 0; i < PT; ++i)
+            pf[i] = BP::piece32(kRing * kSlot, opaque(bp) + pring, i);
 #pragma unroll
-                for (int i = 0; i < PB; ++i)
-                    y = mma(acc_piece(R[d], i, (const T *)nullptr),
-                            kHold ? qf[kHold ? d * PB + i : 0] : BK::piece32(SM::kK + SM::kV, bqo, d * PB + i), y);
-            step();
-        } else {
-            load_u(0);
-            load_k(0);
-        }
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < PB; ++i)
+                y = mma(acc_piece(R[d], i, (const T *)nullptr),
+                        kHold ? qf[kHold ? d * PB + i : 0] : BK::piece32(SM::kK + SM::kV, bqo, d * PB + i), y);
+        step();
 
         // the state update (issued ahead of the other wave of the SIMD)
         __builtin_amdgcn_s_setprio(1);
@@ -459,65 +597,42 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
                 for (int r = 0; r < 16; ++r)
                     R[d][r] *= fd;
         }
-#pragma unroll
-        for (int i = 0; i < PT; ++i) {
-            if constexpr (sizeof(T) == 2) {
-                V x[kTerms];
-                weigh(vf[i], uw[0], uw[1], x);
-#pragma unroll
-                for (int j = 0; j < kTerms; ++j)
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        R[d] = mma(kf[d], x[j], R[d]);
-            } else {
-                const V x = vf[i] * uw[0];
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-                    R[d] = mma(kf[d], x, R[d]);
-            }
-            if (i + 1 < PT) {
-                load_u(i + 1);
-                load_k(i + 1);
-            }
-        }
+        update<T, DK, kTerms>(R, bko, vf, kf, [&](int i, int j) { return i == 0 ? uw[j] : weight4(i, j); });
 
-        if constexpr (kScan) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                y[r] *= f;
+        for (int r = 0; r < 16; ++r)
+            y[r] *= f;
 #pragma unroll
-            for (int i = 0; i < PT; ++i)
-                y = mma(vf[i], pf[i], y);
-            // stores through a descriptor that ends at the segment's last row: always the
-            // same number of store instructions (see the wait above); a row past the last
-            // lies past the descriptor's end whatever the column
-            const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
-                out + orow, (short)0, (int)((unsigned)(rows - 1) * ostride + 32 * (unsigned)sizeof(T)),
-                0x00020000);
-            if constexpr (sizeof(T) == 2) {
+        for (int i = 0; i < PT; ++i)
+            y = mma(vf[i], pf[i], y);
+        // stores through a descriptor that ends at the segment's last row: always the
+        // same number of store instructions (see the wait above); a row past the last
+        // lies past the descriptor's end whatever the column
+        const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
+            out + orow, (short)0, (int)((unsigned)(rows - 1) * ostride + 32 * (unsigned)sizeof(T)), 0x00020000);
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                for (int g = 0; g < 4; g += 2) {
-                    unsigned out[4];
+            for (int g = 0; g < 4; g += 2) {
+                unsigned o4[4];
 #pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        const auto sw = __builtin_amdgcn_permlane32_swap(
-                            pack_bf16(y[4 * g + 2 * h2], y[4 * g + 2 * h2 + 1]),
-                            pack_bf16(y[4 * g + 4 + 2 * h2], y[4 * g + 5 + 2 * h2]), false, false);
-                        out[h2] = sw[0];
-                        out[2 + h2] = sw[1];
-                    }
-                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{out[0], out[1], out[2], out[3]}, orr,
-                                                           olane + 16u * (unsigned)g, 0, 0);
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    const auto sw = __builtin_amdgcn_permlane32_swap(
+                        pack_bf16(y[4 * g + 2 * h2], y[4 * g + 2 * h2 + 1]),
+                        pack_bf16(y[4 * g + 4 + 2 * h2], y[4 * g + 5 + 2 * h2]), false, false);
+                    o4[h2] = sw[0];
+                    o4[2 + h2] = sw[1];
                 }
-            } else {
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    __builtin_amdgcn_raw_buffer_store_b128(
-                        __builtin_bit_cast(u32x4, f32x4{y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]}),
-                        orr, olane + 32u * (unsigned)g, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{o4[0], o4[1], o4[2], o4[3]}, orr,
+                                                       olane + 16u * (unsigned)g, 0, 0);
             }
-            orow += (int64_t)C * Hv * dv;
+        } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    __builtin_bit_cast(u32x4, f32x4{y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]}), orr,
+                    olane + 32u * (unsigned)g, 0, 0);
         }
+        orow += (int64_t)C * Hv * dv;
         __builtin_amdgcn_s_setprio(0);
         if constexpr (!kDirect) {
             ++ep;
@@ -536,47 +651,39 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     } else {
         // tokens that the end of the segment's state has forgotten below 2^-kForget
         // take two terms
-        const int keep = kScan && seg < nseg - 1 ? 0 : (int)std::min(1e6f, kForget / (1e-9f - g2f * (float)C)) + 1;
+        const int keep = seg < nseg - 1 ? 0 : (int)std::min(1e6f, kForget / (1e-9f - g2f * (float)C)) + 1;
         if constexpr (sizeof(T) == 2)
             tiles(std::integral_constant<int, 2>(), ntile - keep);
         tiles(std::integral_constant<int, 3>(), ntile);
     }
-    const float fe = pow_of(g2, e);
-
-    if constexpr (kScan) {
-        if (seg == nseg - 1) {
+    if (seg == nseg - 1) {
+        const float fe = pow_of(g2, e);
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    a->fin[sbase + (int64_t)(32 * d + state_row<T>(r, hh)) * dv] = R[d][r] * fe;
-        }
-    } else {
-        to_ws(seg, fe);
+            for (int r = 0; r < 16; ++r)
+                a->fin[sbase + (int64_t)(32 * d + state_row<T>(r, hh)) * dv] = R[d][r] * fe;
     }
 }
 
-template <typename T, int DK, int NW, bool kScan>
-hipError_t launch_part(const LinArgs &args, int64_t items, hipStream_t s)
+hipError_t launch_part(void (*kernel)(LinArgs), int threads, int smem, std::atomic<uint64_t> &allowed,
+                       const LinArgs &args, int64_t groups, hipStream_t s)
 {
-    typedef LinSmem<T, DK, NW> SM;
-    constexpr int kSmem = (kScan ? SM::kScan : SM::kState) + SM::kTables;
-    static_assert(kSmem <= 160 * 1024, "LDS of a CU");
-    static std::atomic<uint64_t> allowed{0};
-    const hipError_t e =
-        allow_lds(reinterpret_cast<const void *>(&lin_scan_kernel<T, DK, NW, kScan>), kSmem, allowed);
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), smem, allowed);
     if (e != hipSuccess)
         return e;
-    const int64_t grid = items * args.Hv * (args.dv / (32 * NW));
-    lin_scan_kernel<T, DK, NW, kScan><<<dim3((unsigned)grid), dim3(64 * NW), kSmem, s>>>(args);
+    kernel<<<dim3((unsigned)groups), dim3(threads), smem, s>>>(args);
     return hipGetLastError();
 }
 
 template <typename T, int DK, int NW>
 hipError_t scan(LinArgs &args, int64_t nseq, const LinSeq *seqs, hipStream_t s)
 {
-    const int64_t T0 = args.seg_tokens;
-    const int64_t most = INT32_MAX / ((int64_t)args.Hv * (args.dv / (32 * NW)));
+    typedef LinSmem<T, DK, NW> SM;
+    static_assert(SM::kScan + SM::kTables <= 160 * 1024, "LDS of a CU");
+    static std::atomic<uint64_t> allow_state{0}, allow_scan{0};
+    const int64_t T0 = args.seg_tokens, groups = (int64_t)args.Hv * (args.dv / (32 * NW));
+    const int64_t most = INT32_MAX / groups;
     int64_t slot = 0;
     for (int64_t at = 0; at < nseq;) {
         int n = 0;
@@ -607,8 +714,10 @@ hipError_t scan(LinArgs &args, int64_t nseq, const LinSeq *seqs, hipStream_t s)
                 if (i < n)
                     sum += pass == 0 ? segs[i] - 1 : segs[i];
             }
-            e = pass == 0 ? launch_part<T, DK, NW, false>(args, states, s)
-                          : launch_part<T, DK, NW, true>(args, items, s);
+            e = pass == 0 ? launch_part(&lin_state_kernel<T, DK, NW>, 64 * NW, SM::kState + SM::C * 4, allow_state,
+                                        args, states * groups, s)
+                          : launch_part(&lin_scan_kernel<T, DK, NW>, 64 * NW, SM::kScan + SM::kTables, allow_scan,
+                                        args, items * groups, s);
             if (e != hipSuccess)
                 return e;
         }
