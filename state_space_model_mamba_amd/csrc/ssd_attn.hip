@@ -23,10 +23,19 @@ using namespace mx;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;
-constexpr float kNoMax = -1e30f;   // m before the first visible key (finite: m - m is 0)
+constexpr float kNoMax = -3e38f;   // m before the first visible key (finite: m - m is 0)
 // A scale of 0 weights all visible keys alike; it is kept off 0 so that a masked
 // score (-inf) times it stays -inf.
 constexpr float kTinyScale = 1.17549435e-38f;
+
+// s c - m, the product rounded before the difference as it is in m: for the largest
+// score of a row exactly 0 however large it is.  (Fused, the rounding of m remains;
+// the row's weights have it in common, but past 2^30 it overflows the exponential.)
+__device__ __forceinline__ float below_max(float s, float c, float m)
+{
+#pragma clang fp contract(off)
+    return s * c - m;
+}
 
 // A 32-key tile in a wave's own LDS, for 32 rows (score columns): updates (m, l,
 // acc).  Keys from `see` (per lane) on are masked if `masked` (wave-uniform).
@@ -67,7 +76,7 @@ __device__ __forceinline__ void tile32(const unsigned char *Kt, const unsigned c
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        s[r] = exp2_fast(__builtin_fmaf(s[r], c, -m));
+        s[r] = exp2_fast(below_max(s[r], c, m));
         l += s[r];
     }
 #pragma unroll
@@ -144,10 +153,19 @@ __device__ __forceinline__ void join_waves(unsigned char *smem, float (&sm)[Wave
 // ---------------------------------------------------------------------------
 // Rows of a sequence are its (token, head of the group) pairs, token-major, so
 // that all query heads of a key head share its K and V tiles and short prompts
-// still fill the 32-row blocks.  A work-group takes kRows consecutive rows, one
-// 32-row block per wave and qb; the scores are formed transposed (keys x rows):
-// a lane then holds one row, its statistics are per-lane scalars, and the
-// probabilities are the second product's operand as they stand.
+// still fill the 32-row blocks.  A work-group takes kRows consecutive rows, 32 per
+// wave; the scores are formed transposed (keys x rows): a lane then holds one row,
+// its statistics are per-lane scalars, and the probabilities are the second
+// product's operand as they stand.  K and V tiles go from memory straight into two
+// LDS slots, a tile ahead.
+//
+// Bound by the matrix and vector units: one prompt of 8192 tokens, 32 heads over 8
+// of 128 in bf16, takes 500 - 530 us, 1.04 - 1.10 PFLOP/s; a large library product
+// (8192 x 8192 x 8192) reaches 1.20 on the same card.  The matrix units are busy 48%
+// of the time and the vector units 44%.  Tried and no faster: the eight waves'
+// pairs staggered by half a tile (554 us), 64 rows per wave with the two blocks'
+// steps interleaved in one stream (729 us: registers spill), raised priority
+// around the products (545), the K operands of a tile read together (510).
 struct SeqTab {
     static constexpr int kMax = 120;          // sequences per launch (kernel arguments: 4 KB)
     AttnSeq seq[kMax];
@@ -177,18 +195,16 @@ template <> __device__ __forceinline__ f32x4 flip<float>(f32x4 v)
     return -v;
 }
 
-template <typename T, int D, int NW, int QB>
-__global__ __launch_bounds__(64 * NW, QB == 1 && D <= 128 ? 2 : 1) void attn_prefill_kernel(
+template <typename T, int D, int NW>
+__global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void attn_prefill_kernel(
     PrefillArgs args_in_kernarg)
 {
-    constexpr int KT = sizeof(T) == 2 ? 64 : 32;      // keys per tile
+    constexpr int KT = sizeof(T) == 2 ? 64 : 32;          // keys per tile
     constexpr int KB = KT / 32, DB = D / 32;
-    constexpr int E = Piece<T>::E;
-    constexpr int PC = 16 / E * 2 / 2;                // pieces per 32-key block of P
-    constexpr int kRows = 32 * QB * NW;
+    constexpr int E = Piece<T>::E, PC = 16 / E;           // pieces per 32-key block of P
+    constexpr int kRows = 32 * NW;
     typedef Tile<T, D> TL;
     typedef typename Piece<T>::V V;
-    static_assert(PC * 2 * E == 32, "pieces of a 32-row block");
     constexpr int kTileBytes = KT * TL::kPitch;
     extern __shared__ __align__(1024) unsigned char smem[];   // [2][K tile, V tile]
 
@@ -212,30 +228,22 @@ __global__ __launch_bounds__(64 * NW, QB == 1 && D <= 128 ? 2 : 1) void attn_pre
     const T *kp = (const T *)a->k + a->tab.seq[si].k0 * a->k_stride + (int64_t)hk * D;
     const T *vp = (const T *)a->v + a->tab.seq[si].k0 * a->v_stride + (int64_t)hk * D;
 
-    int64_t orow[QB];         // the lane's output row, in units of D elements
-    bool valid[QB];
-    int lim[QB];              // keys the lane's row sees
-    V qf[QB][TL::kPieces];
+    const int64_t row = row0 + w * 32 + cl;
+    const bool valid = row < nrow;
+    const unsigned rr = (unsigned)(valid ? row : nrow - 1);
+    const unsigned tok = rr / (unsigned)grp, head = hk * grp + rr % (unsigned)grp;
+    const int64_t qt = a->tab.seq[si].q0 + tok;
+    const int lim = valid ? std::max(0, lk - lq + (int)tok + 1) : 0;   // keys the lane's row sees
+    V qf[TL::kPieces];
+    const T *qp = (const T *)a->q + qt * a->q_stride + (int64_t)head * D;
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-        const int64_t r = row0 + (w * QB + b) * 32 + cl;
-        valid[b] = r < nrow;
-        const unsigned rr = (unsigned)(valid[b] ? r : nrow - 1);
-        const unsigned t = rr / (unsigned)grp, h = hk * grp + rr % (unsigned)grp;
-        const int64_t qt = a->tab.seq[si].q0 + t;
-        orow[b] = qt * a->Hq + h;
-        lim[b] = valid[b] ? std::max(0, lk - lq + (int)t + 1) : 0;
-        const T *qp = (const T *)a->q + qt * a->q_stride + (int64_t)h * D;
-#pragma unroll
-        for (int p = 0; p < TL::kPieces; ++p) {
-            qf[b][p] = *reinterpret_cast<const V *>(qp + (2 * p + hh) * E);
-            if (a->neg)
-                qf[b][p] = flip<T>(qf[b][p]);
-        }
+    for (int p = 0; p < TL::kPieces; ++p) {
+        qf[p] = *reinterpret_cast<const V *>(qp + (2 * p + hh) * E);
+        if (a->neg)
+            qf[p] = flip<T>(qf[p]);
     }
     // keys that any / every row of the wave sees, and any row of the work-group
-    const int64_t wlast = std::min<int64_t>(nrow, row0 + (w + 1) * 32 * QB) - 1;
-    const int64_t wfirst = row0 + (int64_t)w * 32 * QB;
+    const int64_t wfirst = row0 + (int64_t)w * 32, wlast = std::min<int64_t>(nrow, wfirst + 32) - 1;
     const int wmax = wfirst >= nrow ? 0 : std::max(0, lk - lq + (int)((unsigned)wlast / (unsigned)grp) + 1);
     const int wmin = std::max(0, lk - lq + (int)((unsigned)wfirst / (unsigned)grp) + 1);
     const int64_t glast = std::min<int64_t>(nrow, row0 + kRows) - 1;
@@ -243,14 +251,8 @@ __global__ __launch_bounds__(64 * NW, QB == 1 && D <= 128 ? 2 : 1) void attn_pre
     const int ntile = uniform_int((gmax + KT - 1) / KT);
     const float c = a->c;
 
-    f32x16 acc[DB][QB] = {};
-    float m[QB], l[QB];
-#pragma unroll
-    for (int b = 0; b < QB; ++b) {
-        m[b] = kNoMax;
-        l[b] = 0.f;
-    }
-
+    f32x16 acc[DB] = {};
+    float m = kNoMax, l = 0.f;
     const unsigned lds0 = lds_addr(smem);
     auto issue = [&](int n) {
         const unsigned dst = lds0 + (n & 1) * 2 * kTileBytes;
@@ -269,93 +271,88 @@ __global__ __launch_bounds__(64 * NW, QB == 1 && D <= 128 ? 2 : 1) void attn_pre
             continue;
         const unsigned char *Kt = smem + (n & 1) * 2 * kTileBytes, *Vt = Kt + kTileBytes;
 
-        f32x16 s[KB][QB] = {};
+        f32x16 s[KB] = {};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int p = 0; p < TL::kPieces; ++p) {
-                const V kf = TL::row_nat(Kt, kb * 32 + cl, p, hh);
-#pragma unroll
-                for (int b = 0; b < QB; ++b)
-                    s[kb][b] = mma(kf, qf[b][p], s[kb][b]);
-            }
+            for (int p = 0; p < TL::kPieces; ++p)
+                s[kb] = mma(TL::row_nat(Kt, kb * 32 + cl, p, hh), qf[p], s[kb]);
         if ((n + 1) * KT > wmin) {
-#pragma unroll
-            for (int b = 0; b < QB; ++b) {
-                const int see = lim[b] - n * KT - 4 * hh;
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (32 * kb + 8 * (r >> 2) + (r & 3) >= see)
-                            s[kb][b][r] = -__builtin_inff();
-            }
-        }
-        V pf[KB * PC][QB];
-#pragma unroll
-        for (int b = 0; b < QB; ++b) {
-            float t = s[0][b][0];
+            const int see = lim - n * KT - 4 * hh;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    t = fmaxf(t, s[kb][b][r]);
-            t = half_max(t) * c;
-            if (__any(t > m[b] + kSlack)) {
-                const float mn = fmaxf(m[b], t);
-                const float al = exp2_fast(m[b] - mn);
-                m[b] = mn;
-                l[b] *= al;
+                    if (32 * kb + 8 * (r >> 2) + (r & 3) >= see)
+                        s[kb][r] = -__builtin_inff();
+        }
+        float t = s[0][0];
 #pragma unroll
-                for (int d = 0; d < DB; ++d)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        acc[d][b][r] *= al;
+            for (int r = 0; r < 16; ++r)
+                t = fmaxf(t, s[kb][r]);
+        t = half_max(t) * c;
+        if (__any(t > m + kSlack)) {
+            const float mn = fmaxf(m, t), al = exp2_fast(m - mn);
+            m = mn;
+            l *= al;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc[d][r] *= al;
+        }
+        // the exponents as one fused operation each (3% of the kernel's time), but for
+        // huge scores
+        float ec = c, em = m;
+        if (__any(fabsf(m) > 16777216.f && m != kNoMax)) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[kb][r] = below_max(s[kb][r], c, m);
+            ec = 1.f;
+            em = 0.f;
+        }
+        V pf[KB * PC];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float e = exp2_fast(__builtin_fmaf(s[kb][r], ec, -em));
+                l += e;
+                s[kb][r] = e;
             }
+            // the probabilities are rounded to the operand type once, unnormalised
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float e = exp2_fast(__builtin_fmaf(s[kb][b][r], c, -m[b]));
-                    l[b] += e;
-                    s[kb][b][r] = e;
-                }
-                // the probabilities are rounded to the operand type once, unnormalised
-#pragma unroll
-                for (int p = 0; p < PC; ++p)
-                    pf[kb * PC + p][b] = acc_piece(s[kb][b], p, (const T *)nullptr);
-            }
+            for (int p = 0; p < PC; ++p)
+                pf[kb * PC + p] = acc_piece(s[kb], p, (const T *)nullptr);
         }
 #pragma unroll
         for (int p = 0; p < KB * PC; ++p)
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const V vf = TL::col_acc(Vt, p, 32 * d, lane);
-#pragma unroll
-                for (int b = 0; b < QB; ++b)
-                    acc[d][b] = mma(vf, pf[p][b], acc[d][b]);
-            }
+            for (int d = 0; d < DB; ++d)
+                acc[d] = mma(TL::col_acc(Vt, p, 32 * d, lane), pf[p], acc[d]);
     }
 
+    const float tot = half_sum(l);
+    const float inv = tot > 0.f ? 1.f / tot : 0.f;
+    T *op = (T *)a->o + (qt * a->Hq + head) * D;
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-        const float tot = half_sum(l[b]);
-        const float inv = tot > 0.f ? 1.f / tot : 0.f;
-        T *op = (T *)a->o + orow[b] * D;
+    for (int d = 0; d < DB; ++d) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                acc[d][b][r] *= inv;
-            store_row(op, 32 * d, hh, valid[b], acc[d][b]);
-        }
+        for (int r = 0; r < 16; ++r)
+            acc[d][r] *= inv;
+        store_row(op, 32 * d, hh, valid, acc[d]);
     }
 }
 
 // Few rows (short prompts, or few heads): 32 rows per work-group, the waves taking
 // every kWaves-th 32-key tile of them, each with its own running (m, l, acc), joined
 // at the end.  A work-group then walks its keys in a quarter of the steps, and eight
-// times as many share the chip.
+// times as many share the chip; bound by each work-group's chain of steps, about 1.3
+// us each (figures at the rule that chooses it).
 template <typename T, int D>
 __global__ __launch_bounds__((64 * WaveTiles<T, D>::kWaves), 1) void attn_prefill_few_kernel(
     PrefillArgs args_in_kernarg)
@@ -494,7 +491,7 @@ hipError_t prefill(PrefillArgs &args, int64_t nseq, const AttnSeq *seqs, hipStre
         return prefill_launch(&attn_prefill_few_kernel<T, D>, 32, 64 * WaveTiles<T, D>::kWaves,
                               WaveTiles<T, D>::kSmem, allowed_few, args, nseq, seqs, s);
     constexpr unsigned kSmem = 4u * (sizeof(T) == 2 ? 64 : 32) * D * sizeof(T);
-    return prefill_launch(&attn_prefill_kernel<T, D, NW, 1>, kRows, 64 * NW, kSmem, allowed, args, nseq, seqs, s);
+    return prefill_launch(&attn_prefill_kernel<T, D, NW>, kRows, 64 * NW, kSmem, allowed, args, nseq, seqs, s);
 }
 
 // ---------------------------------------------------------------------------

@@ -6,21 +6,33 @@
 // Over a tile of n tokens entered with state S (t, s = 0 .. n - 1):
 //     o_t = scale (lambda^(t+1) S^T q_t + sum_{s<=t} lambda^(t-s) (q_t . k_s) v_s)
 //     S  <- lambda^n S + sum_s lambda^(n-1-s) k_s v_s^T
-// The decay is the same for every token, so the state is kept as R with
+// The decay is the same for every token, so the scan keeps the state as R with
 // S = lambda^e R, e the tokens since the last rescale: a tile then adds
-// lambda^-(e+s+1) k_s v_s^T to R without touching the rest of it, and R is
-// multiplied by lambda^e only when that falls below 2^-kEpoch (kEpoch = 24: the
-// weights stay within 2^24, and rescales, whose rounding would add up over the
-// tiles of a slowly forgetting head, are a memory length apart).  A head that
-// forgets faster than 2^-kEpoch within a tile is scaled every tile instead.
-// Powers of lambda are formed from the exponent in fp64 (fp32 would be off by
-// up to kEpoch 2^-24 relative).
+// lambda^-(e+s+1) k_s v_s^T to R without touching the rest of it, with weights from
+// a table, and R is multiplied by lambda^e once per epoch: every kEpochTiles tiles,
+// or sooner, before the weights would pass 2^kEpoch.  A head that forgets more than
+// that within a tile is scaled every tile instead.  Powers of lambda are formed from
+// the exponent in fp64 (in fp32 they would be off by up to kEpoch 2^-24 relative).
 //
 // Rounding (bf16): q, k, v are exact operands.  The state and the masked scores
 // are each rounded once to bf16 on their way into the products that form o
 // (each about as large as the rounding of o itself); the state update takes
 // lambda^.. v as the sum of three bf16 numbers, which hold an fp32 product
-// whole: the fp32 state keeps fp32 accuracy (two left it 2.5e-6 off, relative).
+// whole, so that the end state keeps fp32 accuracy (two leave it 2.5e-6 off,
+// relative), or of two where the end state has forgotten the tokens below
+// 2^-kForget, or none is wanted.
+//
+// Bound by memory: q, k, v and o move once in the scan; a sequence cut into
+// segments, to fill the chip, has all but its last segment's k and v read a second
+// time by the state kernel.  4 x 8192 tokens of 32 heads of 128 x 128 over 16 (bf16,
+// 4 segments): 250 - 256 us in all, the scan 135 - 165 us of it for 814 MB (a copy
+// moves 4.8 TB/s on the same card: 170 us; part of k and v is still in the
+// memory-side cache), the state kernel 80 us.  What the scan needed for that: two
+// work-groups per CU (32-token tiles; 64-token ones left room for one, 450 us in
+// all), every wave forming a share of the next tile's scores (338 us before), no
+// register spilled inside the loop (a spill's reload waits for the tiles on their
+// way: 2 to 3 times slower), few vector instructions beside the products (one base
+// register per LDS operand, weights from a table).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -37,7 +49,7 @@ using namespace mx;
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kEpoch = 60.f;
 constexpr int kEpochTiles = 8;
-constexpr float kForget = 4.f;
+constexpr float kForget = 4.f;                // 2.5e-6 times 2^-4 is fp32's own rounding
 
 struct LinTab {
     static constexpr int kMax = 96;           // sequences per launch (kernel arguments: 4 KB)
@@ -249,7 +261,9 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     if (tid < C)
         su[tid] = pow_of(g2, C - 1 - tid);
     // tiles that count: lambda^(n C) >= 2^-150
-    const int cnt = g2f * (float)C * (float)ntile > -150.f ? ntile : std::min(ntile, (int)(-150.f / (g2f * (float)C)) + 1);
+    const int cnt = g2f * (float)C * (float)ntile < -150.f
+                        ? std::max(1, std::min(ntile, (int)std::min(1e6f, -150.f / (g2f * (float)C)) + 1))
+                        : ntile;
     f32x16 R[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -306,7 +320,9 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     if (kRing == 3 && cnt > 1)
         issue(1);
     // tokens that the segment's end has forgotten below 2^-kForget take two terms
-    const int keep = sizeof(T) == 2 ? std::min(cnt, (int)std::min(1e6f, kForget / (1e-9f - g2f * (float)C)) + 1) : cnt;
+    const int keep = sizeof(T) == 2 && g2f <= 0.f
+                         ? std::min(cnt, (int)std::min(1e6f, kForget / (1e-9f - g2f * (float)C)) + 1)
+                         : cnt;
     int n = 0;
     for (; n < keep; ++n)
         tile(n, std::integral_constant<int, 3>());
@@ -398,7 +414,8 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     };
 
     const bool direct = -g2f * (float)C > kEpoch || g2f > 0.f;   // scaled every tile
-    const int epoch = direct ? 0 : std::min(kEpochTiles, (int)(kEpoch / (1e-9f - g2f * (float)C)));
+    const int epoch =
+        direct ? 0 : std::max(1, (int)std::min((float)kEpochTiles, kEpoch / (1e-9f - g2f * (float)C)));
     // what R is multiplied by when it is rescaled, to more than fp32
     float fhi = pow_of(g2, C * (direct ? 1 : epoch)), flo = 0.f;
     if (epoch == kEpochTiles) {
@@ -486,7 +503,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     int n = 0, ep = 0, e = 0;                             // tiles done; S = lambda^e R, ep = e / C
     int64_t orow = ((tok0 + beg) * Hv + head) * (int64_t)dv + col0;
     const unsigned ostride = (unsigned)(Hv * dv * (int)sizeof(T));
-    const unsigned olane = (unsigned)cl * ostride + (sizeof(T) == 2 ? 16u : 16u) * (unsigned)hh;
+    const unsigned olane = (unsigned)cl * ostride + 16u * (unsigned)hh;
 
     // one tile; mode 0: the head is scaled every tile, else the bf16 terms of the
     // update's weighted values
@@ -740,7 +757,8 @@ hipError_t scan_cols(int cols, LinArgs &args, int64_t nseq, const LinSeq *seqs, 
 // A work-group takes CT columns of one value head's state: each lane four
 // consecutive columns of DK / (4 RPI) rows.  The state is read once and written
 // once; every element is updated, stored, and added to its column's output sum
-// from the same register.
+// from the same register.  Bound by memory: 256 sequences of 32 heads of 128 x 128
+// (1.08 GB) in 184 us, 5.9 TB/s.
 constexpr int kStepThreads = 256;
 // State above the 256 MB memory-side cache streams through HBM on every step:
 // its accesses carry non-temporal hints; a smaller one stays cache-resident.
@@ -824,7 +842,8 @@ hipError_t step(int64_t B, int64_t Hk, int64_t Hv, int64_t dv, int64_t qs, int64
                 float scale, const void *q, const void *k, const void *v, const float *g, float *state,
                 void *o, hipStream_t s)
 {
-    // few heads: narrow column tiles, so that more work-groups share the state
+    // few heads: narrow column tiles, so that more work-groups share the state (32
+    // heads of 128 x 128: 3.4 us)
     const bool nt = B * Hv * DK * dv * 4 > kStepNTBytes;
     const int ct = B * Hv * (dv / 64) >= 1024 ? 64 : 32;
     const dim3 grid((unsigned)(B * Hv * (dv / ct)));

@@ -111,18 +111,6 @@ template <typename T, int D> struct Tile {
     {
         return *reinterpret_cast<const typename Piece<T>::V *>(t + off(row, 2 * p + hh));
     }
-    // operand over the columns, accumulator order
-    static __device__ __forceinline__ typename Piece<T>::V row_acc(const unsigned char *t, int row,
-                                                                   int p, int hh)
-    {
-        if constexpr (sizeof(T) == 4) {
-            return row_nat(t, row, p, hh);
-        } else {
-            const bf16x4 lo = *reinterpret_cast<const bf16x4 *>(t + off(row, 2 * p) + 8 * hh);
-            const bf16x4 hi = *reinterpret_cast<const bf16x4 *>(t + off(row, 2 * p + 1) + 8 * hh);
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-    }
     // operand over the rows (transposed), accumulator order: column col0 + lane % 32.
     // bf16 through the transpose read: within 16 lanes, lane i gets element i % 4
     // of the 8 bytes that lanes i / 4, i / 4 + 4, .. + 12 address (one per row), so
@@ -185,7 +173,12 @@ template <typename T, int D> struct LaneBase {
     {
         return at(t, base ^ ((unsigned)p << 6));
     }
-    // transposed operand (see col_nat): block d of 32 columns, piece p of the rows
+    // transposed operand, natural order (bf16): rows 16 p + 8 hh + e of column
+    // 32 d + lane % 32, or with kPerm of the column that makes a result's register
+    // 8 j + i of lane half hh stand for column 16 j + 8 hh + i (so that the result, as
+    // an operand, meets a natural-order operand: in each 16 columns the middle two
+    // groups of four trade places).  fp32: the accumulator order is the natural one,
+    // and register r stands for column 8 (r / 4) + 4 hh + r % 4.
     template <bool kPerm> static __device__ __forceinline__ unsigned col(int lane)
     {
         if constexpr (sizeof(T) == 4) {
@@ -219,30 +212,6 @@ template <typename T, int D> struct LaneBase {
     }
 };
 
-// Transposed operands in the natural order, for bf16: rows 16 p + 8 hh + e of
-// column col0 + lane % 32, or with kPerm of the column that makes a result's
-// register 8 j + i of lane half hh stand for column 16 j + 8 hh + i (so that the
-// result, as an operand, meets a natural-order operand: in each 16 columns the
-// middle two groups of four trade places).  fp32: the accumulator order is the
-// natural one, and the register r stands for column 8 (r / 4) + 4 hh + r % 4.
-template <typename T, int D, bool kPerm>
-__device__ __forceinline__ typename Piece<T>::V col_nat(const unsigned char *t, int p, int col0, int lane)
-{
-    typedef Tile<T, D> TL;
-    if constexpr (sizeof(T) == 4) {
-        return TL::col_acc(t, p, col0, lane);
-    } else {
-        const int row = 16 * p + 8 * (lane >> 5) + ((lane >> 2) & 3);
-        const int q = lane & 3, g4 = kPerm ? ((q & 1) << 1) | (q >> 1) : q;
-        const int col = col0 + 16 * ((lane >> 4) & 1) + 4 * g4;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4 *)(t + TL::off(row, col >> 3) + (col & 7) * 2));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4 *)(t + TL::off(row + 4, col >> 3) + (col & 7) * 2));
-        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    }
-}
-
 __device__ __forceinline__ float exp2_fast(float v)
 {
     return __builtin_amdgcn_exp2f(v);
@@ -252,13 +221,6 @@ __device__ __forceinline__ int uniform_int(int v)
 {
     return __builtin_amdgcn_readfirstlane(v);
 }
-__device__ __forceinline__ int64_t uniform_i64(int64_t v)
-{
-    const unsigned lo = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)v);
-    const unsigned hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(v >> 32));
-    return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
 // Maximum / sum of a value and the one the lane 32 away holds, kept by both.
 // (The second result of the swap goes through an empty asm statement: read by
 // one instruction directly, the two have been taken for the same register.)

@@ -42,7 +42,7 @@ def test_head_layouts(io, hq, hkv, d):
 
 
 @pytest.mark.parametrize("io,hq,hkv,d", [("bf16", 32, 32, 64), ("bf16", 66, 22, 128), ("bf16", 32, 32, 256),
-                                         ("f32", 48, 48, 64), ("f32", 96, 24, 128), ("f32", 48, 48, 256)])
+                                         ("f32", 50, 50, 64), ("f32", 100, 25, 128), ("f32", 50, 50, 256)])
 def test_many_rows(io, hq, hkv, d):
     """Enough rows for the kernel of large row blocks (the small cases take the
     one that splits the keys): several sequences, some on cached prefixes, one that
@@ -88,6 +88,20 @@ def test_growing_scores(io):
     check(io, o, qq.double().numpy(), kk.double().numpy(), v[1], d ** -0.5, "growing")
     o = ssd.ssd_attn_prefill(qq.cuda(), kk.flip(0).contiguous().cuda(), v[0], [0, L])
     check(io, o, qq.double().numpy(), kk.flip(0).double().numpy(), v[1], d ** -0.5, "shrinking")
+
+
+def test_scores_far_below_zero():
+    """Every score of a row near -1e34: still a softmax, in both prefill kernels and
+    the decode step."""
+    for hkv in (1, 40):
+        q, k, v = prompt(8, "f32", 512, 512, hkv, hkv, 64)
+        qq, kk = torch.full_like(q[0], 1e16), torch.full_like(k[0], -1e16)
+        kk *= (1 + torch.arange(512, device="cuda") / 64)[:, None, None]    # the first key scores highest by far
+        o = ssd.ssd_attn_prefill(qq, kk, v[0], [0, 512])
+        assert torch.equal(o, v[0][:1].expand(512, -1, -1))
+    o = ssd.ssd_attn_decode_step(qq[:1], kk[511:], v[0][511:], kk[None].clone(), v[0][None].clone(),
+                                 torch.tensor([511], dtype=torch.int32, device="cuda"))
+    assert torch.equal(o, v[0][:1])
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])

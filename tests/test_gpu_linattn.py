@@ -73,7 +73,7 @@ def test_segments(io):
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_decays(io):
     """No decay, next to none, a memory shorter than a tile, none at all."""
-    g = [0.0, -1e-6, -0.3, -0.6, -2.0, -50.0, -1e4, -np.inf]
+    g = [0.0, -1e-6, -0.3, -1.2996, -2.0, -50.0, -1e4, -np.inf]   # (-1.2996: 60 powers of two a tile)
     q, k, v, gg, S0 = inputs(9, io, (1, 700), 1, 8, 64, 64, 1, g=g)
     o, fin = ssd.ssd_linattn_chunk_scan(q[0], k[0], v[0], gg[0], initial_state=S0[0])
     check(io, o[0], fin[0], q[1][0], k[1][0], v[1][0], gg[1], S0[1][0], 1.0, "decays")
