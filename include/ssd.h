@@ -326,8 +326,11 @@ ssd_status ssd_gdn_decode_steps(const ssd_gdn_dims *dims, int64_t nsteps, const 
  * SSD_BF16.  Scan alignment: q, k, v, o, states and workspace 16 bytes, strides
  * whole 16 bytes; decode step: state 16 bytes, the rest element-aligned.  o
  * must not overlap any input, state or the workspace, a final state no input.
- * Results are deterministic, and a packed batch gives what its sequences give
- * one by one up to rounding.
+ * The workspace holds states between the call's kernels: one per call that may
+ * run at the same time (also per captured graph that may).  Results are
+ * deterministic, and a packed batch gives what its sequences give one by one up
+ * to rounding.  An infinity or NaN in v reaches its own sequence only, there
+ * also the tokens up to 31 before it.
  */
 typedef struct ssd_linattn_dims {
     int64_t batch;     /* B >= 0 (sequences)                                  */
@@ -371,7 +374,9 @@ ssd_status ssd_linattn_decode_step(const ssd_linattn_dims *dims, const void *q, 
  *   q, o [q_rows, Hq, D], k, v [kv_rows, Hkv, D]  io_dtype
  * Strides as in ssd_linattn_dims (o contiguous).  Supported: D in {64, 128,
  * 256}, strides up to 2^22.  Alignment 16 bytes, strides whole 16 bytes.  o must
- * not overlap an input.  Rows of k and v outside the sequences are not read.
+ * not overlap an input.  Rows of k and v outside the sequences are not read.  An
+ * infinity or NaN in v reaches its own sequence only, there also the queries up
+ * to 63 before the first one that sees it.
  */
 typedef struct ssd_attn_dims {
     int64_t batch;     /* sequences, >= 0                                     */

@@ -37,6 +37,8 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
+#include <vector>
 
 #include "ssd_attn.h"
 #include "ssd_mma.h"
@@ -880,13 +882,21 @@ hipError_t step(int64_t B, int64_t Hk, int64_t Hv, int64_t dv, int64_t qs, int64
 LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int64_t Hv, int64_t dk,
                      int64_t dv)
 {
+    // the lengths, runs of equal ones taken together: the host's time grows with their
+    // number
+    std::vector<std::pair<uint32_t, int64_t>> lens;
     int64_t longest = 0;
-    for (int64_t i = 0; i < nseq; ++i)
+    for (int64_t i = 0; i < nseq; ++i) {
         longest = std::max(longest, seqs[i].len);
+        if (lens.empty() || lens.back().first != (uint32_t)seqs[i].len)
+            lens.emplace_back((uint32_t)seqs[i].len, 0);
+        ++lens.back().second;
+    }
     LinPlan best = {};
     double best_us = 1e300;
     const int64_t esz = bf16 ? 2 : 4;
-    const int64_t kmax = std::max<int64_t>(1, std::min<int64_t>(nseq > 256 ? 16 : 64, (longest + 95) / 96));
+    const int64_t trials = std::clamp<int64_t>(4096 / std::max<int64_t>(1, (int64_t)lens.size()), 16, 64);
+    const int64_t kmax = std::max<int64_t>(1, std::min<int64_t>(trials, (longest + 95) / 96));
     for (int cols = dv % 128 == 0 && dk <= 128 ? 128 : 64; cols >= 64; cols /= 2) {
         const int64_t heads = Hv * (dv / cols);
         // work-groups of a CU: by LDS, and by registers (8 waves; 4 of the large heads
@@ -907,10 +917,10 @@ LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int
         for (int64_t k = 1; k <= kmax; ++k) {
             const int64_t T0 = std::max<int64_t>(32, ((longest + k - 1) / k + 31) / 32 * 32);
             int64_t segs = 0, slot = 0;
-            for (int64_t i = 0; i < nseq; ++i) {
-                const int64_t ns = std::max<int64_t>(1, (seqs[i].len + T0 - 1) / T0);
-                segs += ns;
-                slot += ns > 1 ? ns : 0;
+            for (const auto &[len, count] : lens) {
+                const int64_t ns = std::max<int64_t>(1, (len + (uint32_t)T0 - 1) / (uint32_t)T0);
+                segs += count * ns;
+                slot += ns > 1 ? count * ns : 0;
             }
             // rounds of a launch of n work-groups of at most T0 tokens (a partly filled
             // one gains about half of what it leaves free)

@@ -145,6 +145,22 @@ def test_nothing_outside_the_sequences_is_read_or_written():
     assert ob[:10].isnan().all() and ob[10 + L:].isnan().all()
 
 
+@pytest.mark.parametrize("io,hq", [("bf16", 2), ("bf16", 66), ("f32", 2), ("f32", 80)])
+def test_non_finite_keys_and_values(io, hq):
+    """A bad value reaches its own sequence from at most 63 queries before its token
+    on, a bad key only queries that see it."""
+    cu = [0, 260, 520]
+    q, k, v = prompt(21, io, 520, 520, hq, hq, 64)
+    o = ssd.ssd_attn_prefill(q[0], k[0], v[0], cu)
+    for bad in (float("inf"), float("nan")):
+        kx, vx = k[0].clone(), v[0].clone()
+        kx[100], vx[100] = bad, bad
+        assert torch.equal(ssd.ssd_attn_prefill(q[0], kx, v[0], cu)[:100], o[:100])
+        ox = ssd.ssd_attn_prefill(q[0], k[0], vx, cu)
+        assert torch.equal(ox[:37], o[:37]) and torch.equal(ox[260:], o[260:])
+        assert not ox[100:260].isfinite().any()
+
+
 def test_prefill_no_rows():
     z = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
     assert ssd.ssd_attn_prefill(z, z[:, :1], z[:, :1], [0]).shape == z.shape

@@ -93,6 +93,26 @@ def test_packed(io):
             check(io, o[a:b], fin[i], q[1][a:b], k[1][a:b], v[1][a:b], g[1], S0[1][i], -1.5, f"seq {i}")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_non_finite_keys_and_values(io):
+    """A bad value reaches its own sequence from at most 31 tokens before its own on,
+    a bad key or query no token before its own."""
+    cu = [0, 260, 520]
+    q, k, v, g, S0 = inputs(22, io, (520,), 1, 2, 64, 64, 2)
+    o, fin = ssd.ssd_linattn_chunk_scan_varlen(q[0], k[0], v[0], g[0], cu, initial_states=S0[0])
+    for which in range(3):
+        for bad in (float("inf"), float("nan")):
+            x = [q[0], k[0], v[0]]
+            x[which] = x[which].clone()
+            x[which][100] = bad
+            ox, fx = ssd.ssd_linattn_chunk_scan_varlen(*x, g[0], cu, initial_states=S0[0])
+            first = 69 if which == 2 else 100
+            assert torch.equal(ox[:first], o[:first]) and torch.equal(ox[260:], o[260:])
+            assert torch.equal(fx[1], fin[1]) and not ox[100].isfinite().any()
+            if which == 0:
+                assert torch.equal(ox[101:], o[101:]) and torch.equal(fx, fin)
+
+
 @pytest.mark.parametrize("io,dk,dv", [("bf16", 128, 128), ("bf16", 128, 64), ("bf16", 256, 256), ("f32", 64, 64),
                                       ("f32", 256, 64)])
 def test_slow_decays_over_many_tiles(io, dk, dv):
