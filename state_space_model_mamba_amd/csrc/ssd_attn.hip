@@ -160,7 +160,7 @@ __device__ __forceinline__ void join_waves(unsigned char *smem, float (&sm)[Wave
 // LDS slots, a tile ahead.
 //
 // Bound by the matrix and vector units: one prompt of 8192 tokens, 32 heads over 8
-// of 128 in bf16, takes 500 - 530 us, 1.04 - 1.10 PFLOP/s; a large library product
+// of 128 in bf16, takes 500 - 540 us, 1.02 - 1.10 PFLOP/s; a large library product
 // (8192 x 8192 x 8192) reaches 1.20 on the same card.  The matrix units are busy 48%
 // of the time and the vector units 44%.  Tried and no faster: the eight waves'
 // pairs staggered by half a tile (554 us), 64 rows per wave with the two blocks'

@@ -875,7 +875,8 @@ hipError_t step(int64_t B, int64_t Hk, int64_t Hv, int64_t dv, int64_t qs, int64
 // chip's slots full at least slots x `rate` us (memory: the bytes of a tile at
 // 4.8 TB/s, q and k once per head group; or the matrix and vector work).  A launch
 // runs in rounds of `slots` work-groups; a chained state costs its reader about
-// 2.5 us.  Measured at 4 x 8192 tokens (32 heads of 128 x 128, bf16, 512 slots): 262
+// 2.5 us at 128 keys (half of that at 64: 2 x 1000 fp32 tokens of 8 heads of 64 x 64
+// take 29 us with 11 segments, 34 with 8, 43 with 6).  Measured at 4 x 8192 tokens (32 heads of 128 x 128, bf16, 512 slots): 262
 // us with 4 segments per sequence (one round of the scan) against 295 with 8 and
 // 326 with 2; at 8 x 2048 (24 heads of 128 x 64, 768 slots): 75 us with 4 against
 // 97 with 2, 92 with 8, 102 unsplit.
@@ -896,7 +897,7 @@ LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int
     double best_us = 1e300;
     const int64_t esz = bf16 ? 2 : 4;
     const int64_t trials = std::clamp<int64_t>(4096 / std::max<int64_t>(1, (int64_t)lens.size()), 16, 64);
-    const int64_t kmax = std::max<int64_t>(1, std::min<int64_t>(trials, (longest + 95) / 96));
+    const int64_t kmax = std::max<int64_t>(1, std::min<int64_t>(trials, (longest + 31) / 32));
     for (int cols = dv % 128 == 0 && dk <= 128 ? 128 : 64; cols >= 64; cols /= 2) {
         const int64_t heads = Hv * (dv / cols);
         // work-groups of a CU: by LDS, and by registers (8 waves; 4 of the large heads
@@ -933,7 +934,7 @@ LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int
             double us = launch((double)(segs * heads), chain, rate);
             if (segs > nseq)
                 us += 4.0 + launch((double)((segs - nseq) * heads), chain_state, rate_state) +
-                      2.5 * (double)((longest + T0 - 1) / T0 - 1);
+                      2.5 * w * (double)((longest + T0 - 1) / T0 - 1);
             if (us < best_us) {
                 best_us = us;
                 best.seg_tokens = T0;
