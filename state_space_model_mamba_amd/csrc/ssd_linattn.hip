@@ -51,6 +51,11 @@ using namespace mx;
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kEpoch = 60.f;
 constexpr int kEpochTiles = 8;
+// Chained states times keys from which lin_chain_kernel runs (us without and with
+// it): bf16, one sequence, 4 heads of 256 x 64, 6 segments 514 and 496, 16 segments
+// 295 and 207, 64 segments 493 and 83; 32 heads of 128 x 128, 6 segments 394 and 399,
+// 12 segments (2048 tokens) 52 and 45; fp32, 8 heads of 64 x 64, 11 segments 29 and 32.
+constexpr int64_t kChain = 1024;
 constexpr float kForget = 4.f;                // 2.5e-6 times 2^-4 is fp32's own rounding
 
 struct LinTab {
@@ -74,6 +79,7 @@ struct LinArgs {
     int32_t seg_tokens, Hk, Hv, dv;
     float scale;
     int copy_init;                            // fin is init: segment 0 starts from its slot's copy
+    int chained;                              // slots hold entering states (lin_chain_kernel)
 };
 
 typedef const __attribute__((address_space(4))) LinArgs *LinArgsPtr;
@@ -333,6 +339,43 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     store_slot<DK>(slot0 + k.seg * wslot, R);
 }
 
+// The slots of long chains made running states in place: slot j becomes the state
+// after segment j, slot j-1 lambda^T0 + slot j (the factor to more than fp32, as its
+// rounding would be repeated).  Every segment of the scan then reads one slot instead
+// of all before its own.  One thread takes four elements of all segments, eight
+// segments' loads in flight.
+template <int DK> __global__ __launch_bounds__(256) void lin_chain_kernel(LinArgs args_in_kernarg)
+{
+    const LinArgsPtr a = (LinArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    const int per = a->Hv * a->dv * (DK / 64) / 16;       // work-groups of a sequence: 1024 elements each
+    const int si = blockIdx.x / (unsigned)per, at = (blockIdx.x % (unsigned)per) * 1024;
+    const int last = (a->tab.len[si] + a->seg_tokens - 1) / a->seg_tokens - 1;   // slots 0 .. last - 1
+    if (last < 2)
+        return;
+    const double g2 = std::max(a->g[at / (DK * a->dv)] * kLog2e, -1e5);
+    const double fd = exp2(g2 * (double)a->seg_tokens);
+    const float fhi = (float)fd, flo = fhi < 3e38f ? (float)(fd - (double)fhi) : 0.f;
+    const int64_t wslot = (int64_t)a->Hv * DK * a->dv;
+    float *p = a->ws + (int64_t)a->tab.slot[si] * wslot + at + 4 * threadIdx.x;
+    constexpr int U = 8;
+    f32x4 acc = *reinterpret_cast<const f32x4 *>(p);
+    for (int j0 = 1; j0 < last; j0 += U) {
+        f32x4 z[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            z[u] = *reinterpret_cast<const f32x4 *>(p + std::min(j0 + u, last - 1) * wslot);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j0 + u >= last)
+                break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[e] = __builtin_fmaf(acc[e], fhi, __builtin_fmaf(acc[e], flo, z[u][e]));
+            *reinterpret_cast<f32x4 *>(p + (j0 + u) * wslot) = acc;
+        }
+    }
+}
+
 // o over one segment of one (sequence, value head, column tile), and the end state
 // for a sequence's last segment.
 //
@@ -398,7 +441,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     } else {
         // slot 0 holds the state after segment 0 (the initial one included), slot
         // j segment j's from zero; those forgotten below 2^-150 are left out
-        int j = 0;
+        int j = a->chained ? seg - 1 : 0;
         while (j < seg - 1 && g2f * (float)T0 * (float)(seg - 1 - j) < -150.f)
             ++j;
         for (; j < seg; ++j)
@@ -706,7 +749,7 @@ hipError_t scan(LinArgs &args, int64_t nseq, const LinSeq *seqs, hipStream_t s)
     int64_t slot = 0;
     for (int64_t at = 0; at < nseq;) {
         int n = 0;
-        int64_t items = 0, states = 0;
+        int64_t items = 0, states = 0, longest = 0;
         int32_t segs[LinTab::kMax];
         while (at < nseq && n < LinTab::kMax) {
             const int64_t ns = std::max<int64_t>(1, (seqs[at].len + T0 - 1) / T0);
@@ -720,12 +763,14 @@ hipError_t scan(LinArgs &args, int64_t nseq, const LinSeq *seqs, hipStream_t s)
             slot += ns > 1 ? ns : 0;
             items += ns;
             states += ns - 1;
+            longest = std::max(longest, ns);
             ++n;
             ++at;
         }
         if (n == 0)
             return hipErrorInvalidValue;
         hipError_t e;
+        args.chained = (longest - 1) * DK >= kChain;
         for (int pass = states > 0 ? 0 : 1; pass < 2; ++pass) {
             int32_t sum = 0;
             for (int i = 0; i < 128; ++i) {
@@ -739,6 +784,11 @@ hipError_t scan(LinArgs &args, int64_t nseq, const LinSeq *seqs, hipStream_t s)
                                         args, items * groups, s);
             if (e != hipSuccess)
                 return e;
+            if (pass == 0 && args.chained) {
+                lin_chain_kernel<DK><<<dim3((unsigned)(n * (args.Hv * args.dv * (DK / 64) / 16))), dim3(256), 0, s>>>(args);
+                if ((e = hipGetLastError()) != hipSuccess)
+                    return e;
+            }
         }
     }
     return hipSuccess;
@@ -874,12 +924,13 @@ hipError_t step(int64_t B, int64_t Hk, int64_t Hv, int64_t dv, int64_t qs, int64
 // 32-token tile takes at least `chain` us (its own dependent steps), and with the
 // chip's slots full at least slots x `rate` us (memory: the bytes of a tile at
 // 4.8 TB/s, q and k once per head group; or the matrix and vector work).  A launch
-// runs in rounds of `slots` work-groups; a chained state costs its reader about
-// 2.5 us at 128 keys (half of that at 64: 2 x 1000 fp32 tokens of 8 heads of 64 x 64
-// take 29 us with 11 segments, 34 with 8, 43 with 6).  Measured at 4 x 8192 tokens (32 heads of 128 x 128, bf16, 512 slots): 262
-// us with 4 segments per sequence (one round of the scan) against 295 with 8 and
-// 326 with 2; at 8 x 2048 (24 heads of 128 x 64, 768 slots): 75 us with 4 against
-// 97 with 2, 92 with 8, 102 unsplit.
+// runs in rounds of `slots` work-groups; a chained state costs its reader 1, 2.5 or 6
+// us at 64, 128 and 256 keys, unless lin_chain_kernel has joined them, which moves
+// every slot three times over (with the state kernel's writes).  Measured at 4 x 8192
+// tokens (32 heads of 128 x 128, bf16, 512 slots): 259 us with 4 segments per sequence
+// (one round of the scan) against 285 with 8 and 304 with 2; at 8 x 2048 (24 heads of
+// 128 x 64, 768 slots): 73 us with 4 against 103 with 2 and 88 with 8; one sequence of
+// 13384 (4 heads of 256 x 64): 79 us with 84 or more, 207 with 16.
 LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int64_t Hv, int64_t dk,
                      int64_t dv)
 {
@@ -896,7 +947,7 @@ LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int
     LinPlan best = {};
     double best_us = 1e300;
     const int64_t esz = bf16 ? 2 : 4;
-    const int64_t trials = std::clamp<int64_t>(4096 / std::max<int64_t>(1, (int64_t)lens.size()), 16, 64);
+    const int64_t trials = std::clamp<int64_t>(4096 / std::max<int64_t>(1, (int64_t)lens.size()), 16, 128);
     const int64_t kmax = std::max<int64_t>(1, std::min<int64_t>(trials, (longest + 31) / 32));
     for (int cols = dv % 128 == 0 && dk <= 128 ? 128 : 64; cols >= 64; cols /= 2) {
         const int64_t heads = Hv * (dv / cols);
@@ -909,6 +960,7 @@ LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int
         const double slots = 256.0 * per_cu, w = dk / 128.0, waves = (double)nw;
         const double chain = !bf16 ? 1.8 + 4.6 * w : dk <= 128 ? 0.6 + 0.9 * w : 5.8;
         const double chain_state = !bf16 ? 0.7 + 2.4 * w : dk <= 128 ? 0.4 + 0.6 * w : 3.5;
+        const double chain_slot = dk == 64 ? 1.0 : dk == 128 ? 2.5 : 6.0;
         const double shared = (double)dk * Hk / Hv;       // q (or k) columns a work-group pays for
         const double us_byte = 1.0 / 4.8e6;
         const double rate = std::max(32 * esz * (2 * shared + 2 * cols) * us_byte,
@@ -932,9 +984,14 @@ LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int
                                 (rest > 0 ? std::max(ch, 0.5 * (slots + rest) * rt) : 0.0));
             };
             double us = launch((double)(segs * heads), chain, rate);
-            if (segs > nseq)
-                us += 4.0 + launch((double)((segs - nseq) * heads), chain_state, rate_state) +
-                      2.5 * w * (double)((longest + T0 - 1) / T0 - 1);
+            if (segs > nseq) {
+                const int64_t prior = (longest + T0 - 1) / T0 - 1;
+                us += 4.0 + launch((double)((segs - nseq) * heads), chain_state, rate_state);
+                if (prior * dk >= kChain)
+                    us += 9.0 + 0.3 * (double)prior + 3.0 * (double)(slot * Hv * dk * dv * 4) * us_byte;
+                else
+                    us += chain_slot * (double)prior;
+            }
             if (us < best_us) {
                 best_us = us;
                 best.seg_tokens = T0;

@@ -113,6 +113,36 @@ def test_non_finite_keys_and_values(io):
                 assert torch.equal(ox[101:], o[101:]) and torch.equal(fx, fin)
 
 
+@pytest.mark.parametrize("io,dk,dv,init", [("bf16", 256, 64, True), ("f32", 256, 128, False), ("bf16", 128, 64, True),
+                                           ("bf16", 64, 64, False), ("f32", 64, 256, True)])
+def test_long_chains(io, dk, dv, init):
+    """Few heads and long sequences: dozens of segments, whose states a kernel of its
+    own joins, beside sequences of few segments, one and none; in place and replayed."""
+    lens, hv = [4500, 0, 40, 700, 2100, 1], 2
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v, g, S0 = inputs(dk + 3 * dv, io, (int(cu[-1]),), 1, hv, dk, dv, len(lens), init=init, g=[-1e-4, -0.01])
+    o, fin = ssd.ssd_linattn_chunk_scan_varlen(q[0], k[0], v[0], g[0], cu, initial_states=S0[0])
+    for i, n in enumerate(lens):
+        if n > 0:
+            a, b = cu[i], cu[i + 1]
+            check(io, o[a:b], fin[i], q[1][a:b], k[1][a:b], v[1][a:b], g[1], S0[1][i] if init else None, 1.0, f"seq {i}")
+    if not init:
+        return
+    first, st, o2 = S0[0].clone(), S0[0].clone(), torch.empty_like(o)
+    run = lambda: ssd.ssd_linattn_chunk_scan_varlen(q[0], k[0], v[0], g[0], cu, initial_states=st, o=o2, final_states=st)
+    run()
+    assert torch.equal(o2, o) and torch.equal(st, fin)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        st.copy_(first)
+        o2.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, o) and torch.equal(st, fin)
+
+
 @pytest.mark.parametrize("io,dk,dv", [("bf16", 128, 128), ("bf16", 128, 64), ("bf16", 256, 256), ("f32", 64, 64),
                                       ("f32", 256, 64)])
 def test_slow_decays_over_many_tiles(io, dk, dv):
