@@ -329,8 +329,11 @@ ssd_status ssd_gdn_decode_steps(const ssd_gdn_dims *dims, int64_t nsteps, const 
  * The workspace holds states between the call's kernels: one per call that may
  * run at the same time (also per captured graph that may).  Results are
  * deterministic, and a packed batch gives what its sequences give one by one up
- * to rounding.  An infinity or NaN in v reaches its own sequence only, there
- * also the tokens up to 31 before it.
+ * to rounding.  The scan gives what the recurrence gives while the products
+ * q . k and k v, the states and the outputs are finite fp32 numbers; in bf16,
+ * terms below 2^-70 may lose bits, and in both types powers of lambda below
+ * 2^-126 count as 0.  An infinity or NaN in v reaches its own sequence only,
+ * there also the tokens up to 31 before it.
  */
 typedef struct ssd_linattn_dims {
     int64_t batch;     /* B >= 0 (sequences)                                  */

@@ -7,12 +7,14 @@
 //     o_t = scale (lambda^(t+1) S^T q_t + sum_{s<=t} lambda^(t-s) (q_t . k_s) v_s)
 //     S  <- lambda^n S + sum_s lambda^(n-1-s) k_s v_s^T
 // The decay is the same for every token, so the scan keeps the state as R with
-// S = lambda^e R, e the tokens since the last rescale: a tile then adds
-// lambda^-(e+s+1) k_s v_s^T to R without touching the rest of it, with weights from
-// a table, and R is multiplied by lambda^e once per epoch: every kEpochTiles tiles,
-// or sooner, before the weights would pass 2^kEpoch.  A head that forgets more than
-// that within a tile is scaled every tile instead.  Powers of lambda are formed from
-// the exponent in fp64 (in fp32 they would be off by up to kEpoch 2^-24 relative).
+// S = lambda^(e-N) R, e the tokens since the last rescale and N those of an epoch: a
+// tile then adds lambda^(N-e-s-1) k_s v_s^T to R without touching the rest of it,
+// with weights from a table, and R is multiplied by lambda^N once per epoch: every
+// kEpochTiles tiles, or sooner, before the weights would fall below 2^-kEpoch.  A head
+// that forgets more than that within a tile is scaled every tile instead.  No weight
+// passes 1, so R overflows only where S does; below, terms keep their 24 bits down to
+// 2^(kEpoch-110).  Powers of lambda are formed from the exponent in fp64 (in fp32 they
+// would be off by up to kEpoch 2^-24 relative).
 //
 // Rounding (bf16): q, k, v are exact operands.  The state and the masked scores
 // are each rounded once to bf16 on their way into the products that form o
@@ -49,7 +51,10 @@ namespace {
 using namespace mx;
 
 constexpr double kLog2e = 1.4426950408889634;
-constexpr float kEpoch = 60.f;
+// Powers of two that an epoch's weights span.  Larger spans lose small terms, smaller
+// ones rescale more heads in every tile: 8 x 2048 tokens of 24 heads (log decays -0.8
+// to -1/256) 67.0 us with 40, 69.4 with 24.
+constexpr float kEpoch = 40.f;
 constexpr int kEpochTiles = 8;
 // Chained states times keys from which lin_chain_kernel runs (us without and with
 // it): bf16, one sequence, 4 heads of 256 x 64, 6 segments 514 and 496, 16 segments
@@ -400,9 +405,9 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     typedef typename Piece<T>::V V;
     constexpr int kStores = sizeof(T) == 2 ? 2 : 4;       // per wave and tile
     extern __shared__ __align__(1024) unsigned char smem[];
-    // after the ring: update weights of an epoch's tokens, lambda^-(i C + s + 1)
+    // after the ring: update weights of an epoch's tokens, lambda^(N-1-(i C+s))
     // (direct: those of a tile, lambda^(C-1-s); the last C: a ragged tile's), and
-    // lambda^(i C).  (All of it dynamic, so that the ring starts at LDS address 0 and
+    // lambda^(i C-N).  (All of it dynamic, so that the ring starts at LDS address 0 and
     // its offsets are immediates.)
     float *su = reinterpret_cast<float *>(smem + SM::kScan);
     float *spow = su + (kEpochTiles + 1) * C;
@@ -461,18 +466,19 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     const bool direct = -g2f * (float)C > kEpoch || g2f > 0.f;   // scaled every tile
     const int epoch =
         direct ? 0 : std::max(1, (int)std::min((float)kEpochTiles, kEpoch / (1e-9f - g2f * (float)C)));
+    const int N = C * epoch;
     // what R is multiplied by when it is rescaled, to more than fp32
-    float fhi = pow_of(g2, C * (direct ? 1 : epoch)), flo = 0.f;
+    float fhi = pow_of(g2, direct ? C : N), flo = 0.f;
     if (epoch == kEpochTiles) {
-        const double fd = exp2(g2 * (double)(C * epoch));
+        const double fd = exp2(g2 * (double)N);
         fhi = (float)fd;
         flo = (float)(fd - (double)fhi);
     }
     const float scale = a->scale;
     for (int i = tid; i < kEpochTiles * C; i += 64 * NW)
-        su[i] = pow_of(g2, direct ? C - 1 - i : -(i + 1));
+        su[i] = pow_of(g2, (direct ? C : N) - 1 - i);
     if (tid <= kEpochTiles)
-        spow[tid] = direct ? 1.f : pow_of(g2, tid * C);
+        spow[tid] = direct ? 1.f : pow_of(g2, tid * C - N);
     const float ft = scale * pow_of(g2, cl + 1);          // scale lambda^(t+1), the lane's token t
     // the wave's 16 x 16 blocks of a tile's masked scores (transposed: s x t): factors
     // scale lambda^(t-s), and the scores of the tile in `slot` into its P buffer
@@ -545,7 +551,8 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
         }
     }
     T *const out = (T *)a->o;
-    int n = 0, ep = 0, e = 0;                             // tiles done; S = lambda^e R, ep = e / C
+    // tiles done; S = lambda^(e-N) R, ep = e / C (entered with R = S: rescaled at once)
+    int n = 0, ep = epoch, e = N;
     int64_t orow = ((tok0 + beg) * Hv + head) * (int64_t)dv + col0;
     const unsigned ostride = (unsigned)(Hv * dv * (int)sizeof(T));
     const unsigned olane = (unsigned)cl * ostride + 16u * (unsigned)hh;
@@ -719,7 +726,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
         tiles(std::integral_constant<int, 3>(), ntile);
     }
     if (seg == nseg - 1) {
-        const float fe = pow_of(g2, e);
+        const float fe = pow_of(g2, e - N);
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
