@@ -371,7 +371,8 @@ ssd_status ssd_linattn_decode_step(const ssd_linattn_dims *dims, const void *q, 
  * earlier part of the sequence in front, this is the next part of a long
  * prompt.  Query head h reads key head h / (Hq / Hkv):
  *     o[t,h] = sum_s softmax_s(scale q[t,h] . k[s,h']) v[s,h']   (visible s)
- * A query that sees no key (kv_lens[i] < its queries) gets o = 0.  With
+ * A query that sees no key (kv_lens[i] < its queries) gets o = 0, and so does one
+ * whose visible scores are all -infinity (products past the fp32 range).  With
  * kv_starts and kv_lens NULL the keys are the prompts' own rows (kv_rows ==
  * q_rows).  cu_seqlens, kv_starts and kv_lens are HOST arrays.
  *   q, o [q_rows, Hq, D], k, v [kv_rows, Hkv, D]  io_dtype
@@ -404,7 +405,7 @@ ssd_status ssd_attn_prefill(const ssd_attn_dims *dims, const int64_t *cu_seqlens
  * rows 0 .. lengths[b] (the new one included).  lengths is a DEVICE array that
  * the call reads and does not change.  A length outside [0, M) marks an unused
  * slot: o[b] = 0 and its cache stays as it is.  Rows after lengths[b] are not
- * read.
+ * read.  o[b] is 0 also where all scores are -infinity, as in ssd_attn_prefill.
  *   q, o [B, Hq, D], k, v [B, Hkv, D], k_cache, v_cache [B, M, Hkv, D] io_dtype
  *   lengths [B] int32
  * {q,k,v}_stride: elements between the batch rows of q, k, v (0 = contiguous).

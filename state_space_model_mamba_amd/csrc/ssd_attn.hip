@@ -627,7 +627,7 @@ __global__ __launch_bounds__((64 * WaveTiles<T, D>::kWaves), 1) void attn_decode
     const int64_t slot = ((int64_t)item * a.nsplit + split) * 32;
     join_waves<T, D>(smem, sm, sl, w, lane, rows, m, l, acc, [&](int i, f32x4 v, float mr, float lr) {
         if (a.nsplit == 1) {
-            const float inv = 1.f / lr;
+            const float inv = lr > 0.f ? 1.f / lr : 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 op[i + e] = (T)(v[e] * inv);
