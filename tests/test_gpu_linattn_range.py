@@ -1,4 +1,6 @@
-"""Linear attention at the ends of the number range."""
+"""Linear attention at the ends of the number range: large and small values, states of
+which little is left."""
+import numpy as np
 import pytest
 
 import state_space_model_mamba_amd as ssd
@@ -26,3 +28,45 @@ def test_large_and_small_values(io, dk, dv, power):
     bo, bS = lin_bounds(io, ro, ao, A, L, dk)
     within(host(o[0]) / f, ro, bo, "o")
     within(host(fin[0]) / f, rS, bS, "state")
+
+
+def one_token_state(dev, g, n, k, v, L):
+    """A state whose only term is lambda^n k v, against the formula.
+
+    Roundings, relative, in units of 2^-22 (a power of the decay: the exponential's
+    last place and its exponent's fraction in fp32, 1.5 2^-23; a product or sum
+    2^-24): the token's weight and product 1, the partial sums it enters 1, the end
+    factor 1, a segment's power and its sum into the next ones 3, and a rescale every
+    256 tokens or after 2^-32 at most.  Beside these, in bf16, 2^-24 of the token's
+    own product, however much of it is left."""
+    size = np.abs(k[..., :, None] * v[..., None, :])
+    want = np.exp(g * n)[..., None, None] * k[..., :, None] * v[..., None, :]
+    off = np.abs(host(dev) - want) - ((7 + L / 256 + np.abs(g * n)[..., None, None] / 22) * 2.0 ** -22 * np.abs(want)
+                                      + 2.0 ** -24 * size)
+    assert (off <= 0).all(), f"past the bound by {(off / (size + 1e-30)).max():.2e} of the product"
+
+
+@pytest.mark.parametrize("io,dk,dv", [("bf16", 64, 64), ("bf16", 128, 128), ("bf16", 128, 64), ("bf16", 256, 64),
+                                      ("f32", 64, 64)])
+@pytest.mark.parametrize("L,at", [(200, 20), (3000, 20), (3000, 2500)])
+def test_states_of_quiet_ends(io, dk, dv, L, at):
+    """One token that matters, before keys of 0 (padding) by whose end it is forgotten
+    to 2^-3 to 2^-28: the end state is off by no more than fp32 roundings of it and of
+    what it was."""
+    gs = np.log(2.0) * -np.array([3.0, 5.2, 6.5, 9.0, 28.0]) / (L - 1 - at)
+    q, k, v, g, _ = inputs(L + at + dk, io, (1, L), 1, 5, dk, dv, 1, init=False, g=gs)
+    k[0][:, :at], k[0][:, at + 1:] = 0, 0
+    _, fin = ssd.ssd_linattn_chunk_scan(q[0], k[0], v[0], g[0])
+    one_token_state(fin[0], g[1], L - 1 - at, np.repeat(k[1][0, at], 5, axis=0), v[1][0, at], L)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 64), (128, 128), (256, 64)])
+def test_states_handed_between_segments(dk, dv):
+    """As above with enough heads that segments are long: the token that matters is
+    forgotten within its own segment, all of whose later keys are 0."""
+    B, L, hv, at = 8, 2048, 24, 10
+    gs = -np.linspace(0.003, 0.012, hv)
+    q, k, v, g, _ = inputs(dk + dv, "bf16", (B, L), 8, hv, dk, dv, B, init=False, g=gs)
+    k[0][:, :at], k[0][:, at + 1:] = 0, 0
+    _, fin = ssd.ssd_linattn_chunk_scan(q[0], k[0], v[0], g[0])
+    one_token_state(fin, g[1][None], L - 1 - at, np.repeat(k[1][:, at], 3, axis=1), v[1][:, at], L)
