@@ -1,10 +1,10 @@
-"""Softmax attention: the same sequence through every path (both prefill kernels, the
-step with and without chunks to join)."""
+"""Softmax attention: the prefill kernel of large row blocks at scales and scores where
+it can go wrong, and the same sequence through every path."""
 import pytest
 import torch
 
 import state_space_model_mamba_amd as ssd
-from test_gpu_attn import prompt
+from test_gpu_attn import check, prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -15,6 +15,41 @@ MANY = 4096
 
 def heads_for(L):
     return -(-MANY // (-(-L // 32)))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, 1e-40, -0.3, 2.0])
+def test_scales_many_rows(io, scale):
+    L, h = 70, heads_for(70)
+    q, k, v = prompt(3, io, L, L, h, h, 64)
+    o = ssd.ssd_attn_prefill(q[0], k[0], v[0], [0, L], scale=scale)
+    for j in (0, 1, h // 2, h - 1):
+        s = slice(j, j + 1)
+        check(io, o[:, s], q[1][:, s], k[1][:, s], v[1][:, s], scale, f"scale {scale}, head {j}")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_far_below_zero_many_rows(io, d):
+    """Every score of a row near -1e33 and below: the first key's by far the highest."""
+    L, h = 512, heads_for(512)
+    q, k, v = prompt(8, io, L, L, h, h, d)
+    qq, kk = torch.full_like(q[0], 2.0 ** 53), torch.full_like(k[0], -2.0 ** 53)
+    kk *= (1 + torch.arange(L, device="cuda") / 64)[:, None, None].to(kk.dtype)
+    o = ssd.ssd_attn_prefill(qq, kk, v[0], [0, L])
+    assert torch.equal(o, v[0][:1].expand(L, -1, -1))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_scores_far_above_zero_many_rows(io):
+    """Scores that grow far past 2^24 with each key: each query takes its own value."""
+    L, h = 300, heads_for(300)
+    q, k, v = prompt(9, io, L, L, h, h, 64)
+    qq = torch.full_like(q[0], 2.0 ** 20)
+    kk = torch.full_like(k[0], 2.0 ** 20) * (2.0 ** (torch.arange(L, device="cuda") // 8 - 18))[:, None, None].to(q[0].dtype)
+    kk = kk * (1 + torch.arange(L, device="cuda") % 8 / 8)[:, None, None].to(kk.dtype)     # (exact, and growing)
+    o = ssd.ssd_attn_prefill(qq, kk, v[0], [0, L])
+    assert torch.equal(o, v[0])
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
