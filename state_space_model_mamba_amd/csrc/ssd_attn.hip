@@ -350,9 +350,13 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void attn_prefill_kernel
 
 // Few rows (short prompts, or few heads): 32 rows per work-group, the waves taking
 // every kWaves-th 32-key tile of them, each with its own running (m, l, acc), joined
-// at the end.  A work-group then walks its keys in a quarter of the steps, and eight
-// times as many share the chip; bound by each work-group's chain of steps, about 1.3
-// us each (figures at the rule that chooses it).
+// at the end.  Four to eight times as many work-groups then share the chip, and each
+// walks its keys in a kWaves-th of the tiles (four waves; two for rows of 512 bytes
+// and one for rows of 1 KB, whose tiles fill the LDS).  Bound by each work-group's
+// chain of steps: 1.3 us each at 128 in bf16, 5 at 128 in fp32, 13 at 256 in fp32 (64
+// queries on 4000 keys: 40, 320 and 1670 us; figures at the rule that chooses it).
+// The keys are not split over work-groups: the time grows with the prefix whatever
+// the chip has free.
 template <typename T, int D>
 __global__ __launch_bounds__((64 * WaveTiles<T, D>::kWaves), 1) void attn_prefill_few_kernel(
     PrefillArgs args_in_kernarg)
@@ -479,15 +483,21 @@ hipError_t prefill(PrefillArgs &args, int64_t nseq, const AttnSeq *seqs, hipStre
     static std::atomic<uint64_t> allowed{0}, allowed_few{0};
     constexpr int64_t kRows = 32 * NW;
     // Few rows go to the kernel of 32-row work-groups.  Measured (us, few against
-    // many; work-groups of 32 rows in brackets): bf16, 32 heads over 8 of 128, 64
-    // queries on 4000 cached keys 40 against 103 [64], 256 on 4000 46 against 108
-    // [256], a prompt of 500 18.9 against 18.6 [504], of 1000 43 against 31 [1000]; fp32,
-    // 8 heads of 128, 1000 tokens 86 against 189 [252], 2000 tokens 180 against 367
-    // [504].
+    // many, 32 heads over 8) at n work-groups of 32 rows, a prompt alone (n tokens) and
+    // n queries after 4000 cached keys:
+    //            n     256              512              768              1024
+    //   bf16  64  11/11, 33/80     11/14, 46/85     17/18, 72/90     21/23, 88/94
+    //        128  11/12, 47/109    19/19, 89/116    31/25, 130/123   43/32, 172/130
+    //        256  17/20, 120/213   33/33, 232/227   59/45, 355/242   88/58, 483/259
+    //   fp32  64  12/24, 116/323   25/43, 222/342   47/63, 331/364   72/82, 453/385
+    //        128  28/52, 343/761   58/97, 675/804   122/143, 1053/850  192/188, 1433/896
+    //        256  115/152, 1762/2590  242/321, 3547/2736  555/485, 5415/2886  905/639, 7430/3037
+    // 8 heads over 8 (longer sequences at the same n) cross at the same n or up to half
+    // as much again later.
     int64_t blocks = 0;
     for (int64_t i = 0; i < nseq && blocks < (int64_t(1) << 32); ++i)
         blocks += (seqs[i].lq * (int64_t)args.grp + 31) / 32;
-    if (blocks * args.Hkv <= (sizeof(T) == 2 ? 512 : 1024))
+    if (blocks * args.Hkv <= (sizeof(T) == 2 ? 512 : 65536 / D))
         return prefill_launch(&attn_prefill_few_kernel<T, D>, 32, 64 * WaveTiles<T, D>::kWaves,
                               WaveTiles<T, D>::kSmem, allowed_few, args, nseq, seqs, s);
     constexpr unsigned kSmem = 4u * (sizeof(T) == 2 ? 64 : 32) * D * sizeof(T);

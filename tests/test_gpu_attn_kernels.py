@@ -13,6 +13,11 @@ pytestmark = pytest.mark.gpu
 MANY = 4096
 
 
+# the limit, in work-groups of 32 rows
+FEW = {("bf16", 64): 512, ("bf16", 128): 512, ("bf16", 256): 512, ("f32", 64): 1024, ("f32", 128): 512,
+       ("f32", 256): 256}
+
+
 def heads_for(L):
     return -(-MANY // (-(-L // 32)))
 
@@ -50,6 +55,17 @@ def test_scores_far_above_zero_many_rows(io):
     kk = kk * (1 + torch.arange(L, device="cuda") % 8 / 8)[:, None, None].to(kk.dtype)     # (exact, and growing)
     o = ssd.ssd_attn_prefill(qq, kk, v[0], [0, L])
     assert torch.equal(o, v[0])
+
+
+@pytest.mark.parametrize("io,d", list(FEW))
+def test_on_both_sides_of_the_limit(io, d):
+    """One work-group of 32 rows more or less: the other kernel, the same answers."""
+    for h in (FEW[io, d] // 2, FEW[io, d] // 2 + 1):       # two row blocks a head
+        q, k, v = prompt(d + h, io, 45, 78, h, h, d)
+        o = ssd.ssd_attn_prefill(q[0], k[0], v[0], [0, 45], kv_starts=[3], kv_lens=[75])
+        for j in (0, h // 3, h - 1):
+            s = slice(j, j + 1)
+            check(io, o[:, s], q[1][:, s], k[1][3:, s], v[1][3:, s], d ** -0.5, f"{h} heads, head {j}")
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
