@@ -322,8 +322,8 @@ ssd_status ssd_gdn_decode_steps(const ssd_gdn_dims *dims, int64_t nsteps, const 
  * slices of one projection: {q,k,v}_stride is the distance between consecutive
  * tokens (rows b L + t of the scan) in elements, 0 for contiguous rows.  o is
  * contiguous.  A sequence of length 0 hands its state through.
- * Supported: dk, dv in {64, 128, 256}, strides up to 2^22, io_dtype SSD_F32 or
- * SSD_BF16.  Scan alignment: q, k, v, o, states and workspace 16 bytes, strides
+ * Supported: dk, dv in {64, 128, 256}, strides up to 2^22, sequences up to 2^30
+ * tokens, io_dtype SSD_F32 or SSD_BF16.  Scan alignment: q, k, v, o, states and workspace 16 bytes, strides
  * whole 16 bytes; decode step: state 16 bytes, the rest element-aligned.  o
  * must not overlap any input, state or the workspace, a final state no input.
  * The workspace holds states between the call's kernels: one per call that may

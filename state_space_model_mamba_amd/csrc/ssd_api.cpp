@@ -904,6 +904,7 @@ namespace {
 
 constexpr int64_t kMaxStride = 1 << 22;   // a 64-row tile's byte offsets stay in 32 bits
 constexpr int64_t kMaxRows = INT32_MAX - 4096;
+constexpr int64_t kMaxScanTokens = 1 << 30;   // of a sequence: token + segment stays in 32 bits
 
 bool head_size(int64_t d)
 {
@@ -994,7 +995,7 @@ ssd_status linattn_seqs(const ssd_linattn_dims *d, const int64_t *cu, bool varle
         ssd::LinSeq &s = (*seqs)[(size_t)i];
         s.tok = varlen ? cu[i] : i * d->seqlen;
         s.len = varlen ? cu[i + 1] - cu[i] : d->seqlen;
-        if (s.len > kMaxRows)
+        if (s.len > kMaxScanTokens)
             return SSD_ERR_UNSUPPORTED;
     }
     return SSD_OK;

@@ -1,0 +1,21 @@
+"""Sizes at the attention layers' limits (CPU only: no call here reaches a launch)."""
+import ctypes
+
+import state_space_model_mamba_amd as ssd
+from test_attention_abi_cpu import attn, lib, lin, lin_scan, offsets  # noqa: F401 (lib: a fixture)
+
+
+def test_scan_tokens(lib):  # noqa: F811
+    """Token counts and offsets within a sequence are 32-bit sums of a token and a
+    segment's length: 2^30 tokens fit, more are refused."""
+    most = 1 << 30
+    small = dict(qk_heads=1, v_heads=1, dk=64, dv=64)
+    n = ctypes.c_size_t(7)
+    size = lib.ssd_linattn_chunk_scan_workspace_size
+    assert size(ctypes.byref(lin(batch=1, seqlen=most, **small)), ctypes.byref(n)) == 0 and n.value > 7
+    assert size(ctypes.byref(lin(batch=1, seqlen=most + 1, **small)), ctypes.byref(n)) == 3
+    assert lin_scan(lib, lin(batch=1, seqlen=most + 1, **small)) == 3
+    d = lin(batch=2, seqlen=2 * most, **small)
+    size = lib.ssd_linattn_chunk_scan_varlen_workspace_size
+    assert size(ctypes.byref(d), offsets(0, most, 2 * most), ctypes.byref(n)) == 0
+    assert size(ctypes.byref(d), offsets(0, most - 1, 2 * most), ctypes.byref(n)) == 3
