@@ -323,7 +323,7 @@ ssd_status ssd_gdn_decode_steps(const ssd_gdn_dims *dims, int64_t nsteps, const 
  * tokens (rows b L + t of the scan) in elements, 0 for contiguous rows.  o is
  * contiguous.  A sequence of length 0 hands its state through.
  * Supported: dk, dv in {64, 128, 256}, strides up to 2^22, sequences up to 2^30
- * tokens, io_dtype SSD_F32 or SSD_BF16.  Scan alignment: q, k, v, o, states and workspace 16 bytes, strides
+ * tokens, decode steps of B Hv dv < 2^30, io_dtype SSD_F32 or SSD_BF16.  Scan alignment: q, k, v, o, states and workspace 16 bytes, strides
  * whole 16 bytes; decode step: state 16 bytes, the rest element-aligned.  o
  * must not overlap any input, state or the workspace, a final state no input.
  * The workspace holds states between the call's kernels: one per call that may
@@ -410,7 +410,8 @@ ssd_status ssd_attn_prefill(const ssd_attn_dims *dims, const int64_t *cu_seqlens
  *   q, o [B, Hq, D], k, v [B, Hkv, D], k_cache, v_cache [B, M, Hkv, D] io_dtype
  *   lengths [B] int32
  * {q,k,v}_stride: elements between the batch rows of q, k, v (0 = contiguous).
- * Supported shapes and alignment as for ssd_attn_prefill, M < 2^31 - 4096.  The
+ * Supported shapes and alignment as for ssd_attn_prefill, M < 2^31 - 4096, fewer
+ * than 2^24 sequences times key heads times 32-head tiles of a key head's queries.  The
  * caches and o must not overlap an input, each other or the workspace.  The
  * workspace holds partial results between the call's kernels: one per call that
  * may run at the same time (also per captured graph that may).

@@ -904,6 +904,7 @@ namespace {
 
 constexpr int64_t kMaxStride = 1 << 22;   // a 64-row tile's byte offsets stay in 32 bits
 constexpr int64_t kMaxRows = INT32_MAX - 4096;
+constexpr int64_t kMaxGroups = (1 << 24) - 1; // of 256 threads: a launch holds fewer than 2^32
 constexpr int64_t kMaxScanTokens = 1 << 30;   // of a sequence: token + segment stays in 32 bits
 
 bool head_size(int64_t d)
@@ -1115,7 +1116,7 @@ ssd_status attn_decode_check(const ssd_attn_dims *d, AttnShape *sh, int64_t *cac
         return SSD_ERR_SHAPE;
     *cache = t;
     const int64_t rtiles = (d->q_heads / d->kv_heads + 31) / 32;
-    if (d->batch * d->q_heads > INT32_MAX / 2 || d->batch * d->kv_heads * rtiles > INT32_MAX / 2)
+    if (d->batch * d->q_heads > INT32_MAX / 2 || d->batch * d->kv_heads * rtiles > kMaxGroups)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
@@ -1167,6 +1168,8 @@ SSD_EXPORT ssd_status ssd_linattn_decode_step(const ssd_linattn_dims *dims, cons
     const ssd_status st = linattn_dims_check(dims, dims ? dims->batch : 0, false, &sh);
     if (st != SSD_OK || dims->batch == 0)
         return st;
+    if (dims->batch * dims->v_heads * (dims->dv / 64) > kMaxGroups)
+        return SSD_ERR_UNSUPPORTED;
     if (!q || !k || !v || !log_decay || !state || !o)
         return SSD_ERR_NULL;
     if (!aligned(state, 16) || !aligned(q, sh.esz) || !aligned(k, sh.esz) || !aligned(v, sh.esz) ||

@@ -446,12 +446,12 @@ hipError_t prefill_launch(void (*kernel)(PrefillArgs), int64_t rows, int threads
     hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), (int)smem, allowed);
     if (e != hipSuccess)
         return e;
-    // launches of at most SeqTab::kMax sequences and 2^31 - 1 work-groups,
-    // the sequences with the most work per row block first
+    // launches of at most SeqTab::kMax sequences and 2^32 - 1 threads, the sequences
+    // with the most work per row block first
     for (int64_t at = 0; at < nseq;) {
         int n = 0;
         int64_t items = 0;
-        const int64_t most = INT32_MAX / args.Hkv;
+        const int64_t most = (int64_t)UINT32_MAX / threads / args.Hkv;
         while (at < nseq && n < SeqTab::kMax) {
             const int64_t blocks = (seqs[at].lq * (int64_t)args.grp + rows - 1) / rows;
             if (blocks > most - items)

@@ -753,7 +753,7 @@ hipError_t scan(LinArgs &args, int64_t nseq, const LinSeq *seqs, hipStream_t s)
     static_assert(SM::kScan + SM::kTables <= 160 * 1024, "LDS of a CU");
     static std::atomic<uint64_t> allow_state{0}, allow_scan{0};
     const int64_t T0 = args.seg_tokens, groups = (int64_t)args.Hv * (args.dv / (32 * NW));
-    const int64_t most = INT32_MAX / groups;
+    const int64_t most = (int64_t)UINT32_MAX / (64 * NW) / groups;   // a launch holds fewer than 2^32 threads
     int64_t slot = 0;
     for (int64_t at = 0; at < nseq;) {
         int n = 0;

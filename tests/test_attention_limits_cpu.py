@@ -2,7 +2,7 @@
 import ctypes
 
 import state_space_model_mamba_amd as ssd
-from test_attention_abi_cpu import attn, lib, lin, lin_scan, offsets  # noqa: F401 (lib: a fixture)
+from test_attention_abi_cpu import at, attn, lib, lin, lin_scan, offsets  # noqa: F401 (lib: a fixture)
 
 
 def test_scan_tokens(lib):  # noqa: F811
@@ -19,3 +19,20 @@ def test_scan_tokens(lib):  # noqa: F811
     size = lib.ssd_linattn_chunk_scan_varlen_workspace_size
     assert size(ctypes.byref(d), offsets(0, most, 2 * most), ctypes.byref(n)) == 0
     assert size(ctypes.byref(d), offsets(0, most - 1, 2 * most), ctypes.byref(n)) == 3
+
+
+def test_decode_launches(lib):  # noqa: F811
+    """A launch holds fewer than 2^32 threads: a step of more work-groups of 256 is
+    refused with the size, not by the device."""
+    n = ctypes.c_size_t(7)
+    size = lib.ssd_attn_decode_workspace_size
+    one = dict(kv_rows=1, head_dim=64)
+    for kw in (dict(batch=1 << 24, q_heads=1, kv_heads=1), dict(batch=1 << 22, q_heads=8, kv_heads=4),
+               dict(batch=1 << 22, q_heads=128, kv_heads=1)):
+        assert size(ctypes.byref(attn(**one, **kw)), ctypes.byref(n)) == 3
+        assert lib.ssd_attn_decode_step(ctypes.byref(attn(**one, **kw)), *[at(8 * i) for i in range(8)], 0, None) == 3
+        kw["batch"] -= 1
+        assert size(ctypes.byref(attn(**one, **kw)), ctypes.byref(n)) == 0
+    for kw in (dict(batch=1 << 24, v_heads=1, dv=64), dict(batch=1 << 20, v_heads=4, dv=256)):
+        d = lin(qk_heads=1, dk=64, **kw)
+        assert lib.ssd_linattn_decode_step(ctypes.byref(d), *[at(64 * i) for i in range(6)], None) == 3
