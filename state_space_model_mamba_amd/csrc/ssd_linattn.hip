@@ -111,6 +111,7 @@ template <typename T, int DK, int NW> struct LinSmem {
     static constexpr int kScan = kRing * (kScanSlot + kP);
     static constexpr int kStateRing = 3 * kStateSlot <= 159 * 1024 ? 3 : 2, kState = kStateRing * kStateSlot;
     static constexpr int kTables = ((kEpochTiles + 1) * C + kEpochTiles + 1) * 4;
+    static constexpr int kScanBytes = kScan + kTables;
 };
 
 // The state row (of a 32-row block) that register r of lane half hh holds.
@@ -746,11 +747,24 @@ hipError_t launch_part(void (*kernel)(LinArgs), int threads, int smem, std::atom
     return hipGetLastError();
 }
 
+// LDS bytes of a scan work-group, for the planner.
+template <typename T> int scan_lds_of(int64_t dk, int cols)
+{
+    if (cols == 128)
+        return dk == 64 ? LinSmem<T, 64, 4>::kScanBytes : LinSmem<T, 128, 4>::kScanBytes;
+    return dk == 64 ? LinSmem<T, 64, 2>::kScanBytes
+                    : dk == 128 ? LinSmem<T, 128, 2>::kScanBytes : LinSmem<T, 256, 2>::kScanBytes;
+}
+int scan_lds(int bf16, int64_t dk, int cols)
+{
+    return bf16 ? scan_lds_of<__bf16>(dk, cols) : scan_lds_of<float>(dk, cols);
+}
+
 template <typename T, int DK, int NW>
 hipError_t scan(LinArgs &args, int64_t nseq, const LinSeq *seqs, hipStream_t s)
 {
     typedef LinSmem<T, DK, NW> SM;
-    static_assert(SM::kScan + SM::kTables <= 160 * 1024, "LDS of a CU");
+    static_assert(SM::kScanBytes <= 160 * 1024, "LDS of a CU");
     static std::atomic<uint64_t> allow_state{0}, allow_scan{0};
     const int64_t T0 = args.seg_tokens, groups = (int64_t)args.Hv * (args.dv / (32 * NW));
     const int64_t most = (int64_t)UINT32_MAX / (64 * NW) / groups;   // a launch holds fewer than 2^32 threads
@@ -788,7 +802,7 @@ hipError_t scan(LinArgs &args, int64_t nseq, const LinSeq *seqs, hipStream_t s)
             }
             e = pass == 0 ? launch_part(&lin_state_kernel<T, DK, NW>, 64 * NW, SM::kState + SM::C * 4, allow_state,
                                         args, states * groups, s)
-                          : launch_part(&lin_scan_kernel<T, DK, NW>, 64 * NW, SM::kScan + SM::kTables, allow_scan,
+                          : launch_part(&lin_scan_kernel<T, DK, NW>, 64 * NW, SM::kScanBytes, allow_scan,
                                         args, items * groups, s);
             if (e != hipSuccess)
                 return e;
@@ -961,10 +975,9 @@ LinPlan plan_linattn(int bf16, int64_t nseq, const LinSeq *seqs, int64_t Hk, int
         const int64_t heads = Hv * (dv / cols);
         // work-groups of a CU: by LDS, and by registers (8 waves; 4 of the large heads
         // and of fp32)
-        const int64_t nw = cols / 32, slot_b = 32 * esz * (2 * dk + cols), p_b = 32 * 32 * esz;
-        const int64_t ring = nw == 4 && 3 * (slot_b + p_b) <= 158 * 1024 ? 3 : 2;
+        const int64_t nw = cols / 32;
         const int64_t per_cu = std::max<int64_t>(
-            1, std::min((bf16 && dk <= 128 ? 8 : 4) / nw, 160 * 1024 / (ring * (slot_b + p_b) + 1280)));
+            1, std::min<int64_t>((bf16 && dk <= 128 ? 8 : 4) / nw, 160 * 1024 / scan_lds(bf16, dk, cols)));
         const double slots = 256.0 * per_cu, w = dk / 128.0, waves = (double)nw;
         const double chain = !bf16 ? 1.8 + 4.6 * w : dk <= 128 ? 0.6 + 0.9 * w : 5.8;
         const double chain_state = !bf16 ? 0.7 + 2.4 * w : dk <= 128 ? 0.4 + 0.6 * w : 3.5;

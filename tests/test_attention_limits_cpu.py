@@ -36,3 +36,21 @@ def test_decode_launches(lib):  # noqa: F811
     for kw in (dict(batch=1 << 24, v_heads=1, dv=64), dict(batch=1 << 20, v_heads=4, dv=256)):
         d = lin(qk_heads=1, dk=64, **kw)
         assert lib.ssd_linattn_decode_step(ctypes.byref(d), *[at(64 * i) for i in range(6)], None) == 3
+
+
+def test_planner_segment_counts(lib):  # noqa: F811
+    """The scan planner's segment counts at shapes whose times are documented, read back
+    from the workspace size (one fp32 dk x dv state per head and segment of a sequence
+    of more than one)."""
+    for batch, seqlen, hk, hv, dk, dv, io, segments in (
+            (1, 77, 16, 32, 128, 128, ssd.SSD_BF16, 0),        # one: no workspace
+            (8, 2048, 8, 24, 128, 64, ssd.SSD_BF16, 4),
+            (4, 8192, 16, 32, 128, 128, ssd.SSD_BF16, 4),
+            (2, 4096, 16, 16, 256, 256, ssd.SSD_BF16, 4),
+            (1, 13384, 4, 4, 256, 64, ssd.SSD_BF16, 84),
+            (2, 1000, 4, 8, 64, 64, ssd.SSD_F32, 16),
+            (1, 11370, 1, 1, 256, 128, ssd.SSD_F32, 119)):
+        size = ssd.ssd_linattn_chunk_scan_workspace_size(batch, seqlen, hk, hv, dk, dv, io)
+        assert size == batch * segments * hv * dk * dv * 4, (seqlen, dk, dv, size / (batch * hv * dk * dv * 4))
+    cu = [0, 8192, 12289, 15289, 17337, 18837, 19861, 20638, 21150]
+    assert ssd.ssd_linattn_chunk_scan_varlen_workspace_size(cu, 16, 32, 128, 128) == 12 * 32 * 128 * 128 * 4
