@@ -330,9 +330,9 @@ ssd_status ssd_gdn_decode_steps(const ssd_gdn_dims *dims, int64_t nsteps, const 
  * run at the same time (also per captured graph that may).  Results are
  * deterministic, and a packed batch gives what its sequences give one by one up
  * to rounding.  The scan gives what the recurrence gives while the products
- * q . k and k v, the states and the outputs are finite fp32 numbers; in bf16,
- * terms below 2^-70 may lose bits, and in both types powers of lambda below
- * 2^-126 count as 0.  In bf16 a state carries 2^-24 of every product k v that it
+ * q . k and k v, the states and the outputs are finite fp32 numbers; terms k v
+ * and q . S below 2^-60 may lose bits, and powers of lambda below 2^-126 count as
+ * 0.  In bf16 a state carries 2^-24 of every product k v that it
  * has held as error, beside fp32's roundings of what is left of it.  An infinity or NaN in v reaches its own sequence only,
  * there also the tokens up to 31 before it.
  */

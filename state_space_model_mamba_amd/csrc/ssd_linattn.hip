@@ -12,8 +12,9 @@
 // with weights from a table, and R is multiplied by lambda^N once per epoch: every
 // kEpochTiles tiles, or sooner, before the weights would fall below 2^-kEpoch.  A head
 // that forgets more than that within a tile is scaled every tile instead.  No weight
-// passes 1, so R overflows only where S does; below, terms keep their 24 bits down to
-// 2^(kEpoch-110).  Powers of lambda are formed from the exponent in fp64 (in fp32 they
+// passes 1, so R overflows only where S does; below, terms of S (three bf16 numbers)
+// keep their 24 bits down to 2^(kEpoch-110) and those of q . S down to 2^(kEpoch-102).
+// Powers of lambda are formed from the exponent in fp64 (in fp32 they
 // would be off by up to kEpoch 2^-24 relative).
 //
 // Rounding (bf16): q, k, v are exact operands.  The state and the masked scores
@@ -482,6 +483,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
     if (tid <= kEpochTiles)
         spow[tid] = direct ? 1.f : pow_of(g2, tid * C - N);
     const float ft = scale * pow_of(g2, cl + 1);          // scale lambda^(t+1), the lane's token t
+    const bool wide = fabsf(scale) > 0x1p80f;             // times lambda^-N may pass fp32
     // the wave's 16 x 16 blocks of a tile's masked scores (transposed: s x t): factors
     // scale lambda^(t-s), and the scores of the tile in `slot` into its P buffer
     constexpr int kBlk = 4 / NW;
@@ -636,7 +638,7 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
 #pragma unroll
             for (int i = 0; i < TK::kPieces; ++i)
                 qf[i] = BK::piece32(SM::kK + SM::kV, bqo, i);
-        const float f = ft * spow[ep];
+        float f = ft * spow[ep];
         step();
         score_store(kAhead ? next : slot, in);
 #pragma unroll
@@ -670,6 +672,12 @@ __global__ __launch_bounds__(64 * NW, DK == 256 || sizeof(T) == 4 ? 1 : 2) void 
         }
         update<T, DK, kTerms>(R, bko, vf, kf, [&](int i, int j) { return i == 0 ? uw[j] : weight4(i, j); });
 
+        if (wide) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                y[r] *= spow[ep];
+            f = ft;
+        }
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             y[r] *= f;

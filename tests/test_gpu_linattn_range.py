@@ -30,6 +30,20 @@ def test_large_and_small_values(io, dk, dv, power):
     within(host(fin[0]) / f, rS, bS, "state")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("power", [-110, 115])
+def test_large_and_small_scales(io, power):
+    """Outputs near the ends of the range by their scale: no factor on the way leaves it.
+    (Values of the inverse size are not tried: q . S must stay above 2^-60, since the
+    products behind it carry weights down to 2^-40 and fp32 ends at 2^-126.)"""
+    L, hv, dk, dv, f = 400, len(DECAYS), 64, 64, 2.0 ** power
+    q, k, v, g, S0 = inputs(power + 200, io, (1, L), 2, hv, dk, dv, 1, g=DECAYS)
+    o, _ = ssd.ssd_linattn_chunk_scan(q[0], k[0], v[0], g[0], initial_state=S0[0], scale=f)
+    ro, _, ao, A = att.linattn(q[1][0], k[1][0], v[1][0], g[1], S0[1][0])
+    bo, _ = lin_bounds(io, ro, ao, A, L, dk)
+    within(host(o[0]) / f, ro, bo, "o")
+
+
 def one_token_state(dev, g, n, k, v, L):
     """A state whose only term is lambda^n k v, against the formula.
 
