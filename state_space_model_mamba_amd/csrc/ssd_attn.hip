@@ -24,9 +24,13 @@ using namespace mx;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;
 constexpr float kNoMax = -3e38f;   // m before the first visible key (finite: m - m is 0)
-// A scale of 0 weights all visible keys alike; it is kept off 0 so that a masked
-// score (-inf) times it stays -inf.
-constexpr float kTinyScale = 1.17549435e-38f;
+// |scale| log2 e.  A scale of 0 weights all visible keys alike; it is kept off 0 so
+// that a masked score (-inf) times it stays -inf, and finite so that a score of 0 times
+// it stays 0.
+float score_factor(float scale)
+{
+    return std::clamp(std::abs(scale) * kLog2e, 1.17549435e-38f, 3.40282347e38f);
+}
 
 // s c - m, the product rounded before the difference as it is in m: for the largest
 // score of a row exactly 0 however large it is.  (Fused, the rounding of m remains;
@@ -754,7 +758,7 @@ hipError_t launch_attn_prefill(int bf16, int64_t nseq, const AttnSeq *seqs, int6
     args.Hq = (int)Hq;
     args.Hkv = (int)Hkv;
     args.grp = (int)(Hq / Hkv);
-    args.c = std::max(std::abs(scale) * kLog2e, kTinyScale);
+    args.c = score_factor(scale);
     args.neg = scale < 0.f;
     if (bf16) {
         switch (D) {
@@ -815,7 +819,7 @@ hipError_t launch_attn_decode(int bf16, int64_t B, int64_t M, int64_t Hq, int64_
     a.rtiles = (a.grp + 31) / 32;
     a.chunk = (int)decode_chunk(B, M, Hkv, a.rtiles);
     a.nsplit = (int)attn_decode_splits(B, M, Hq, Hkv);
-    a.c = std::max(std::abs(scale) * kLog2e, kTinyScale);
+    a.c = score_factor(scale);
     a.neg = scale < 0.f;
     a.part = static_cast<float *>(ws);
     a.ml = reinterpret_cast<float2 *>(a.part + B * Hkv * a.rtiles * (int64_t)a.nsplit * 32 * D);

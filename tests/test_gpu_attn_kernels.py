@@ -92,3 +92,20 @@ def test_scores_of_minus_infinity(io):
         o = ssd.ssd_attn_decode_step(qq[-1:], kk[-1:], v[0][-1:], kc, vc, at)
         want = v[0][40].repeat_interleave(hq // hkv, dim=0)
         assert torch.equal(o[0], want), f"capacity {M}"
+
+
+@pytest.mark.parametrize("scale", [3.4e38, -3.4e38])
+def test_largest_scales(scale):
+    """Scores of 0 are 0 at every finite scale: equal weights."""
+    L, hq, hkv, d = 40, 4, 2, 64
+    q, k, v = prompt(12, "f32", L, L, hq, hkv, d)
+    zero = torch.zeros_like(k[0])
+    n = torch.arange(1, L + 1, device="cuda")[:, None, None]
+    want, size = (x.cumsum(0).repeat_interleave(2, dim=1) / n for x in (v[0].double(), v[0].double().abs()))
+    o = ssd.ssd_attn_prefill(q[0], zero, v[0], [0, L], scale=scale)
+    # L terms of weight 1 and their sum in fp32, a division, a product
+    assert ((o - want).abs() <= (L + 4) * 2.0 ** -24 * size).all()
+    kc, vc = zero[None].clone(), v[0][None].clone()
+    at = torch.tensor([L - 1], dtype=torch.int32, device="cuda")
+    o = ssd.ssd_attn_decode_step(q[0][-1:], zero[-1:], v[0][-1:], kc, vc, at, scale=scale)
+    assert ((o[0] - want[-1]).abs() <= (L + 4) * 2.0 ** -24 * size[-1]).all()
