@@ -666,6 +666,10 @@ def ssd_linattn_decode_step(q, k, v, log_decay, state, o=None, scale=1.0, stream
     return o
 
 
+def _attn_scale(scale, D):
+    return max(D, 1) ** -0.5 if scale is None else scale
+
+
 def ssd_attn_prefill(q, k, v, cu_seqlens, kv_starts=None, kv_lens=None, scale=None, o=None,
                      stream=None):
     """Causal softmax attention over packed prompts: q [T, Hq, D], k, v [Tk, Hkv, D];
@@ -686,7 +690,7 @@ def ssd_attn_prefill(q, k, v, cu_seqlens, kv_starts=None, kv_lens=None, scale=No
     st, stp = (None, None) if kv_starts is None else _offsets("kv_starts", kv_starts, len(cu) - 1)
     kl, klp = (None, None) if kv_lens is None else _offsets("kv_lens", kv_lens, len(cu) - 1)
     d = SsdAttnDims(len(cu) - 1, T, Tk, Hq, Hkv, D, qs, ks, vs,
-                    D ** -0.5 if scale is None else scale, _io_dtype(q))
+                    _attn_scale(scale, D), _io_dtype(q))
     with _guard(dev):
         if o is None:
             with _on(stream):
@@ -727,7 +731,7 @@ def ssd_attn_decode_step(q, k, v, k_cache, v_cache, lengths, scale=None, o=None,
     _need("o", o, dev, q.dtype, q.shape, optional=True)
     _need("workspace", workspace, dev, optional=True)
     lib = load()
-    d = SsdAttnDims(B, 0, M, Hq, Hkv, D, qs, ks, vs, D ** -0.5 if scale is None else scale,
+    d = SsdAttnDims(B, 0, M, Hq, Hkv, D, qs, ks, vs, _attn_scale(scale, D),
                     _io_dtype(q))
     need = 0
     if workspace is None:

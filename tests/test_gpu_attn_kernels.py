@@ -109,3 +109,13 @@ def test_largest_scales(scale):
     at = torch.tensor([L - 1], dtype=torch.int32, device="cuda")
     o = ssd.ssd_attn_decode_step(q[0][-1:], zero[-1:], v[0][-1:], kc, vc, at, scale=scale)
     assert ((o[0] - want[-1]).abs() <= (L + 4) * 2.0 ** -24 * size[-1]).all()
+
+
+def test_heads_of_no_width_are_refused():
+    x = torch.empty(4, 2, 0, dtype=torch.bfloat16, device="cuda")
+    c = torch.empty(4, 8, 2, 0, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: ssd.ssd_attn_prefill(x, x, x, [0, 4]),
+                 lambda: ssd.ssd_attn_decode_step(x, x, x, c, c, torch.zeros(4, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ssd.SsdError) as e:
+            call()
+        assert e.value.code == 3
