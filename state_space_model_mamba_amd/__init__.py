@@ -630,7 +630,7 @@ def ssd_linattn_chunk_scan(q, k, v, log_decay, initial_state=None, o=None, final
 
 def ssd_linattn_chunk_scan_varlen_workspace_size(cu_seqlens, qk_heads, v_heads, dk, dv,
                                                  io_dtype=SSD_BF16) -> int:
-    cu, cup = _cu_array(cu_seqlens)
+    cu, cup = _offsets("cu_seqlens", cu_seqlens)
     d = SsdLinattnDims(len(cu) - 1, int(cu[-1]), qk_heads, v_heads, dk, dv, 0, 0, 0, 1.0, io_dtype)
     n = ctypes.c_size_t(0)
     _check("ssd_linattn_chunk_scan_varlen_workspace_size",

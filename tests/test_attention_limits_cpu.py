@@ -1,6 +1,8 @@
 """Sizes at the attention layers' limits (CPU only: no call here reaches a launch)."""
 import ctypes
 
+import pytest
+
 import state_space_model_mamba_amd as ssd
 from test_attention_abi_cpu import at, attn, lib, lin, lin_scan, offsets  # noqa: F401 (lib: a fixture)
 
@@ -54,3 +56,13 @@ def test_planner_segment_counts(lib):  # noqa: F811
         assert size == batch * segments * hv * dk * dv * 4, (seqlen, dk, dv, size / (batch * hv * dk * dv * 4))
     cu = [0, 8192, 12289, 15289, 17337, 18837, 19861, 20638, 21150]
     assert ssd.ssd_linattn_chunk_scan_varlen_workspace_size(cu, 16, 32, 128, 128) == 12 * 32 * 128 * 128 * 4
+
+
+def test_offsets_of_a_size_query():
+    size = ssd.ssd_linattn_chunk_scan_varlen_workspace_size
+    for cu in ([], [[0, 4]]):
+        with pytest.raises(ValueError):
+            size(cu, 1, 1, 64, 64)
+    with pytest.raises(ssd.SsdError) as e:               # one offset, not 0
+        size(5, 1, 1, 64, 64)
+    assert e.value.code == 2
