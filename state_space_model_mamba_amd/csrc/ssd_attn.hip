@@ -497,11 +497,13 @@ hipError_t prefill(PrefillArgs &args, int64_t nseq, const AttnSeq *seqs, hipStre
     //        128  28/52, 343/761   58/97, 675/804   122/143, 1053/850  192/188, 1433/896
     //        256  115/152, 1762/2590  242/321, 3547/2736  555/485, 5415/2886  905/639, 7430/3037
     // 8 heads over 8 (longer sequences at the same n) cross at the same n or up to half
-    // as much again later.
+    // as much again later.  Prompts alone cross later than queries after cached keys
+    // (their row blocks differ in length and even out): the limits lie between.
+    constexpr int64_t kFew = sizeof(T) == 2 ? 512 : D == 64 ? 1024 : D == 128 ? 768 : 512;
     int64_t blocks = 0;
     for (int64_t i = 0; i < nseq && blocks < (int64_t(1) << 32); ++i)
         blocks += (seqs[i].lq * (int64_t)args.grp + 31) / 32;
-    if (blocks * args.Hkv <= (sizeof(T) == 2 ? 512 : 65536 / D))
+    if (blocks * args.Hkv <= kFew)
         return prefill_launch(&attn_prefill_few_kernel<T, D>, 32, 64 * WaveTiles<T, D>::kWaves,
                               WaveTiles<T, D>::kSmem, allowed_few, args, nseq, seqs, s);
     constexpr unsigned kSmem = 4u * (sizeof(T) == 2 ? 64 : 32) * D * sizeof(T);

@@ -14,8 +14,8 @@ MANY = 4096
 
 
 # the limit, in work-groups of 32 rows
-FEW = {("bf16", 64): 512, ("bf16", 128): 512, ("bf16", 256): 512, ("f32", 64): 1024, ("f32", 128): 512,
-       ("f32", 256): 256}
+FEW = {("bf16", 64): 512, ("bf16", 128): 512, ("bf16", 256): 512, ("f32", 64): 1024, ("f32", 128): 768,
+       ("f32", 256): 512}
 
 
 def heads_for(L):
