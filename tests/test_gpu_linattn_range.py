@@ -2,6 +2,7 @@
 which little is left."""
 import numpy as np
 import pytest
+import torch
 
 import state_space_model_mamba_amd as ssd
 from attention_cases import host, lin_bounds, within
@@ -84,3 +85,16 @@ def test_states_handed_between_segments(dk, dv):
     k[0][:, :at], k[0][:, at + 1:] = 0, 0
     _, fin = ssd.ssd_linattn_chunk_scan(q[0], k[0], v[0], g[0])
     one_token_state(fin, g[1][None], L - 1 - at, np.repeat(k[1][:, at], 3, axis=1), v[1][:, at], L)
+
+
+def test_the_same_layer_through_the_ssd_scan():
+    """128 keys by 64 values in bf16 are an SSD layer with dt = 1, A = g, D = 0: the
+    same recurrence through the other kernels, its state transposed."""
+    B, L, hk, hv, dk, dv = 2, 700, 2, 4, 128, 64
+    q, k, v, g, _ = inputs(3, "bf16", (B, L), hk, hv, dk, dv, B, init=False, g=[-0.003, -0.05, -0.3, -1.0])
+    o, fin = ssd.ssd_linattn_chunk_scan(q[0], k[0], v[0], g[0])
+    y, H = ssd.ssd_chunk_scan(v[0], torch.ones(B, L, hv, device="cuda"), g[0], k[0], q[0],
+                              torch.zeros(hv, device="cuda"), 256)
+    for a, b in ((y, o), (H.transpose(2, 3), fin)):       # the SSD scan's bound in bf16: 2e-2
+        e = torch.linalg.vector_norm((a - b).double()) / torch.linalg.vector_norm(b.double())
+        assert e < 2e-2, f"off by {e:.2e}"
