@@ -83,6 +83,8 @@ __device__ __forceinline__ void tile32(const unsigned char *Kt, const unsigned c
         s[r] = exp2_fast(below_max(s[r], c, m));
         l += s[r];
     }
+    // the probabilities are rounded to the operand type once, unnormalised (bf16: off by
+    // up to 2^-8 of each, as the output's own rounding; the sum l takes them unrounded)
 #pragma unroll
     for (int p = 0; p < PC; ++p) {
         const typename Piece<T>::V pf = acc_piece(s, p, (const T *)nullptr);
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void attn_prefill_kernel
                 l += e;
                 s[kb][r] = e;
             }
-            // the probabilities are rounded to the operand type once, unnormalised
+            // (rounded once, as in tile32)
 #pragma unroll
             for (int p = 0; p < PC; ++p)
                 pf[kb * PC + p] = acc_piece(s[kb], p, (const T *)nullptr);

@@ -26,17 +26,20 @@
 // no token's rounding is larger than 2^-24 of its product, whatever follows it.  (Three
 // throughout: 273 against 255 us for the scan below.)
 //
-// Bound by memory: q, k, v and o move once in the scan; a sequence cut into
-// segments, to fill the chip, has all but its last segment's k and v read a second
-// time by the state kernel.  4 x 8192 tokens of 32 heads of 128 x 128 over 16 (bf16,
-// 4 segments): 250 - 256 us in all, the scan 135 - 165 us of it for 814 MB (a copy
-// moves 4.8 TB/s on the same card: 170 us; part of k and v is still in the
-// memory-side cache), the state kernel 80 us.  What the scan needed for that: two
-// work-groups per CU (32-token tiles; 64-token ones left room for one, 450 us in
-// all), every wave forming a share of the next tile's scores (338 us before), no
-// register spilled inside the loop (a spill's reload waits for the tiles on their
-// way: 2 to 3 times slower), few vector instructions beside the products (one base
-// register per LDS operand, weights from a table).
+// q, k, v and o move once in the scan; a sequence cut into segments, to fill the chip,
+// has all but its last segment's k and v read a second time by the state kernel.  4 x
+// 8192 tokens of 32 heads of 128 x 128 over 16 (bf16, 4 segments): 250 - 256 us in all,
+// the scan 134 - 180 us of it for 850 MB counted (bound by memory: a copy moves 4.8
+// TB/s on the same card, 180 us; part of k and v is still in the memory-side cache),
+// the state kernel 87 - 102 us for 223 MB (bound by its chain of up to 64 tiles, about
+// 1.4 us each; heads that forget fast stop early).  What the scan needed for that: two
+// work-groups per CU (32-token tiles; 64-token ones left room for one, 450 us in all),
+// every wave forming a share of the next tile's scores (338 us before), no register
+// spilled inside the loop (a spill's reload waits for the tiles on their way: 2 to 3
+// times slower), few vector instructions beside the products (one base register per LDS
+// operand, weights from a table).  With 256 keys the registers do not suffice: bf16
+// reloads 20 from scratch in each tile and moves 520 to or from the accumulators (6 us
+// a tile), fp32 reloads up to 9, and 3 with 128 keys by 64 columns.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -320,8 +320,8 @@ __device__ __forceinline__ unsigned lds_addr(const void *p)
         (int)(unsigned)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
 }
 
-// A wave's share of loading a [kRows][D] tile: 1 KB blocks w, w + kWaves, ..,
-// lane l writing bytes 16 l .. 16 l + 15 of each, so the chunk permutation is
+// A wave's share of loading a [kRows][D] tile: the 1 KB blocks from w kPer on, lane l
+// writing bytes 16 l .. 16 l + 15 of each, so the chunk permutation is
 // applied to the source.  Rows past the last valid one repeat it: what is
 // masked afterwards is then finite whenever the sequence's own values are, and
 // nothing outside the sequence is read.
