@@ -42,8 +42,11 @@ __device__ __forceinline__ float below_max(float s, float c, float m)
 }
 
 // A 32-key tile in a wave's own LDS, for 32 rows (score columns): updates (m, l,
-// acc).  Keys from `see` (per lane) on are masked if `masked` (wave-uniform).
-template <typename T, int D>
+// acc).  Keys from `see` (per lane) on are masked if `masked` (wave-uniform).  The
+// probabilities, unnormalised, are the second product's operand as kTerms numbers of
+// its type: in bf16 one is off by up to 2^-8, as the output's own rounding, two by up
+// to 2^-17.  (The sum l takes them unrounded.)
+template <typename T, int D, int kTerms>
 __device__ __forceinline__ void tile32(const unsigned char *Kt, const unsigned char *Vt,
                                        const typename Piece<T>::V (&qf)[Tile<T, D>::kPieces], bool masked,
                                        int see, float c,
@@ -83,14 +86,24 @@ __device__ __forceinline__ void tile32(const unsigned char *Kt, const unsigned c
         s[r] = exp2_fast(below_max(s[r], c, m));
         l += s[r];
     }
-    // the probabilities are rounded to the operand type once, unnormalised (bf16: off by
-    // up to 2^-8 of each, as the output's own rounding; the sum l takes them unrounded)
 #pragma unroll
     for (int p = 0; p < PC; ++p) {
-        const typename Piece<T>::V pf = acc_piece(s, p, (const T *)nullptr);
+        typename Piece<T>::V pf[kTerms];
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-            acc[d] = mma(TL::col_acc(Vt, p, 32 * d, lane), pf, acc[d]);
+        for (int i = 0; i < kTerms; ++i) {
+            pf[i] = acc_piece(s, p, (const T *)nullptr);
+            if (i + 1 < kTerms)
+#pragma unroll
+                for (int e = 0; e < Piece<T>::E; ++e)
+                    s[Piece<T>::E * p + e] -= (float)pf[i][e];
+        }
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+            const typename Piece<T>::V v = TL::col_acc(Vt, p, 32 * d, lane);
+#pragma unroll
+            for (int i = 0; i < kTerms; ++i)
+                acc[d] = mma(v, pf[i], acc[d]);
+        }
     }
 }
 
@@ -330,7 +343,8 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void attn_prefill_kernel
                 l += e;
                 s[kb][r] = e;
             }
-            // (rounded once, as in tile32)
+            // (one operand each, as in tile32: two would be half as many matrix
+            // instructions again in a kernel that they bound)
 #pragma unroll
             for (int p = 0; p < PC; ++p)
                 pf[kb * PC + p] = acc_piece(s[kb], p, (const T *)nullptr);
@@ -432,7 +446,7 @@ __global__ __launch_bounds__((64 * WaveTiles<T, D>::kWaves), 1) void attn_prefil
             wait_vmcnt<0>();
         }
         const unsigned char *Kt = mine + (n & 1) * 2 * GM::kTileBytes, *Vt = Kt + GM::kTileBytes;
-        tile32<T, D>(Kt, Vt, qf, t0 + 32 > kall, lim - t0, a->c, lane, m, l, acc);
+        tile32<T, D, 1>(Kt, Vt, qf, t0 + 32 > kall, lim - t0, a->c, lane, m, l, acc);
     }
     T *o = (T *)a->o;
     join_waves<T, D>(smem, sm, sl, w, lane, rows, m, l, acc, [&](int i, f32x4 v, float, float lr) {
@@ -640,7 +654,8 @@ __global__ __launch_bounds__((64 * WaveTiles<T, D>::kWaves), 1) void attn_decode
             put_rows<T, D>(Vt, vn, at - t0, lane);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
-        tile32<T, D>(Kt, Vt, qf, t0 + 32 > kend, kend - t0, a.c, lane, m, l, acc);
+        // (two terms: the matrix units are idle most of the time here)
+        tile32<T, D, sizeof(T) == 2 ? 2 : 1>(Kt, Vt, qf, t0 + 32 > kend, kend - t0, a.c, lane, m, l, acc);
     }
     const int64_t slot = ((int64_t)item * a.nsplit + split) * 32;
     join_waves<T, D>(smem, sm, sl, w, lane, rows, m, l, acc, [&](int i, f32x4 v, float mr, float lr) {

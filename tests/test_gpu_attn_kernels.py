@@ -1,10 +1,13 @@
 """Softmax attention: the prefill kernel of large row blocks at scales and scores where
 it can go wrong, and the same sequence through every path."""
+import numpy as np
 import pytest
 import torch
 
 import state_space_model_mamba_amd as ssd
-from test_gpu_attn import check, prompt
+from attention_cases import U, attn_bound, within
+from oracle import attention as att
+from test_gpu_attn import check, prompt, step_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +122,19 @@ def test_heads_of_no_width_are_refused():
         with pytest.raises(ssd.SsdError) as e:
             call()
         assert e.value.code == 3
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (8, 2, 128), (4, 4, 256), (40, 1, 128)])
+@pytest.mark.parametrize("M", [100, 2000])
+def test_step_rounds_once(hq, hkv, d, M):
+    """The bf16 step's only rounding to 8 bits is the output's: its probabilities enter
+    as two bf16 numbers, off by up to 2^-17 of each."""
+    q, k, v, kc, vc = step_inputs(M + d, "bf16", 3, M, hq, hkv, d)
+    lengths = [M - 1, M // 3, 0]
+    o = ssd.ssd_attn_decode_step(q[0], k[0], v[0], kc[0], vc[0],
+                                 torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+    for b, n in enumerate(lengths):
+        kk, vv = (np.concatenate([c[1][b, :n], x[1][b:b + 1]]) for c, x in ((kc, k), (vc, v)))
+        ro, ao, big = att.attn(q[1][b:b + 1], kk, vv, d ** -0.5)
+        bound = attn_bound("f32", ro, ao, big, n + 1, d) + U["bf16"] * np.abs(ro) * 1.01 + 1.01 * 2.0 ** -17 * ao
+        within(o[b:b + 1], ro, bound, f"{n} rows")
