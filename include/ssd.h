@@ -323,18 +323,19 @@ ssd_status ssd_gdn_decode_steps(const ssd_gdn_dims *dims, int64_t nsteps, const 
  * tokens (rows b L + t of the scan) in elements, 0 for contiguous rows.  o is
  * contiguous.  A sequence of length 0 hands its state through.
  * Supported: dk, dv in {64, 128, 256}, strides up to 2^22, sequences up to 2^30
- * tokens, decode steps of B Hv dv < 2^30, io_dtype SSD_F32 or SSD_BF16.  Scan alignment: q, k, v, o, states and workspace 16 bytes, strides
- * whole 16 bytes; decode step: state 16 bytes, the rest element-aligned.  o
- * must not overlap any input, state or the workspace, a final state no input.
+ * tokens, decode steps of B Hv dv < 2^30, io_dtype SSD_F32 or SSD_BF16.
+ * Scan alignment: q, k, v, o, states and workspace 16 bytes, strides whole 16
+ * bytes; decode step: state 16 bytes, the rest element-aligned.  o must not
+ * overlap any input, state or the workspace, a final state no input.
  * The workspace holds states between the call's kernels: one per call that may
  * run at the same time (also per captured graph that may).  Results are
  * deterministic, and a packed batch gives what its sequences give one by one up
  * to rounding.  The scan gives what the recurrence gives while the products
  * q . k and k v, the states and the outputs are finite fp32 numbers; terms k v
  * and q . S below 2^-60 may lose bits, and powers of lambda below 2^-126 count as
- * 0.  In bf16 a state carries 2^-24 of every product k v that it
- * has held as error, beside fp32's roundings of what is left of it.  An infinity or NaN in v reaches its own sequence only,
- * there also the tokens up to 31 before it.
+ * 0.  In bf16 a state is off by up to 2^-24 of every product k v that it has
+ * held, beside fp32's roundings of what is left of it.  An infinity or NaN in v
+ * reaches its own sequence only, there also the tokens up to 31 before it.
  */
 typedef struct ssd_linattn_dims {
     int64_t batch;     /* B >= 0 (sequences)                                  */

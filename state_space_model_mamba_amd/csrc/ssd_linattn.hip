@@ -14,8 +14,8 @@
 // that forgets more than that within a tile is scaled every tile instead.  No weight
 // passes 1, so R overflows only where S does; below, terms of S (three bf16 numbers)
 // keep their 24 bits down to 2^(kEpoch-110) and those of q . S down to 2^(kEpoch-102).
-// Powers of lambda are formed from the exponent in fp64 (in fp32 they
-// would be off by up to kEpoch 2^-24 relative).
+// Powers of lambda are formed from the exponent in fp64 (in fp32 they would be off by
+// up to kEpoch 2^-24 relative).
 //
 // Rounding (bf16): q, k, v are exact operands.  The state and the masked scores
 // are each rounded once to bf16 on their way into the products that form o
