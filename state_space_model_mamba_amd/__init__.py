@@ -162,12 +162,12 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _io_dtype(t):
+def _io_dtype(t, names="x/B/C"):
     if t.dtype == torch.bfloat16:
         return SSD_BF16
     if t.dtype == torch.float32:
         return SSD_F32
-    raise TypeError(f"x/B/C must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"{names} must be bfloat16 or float32, got {t.dtype}")
 
 
 def _need(name, t, di, dtype=None, shape=None, optional=False):
@@ -446,7 +446,7 @@ def ssd_gdn_decode_step(q, k, v, g, beta, state, o=None, stream=None):
     _need("beta", beta, dev, f32, (bsz, Hv))
     _need("state", state, dev, f32, (bsz, Hv, dk, dv))
     _need("o", o, dev, q.dtype, v.shape, optional=True)
-    d = SsdGdnDims(bsz, Hk, Hv, dk, dv, _io_dtype(q), 0)
+    d = SsdGdnDims(bsz, Hk, Hv, dk, dv, _io_dtype(q, "q/k/v"), 0)
     if o is None:
         with _on(stream):
             o = torch.empty_like(v)
@@ -472,7 +472,7 @@ def ssd_gdn_decode_steps(q, k, v, g, beta, state, o=None, stream=None):
     _need("beta", beta, dev, f32, (nsteps, bsz, Hv))
     _need("state", state, dev, f32, (bsz, Hv, dk, dv))
     _need("o", o, dev, q.dtype, v.shape, optional=True)
-    d = SsdGdnDims(bsz, Hk, Hv, dk, dv, _io_dtype(q), 0)
+    d = SsdGdnDims(bsz, Hk, Hv, dk, dv, _io_dtype(q, "q/k/v"), 0)
     if o is None:
         with _on(stream):
             o = torch.empty_like(v)
@@ -567,7 +567,7 @@ def _linattn_dims(q, k, v, lead, batch, seqlen, scale, dev):
     return SsdLinattnDims(batch, seqlen, shp[-2], vshp[-2], shp[-1], vshp[-1],
                           _row_stride("q", q, dev, dtype, shp),
                           _row_stride("k", k, dev, dtype, shp),
-                          _row_stride("v", v, dev, dtype, vshp), scale, _io_dtype(q))
+                          _row_stride("v", v, dev, dtype, vshp), scale, _io_dtype(q, "q/k/v"))
 
 
 def _linattn_scan(fn, lead, q, k, v, log_decay, cu_seqlens, initial_state, o, final_state, workspace,
@@ -690,7 +690,7 @@ def ssd_attn_prefill(q, k, v, cu_seqlens, kv_starts=None, kv_lens=None, scale=No
     st, stp = (None, None) if kv_starts is None else _offsets("kv_starts", kv_starts, len(cu) - 1)
     kl, klp = (None, None) if kv_lens is None else _offsets("kv_lens", kv_lens, len(cu) - 1)
     d = SsdAttnDims(len(cu) - 1, T, Tk, Hq, Hkv, D, qs, ks, vs,
-                    _attn_scale(scale, D), _io_dtype(q))
+                    _attn_scale(scale, D), _io_dtype(q, "q/k/v"))
     with _guard(dev):
         if o is None:
             with _on(stream):
@@ -732,7 +732,7 @@ def ssd_attn_decode_step(q, k, v, k_cache, v_cache, lengths, scale=None, o=None,
     _need("workspace", workspace, dev, optional=True)
     lib = load()
     d = SsdAttnDims(B, 0, M, Hq, Hkv, D, qs, ks, vs, _attn_scale(scale, D),
-                    _io_dtype(q))
+                    _io_dtype(q, "q/k/v"))
     need = 0
     if workspace is None:
         n = ctypes.c_size_t(0)

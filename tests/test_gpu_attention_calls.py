@@ -110,3 +110,16 @@ def test_two_graphs_of_one_step():
             torch.cuda.synchronize()
             assert torch.equal(o, want)
             assert torch.equal(ssd.ssd_attn_decode_step(q[0], k[0], v[0], kc[0], vc[0], n), want)
+
+
+def test_other_types_are_refused_by_name():
+    x, g = torch.zeros(2, 8, 1, 64, dtype=torch.float16, device="cuda"), torch.zeros(1, device="cuda")
+    n = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for call in (lambda: ssd.ssd_linattn_chunk_scan(x, x, x, g),
+                 lambda: ssd.ssd_linattn_decode_step(x[:, 0], x[:, 0], x[:, 0], g, torch.zeros(2, 1, 64, 64, device="cuda")),
+                 lambda: ssd.ssd_attn_prefill(x[0], x[0], x[0], [0, 8]),
+                 lambda: ssd.ssd_attn_decode_step(x[:, 0], x[:, 0], x[:, 0], x, x.clone(), n),
+                 lambda: ssd.ssd_gdn_decode_step(*(x[:, 0].contiguous(),) * 3, g.expand(2, 1).contiguous(),
+                                                 g.expand(2, 1).contiguous(), torch.zeros(2, 1, 64, 64, device="cuda"))):
+        with pytest.raises(TypeError, match="q/k/v must be bfloat16 or float32"):
+            call()
