@@ -6,7 +6,8 @@
  * Gated DeltaNet decode step of the FPGA decode page (ssd_gdn_*), and the two
  * attention layers of hybrid stacks: linear attention with one decay per head
  * (ssd_linattn_*) and causal softmax attention (ssd_attn_*), each over prompts
- * and for single tokens.
+ * and for single tokens, with the norm and rotation of the latter's queries and
+ * keys and a paged key/value cache in the input type or in 4 bits.
  *
  * The operation.  "Compiler-First State Space Duality and Portable O(1)
  * Autoregressive Caching for Inference" (section 2, methodology) describes
@@ -422,6 +423,130 @@ ssd_status ssd_attn_decode_step(const ssd_attn_dims *dims, const void *q, const 
                                 const void *v, void *k_cache, void *v_cache,
                                 const int32_t *lengths, void *o, void *workspace,
                                 size_t workspace_bytes, void *stream);
+
+/*
+ * The rest of a softmax layer's serving path: the norm and rotation of its queries and
+ * keys, and a paged cache.
+ *
+ * Pages.  k_pages and v_pages are [num_pages, Hkv, page_size, D]; row r of sequence b is
+ * line r % page_size of page block_table[b, r / page_size], for all key heads.
+ * block_table [B, max_pages] int32 is a DEVICE array (as lengths is): an entry outside
+ * [0, num_pages) is no page.  Sequences may share pages that no call writes while they
+ * do.  Page formats (ssd_paged_dims.page_format):
+ *   SSD_PAGES_IO    the input type
+ *   SSD_PAGES_4BIT  [num_pages, Hkv, page_size, D / 2] bytes, value 2 i in the low half
+ *                   of byte i and 2 i + 1 in the high half, and k_scales, v_scales
+ *                   [num_pages, Hkv, page_size, D / 64, 2] in IEEE half precision: for
+ *                   every 64 values a step s and a least value m, value = code s + m.
+ *                   Written as m = half(min), s = half((max - min) / 15), both held
+ *                   within +-65504, code = round((x - m) / s) within 0 .. 15 (ties to
+ *                   even; 0 where s is 0).  Values within +-65504 are off by half a step
+ *                   at most, beside the roundings of m and s.
+ * Supported: D in {64, 128, 256}, page_size a power of two from 16 to 1024,
+ * max_pages * page_size < 2^31 - 4096, row strides up to 2^22.
+ *
+ * Norm and rotation (ssd_qk_rope).  For a head x of a token at position t:
+ *     n = x w / sqrt(mean(x^2) + eps)            (w: q_weight or k_weight; NULL: n = x)
+ *     (n_a, n_b) <- (n_a cos u - n_b sin u, n_b cos u + n_a sin u),  u = t inv_freq[i]
+ * for i < rot_dim / 2 and the pairs (a, b) = (i, i + rot_dim / 2), or with interleaved
+ * (2 i, 2 i + 1); values from rot_dim on stay as normed.  In fp32, the angle in fp64;
+ * rounded once.  Squares of normed inputs must be finite in fp32.
+ */
+#define SSD_PAGES_IO 0
+#define SSD_PAGES_4BIT 1
+
+typedef struct ssd_paged_dims {
+    int64_t batch;     /* sequences, >= 0                                     */
+    int64_t rows;      /* token rows of q, k, v (gather: rows of k and v);
+                          decode step: ignored                                */
+    int64_t q_heads;   /* Hq >= 1, Hq % Hkv == 0                              */
+    int64_t kv_heads;  /* Hkv >= 1                                            */
+    int64_t head_dim;  /* D                                                   */
+    int64_t num_pages, page_size, max_pages; /* >= 1; ssd_attn_qk_norm_rope: ignored */
+    int64_t q_stride, k_stride, v_stride;    /* elements between rows, 0 = contiguous */
+    int64_t q_out_stride, k_out_stride;      /* likewise                      */
+    float scale;       /* finite; decode step only                            */
+    int32_t io_dtype;  /* ssd_dtype of q, k, v and outputs                    */
+    int32_t page_format; /* SSD_PAGES_IO or SSD_PAGES_4BIT                    */
+    int32_t reserved;  /* must be 0                                           */
+} ssd_paged_dims;
+
+typedef struct ssd_qk_rope {
+    const float *inv_freq;   /* [rot_dim / 2] fp32; may be NULL with rot_dim 0 */
+    const float *q_weight;   /* [D] fp32 or NULL                              */
+    const float *k_weight;   /* [D] fp32 or NULL                              */
+    const int32_t *positions;/* [rows]; append: NULL = the token's row        */
+    int32_t rot_dim;         /* 0 .. D, a multiple of 8                       */
+    int32_t interleaved;     /* 0 or 1                                        */
+    float eps;               /* finite, >= 0                                  */
+    int32_t reserved;        /* must be 0                                     */
+} ssd_qk_rope;
+
+/*
+ * ssd_attn_qk_norm_rope -- norm and rotation in one pass over q [rows, Hq, D] and
+ * k [rows, Hkv, D] (the tokens of prompts or one per sequence), in front of
+ * ssd_attn_prefill or ssd_attn_decode_step.  q_out may be q and k_out may be k (the
+ * same pointer and stride); outputs overlap nothing else.  Rows of slices of one
+ * projection do not overlap.  Alignment 16 bytes, strides whole 16 bytes.
+ */
+ssd_status ssd_attn_qk_norm_rope(const ssd_paged_dims *dims, const ssd_qk_rope *rope,
+                                 const void *q, const void *k, void *q_out, void *k_out,
+                                 void *stream);
+
+/*
+ * ssd_attn_paged_append -- the tokens of a batch on their way into a paged cache: q is
+ * normed and rotated into q_out, k into the pages (and into k_out unless NULL: what
+ * ssd_attn_prefill takes), v is copied into the pages, in one launch per 120 sequences.
+ * Token j of sequence b becomes row lengths[b] + j, which is also its position unless
+ * rope->positions is given.  cu_seqlens: HOST offsets of batch + 1 entries, or NULL for
+ * one token per sequence (rows == batch; may be captured in a graph and replayed with
+ * other lengths).  lengths is read and not changed.  A token whose row has no page
+ * (lengths[b] < 0, a row past the table, an entry that is no page) is stored nowhere;
+ * its q_out and k_out are written as for any row.  q and q_out may both be NULL.
+ * In-place outputs and alignment as for ssd_attn_qk_norm_rope; the pages, scales and
+ * outputs overlap no input and not each other.
+ */
+ssd_status ssd_attn_paged_append(const ssd_paged_dims *dims, const ssd_qk_rope *rope,
+                                 const int64_t *cu_seqlens, const void *q, const void *k,
+                                 const void *v, void *k_pages, void *v_pages, void *k_scales,
+                                 void *v_scales, const int32_t *block_table,
+                                 const int32_t *lengths, void *q_out, void *k_out, void *stream);
+
+/*
+ * ssd_attn_paged_gather -- rows back from pages: rows starts[b] .. of sequence b (NULL: 0
+ * ..) become the packed rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 of k and v
+ * [rows, Hkv, D] in io_dtype, 4-bit values rounded to it.  What ssd_attn_prefill
+ * attends for the next part of a prompt.  starts and cu_seqlens are HOST arrays; rows
+ * past the table are SSD_ERR_SHAPE, rows on no page are 0.
+ */
+ssd_status ssd_attn_paged_gather(const ssd_paged_dims *dims, const int64_t *cu_seqlens,
+                                 const int64_t *starts, const void *k_pages,
+                                 const void *v_pages, const void *k_scales,
+                                 const void *v_scales, const int32_t *block_table, void *k,
+                                 void *v, void *stream);
+
+/*
+ * ssd_attn_paged_decode_step -- ssd_attn_decode_step's attention over pages, after an
+ * ssd_attn_paged_append of one token per sequence with the same lengths: q[b] attends
+ * rows 0 .. lengths[b].  A length outside [0, max_pages page_size) marks an unused slot:
+ * o[b] = 0.  Rows on no page are not attended, and other rows than those are not read;
+ * o[b] is 0 also where no row is attended or all scores are -infinity.
+ *   q, o [B, Hq, D] io_dtype; q_stride: elements between rows of q
+ * The work is shared out on the device by the lengths, so the width of the table does
+ * not matter, and results depend on the batch only by rounding (deterministic for the
+ * same lengths).  In bf16 an infinity or NaN in a value row reaches its own sequence
+ * only.  batch * kv_heads * (32-head tiles of a key head's queries) < 2^24.
+ * workspace: >= ssd_attn_paged_decode_workspace_size bytes, which do not depend on
+ * the lengths, 16-byte aligned; one per call that may run at the same time (also per
+ * captured graph that may).  o and the workspace overlap no input and not each other.
+ */
+ssd_status ssd_attn_paged_decode_workspace_size(const ssd_paged_dims *dims, size_t *bytes);
+ssd_status ssd_attn_paged_decode_step(const ssd_paged_dims *dims, const void *q,
+                                      const void *k_pages, const void *v_pages,
+                                      const void *k_scales, const void *v_scales,
+                                      const int32_t *block_table, const int32_t *lengths,
+                                      void *o, void *workspace, size_t workspace_bytes,
+                                      void *stream);
 
 /*
  * ssd_chunk_scan_timed -- measurement entry point: the same computation as

@@ -24,6 +24,11 @@ and the attention layers of hybrid stacks:
     ssd_linattn_decode_step(q, k, v, log_decay, state, o=None) -> o
     ssd_attn_prefill(q, k, v, cu_seqlens, kv_starts=None, kv_lens=None, ...) -> o
     ssd_attn_decode_step(q, k, v, k_cache, v_cache, lengths, ...) -> o  (cache appended in place)
+with the norm and rotation of the latter's queries and keys, and a paged cache of its own:
+    ssd_attn_qk_norm_rope(q, k, positions, inv_freq=None, q_weight=None, ...) -> (q_out, k_out)
+    ssd_attn_paged_append(q, k, v, k_pages, v_pages, block_table, lengths, ...) -> q_out
+    ssd_attn_paged_gather(k_pages, v_pages, block_table, cu_seqlens, ...) -> (k, v)
+    ssd_attn_paged_decode_step(q, k_pages, v_pages, block_table, lengths, ...) -> o
 """
 from __future__ import annotations
 
@@ -37,6 +42,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(PKG, "libssd.so")
 
 SSD_F32, SSD_BF16 = 0, 1
+SSD_PAGES_IO, SSD_PAGES_4BIT = 0, 1
 SSD_DT_SOFTPLUS = 1            # ssd_dims.flags: dt holds u, the step size is softplus(u + dt_bias)
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL", 2: "SSD_ERR_SHAPE", 3: "SSD_ERR_UNSUPPORTED",
           4: "SSD_ERR_ALIAS", 5: "SSD_ERR_WORKSPACE", 6: "SSD_ERR_DEVICE", 7: "SSD_ERR_ALIGNMENT"}
@@ -47,7 +53,9 @@ EXPORTS = ("ssd_status_string", "ssd_version", "ssd_state_init", "ssd_chunk_scan
            "ssd_linattn_chunk_scan_workspace_size", "ssd_linattn_chunk_scan",
            "ssd_linattn_chunk_scan_varlen_workspace_size", "ssd_linattn_chunk_scan_varlen",
            "ssd_linattn_decode_step", "ssd_attn_prefill", "ssd_attn_decode_workspace_size",
-           "ssd_attn_decode_step")
+           "ssd_attn_decode_step", "ssd_attn_qk_norm_rope", "ssd_attn_paged_append",
+           "ssd_attn_paged_gather", "ssd_attn_paged_decode_workspace_size",
+           "ssd_attn_paged_decode_step")
 NOALLOC_SCRATCH_BYTES = 96 << 20   # SSD_NOALLOC_SCRATCH_BYTES of include/ssd.h
 
 
@@ -117,6 +125,7 @@ def load(path: str | None = None):
     lib.ssd_gdn_decode_steps.argtypes = [ctypes.POINTER(SsdGdnDims), ctypes.c_int64] + [vp] * 8
     lib.ssd_gdn_decode_steps.restype = ctypes.c_int
     lin, att, sz = ctypes.POINTER(SsdLinattnDims), ctypes.POINTER(SsdAttnDims), ctypes.c_size_t
+    pag, rope = ctypes.POINTER(SsdPagedDims), ctypes.POINTER(SsdQkRope)
     for name, args in (
             ("ssd_linattn_chunk_scan_workspace_size", [lin, i64p]),
             ("ssd_linattn_chunk_scan", [lin] + [vp] * 8 + [sz, vp]),
@@ -125,7 +134,12 @@ def load(path: str | None = None):
             ("ssd_linattn_decode_step", [lin] + [vp] * 7),
             ("ssd_attn_prefill", [att] + [cu] * 3 + [vp] * 5),
             ("ssd_attn_decode_workspace_size", [att, i64p]),
-            ("ssd_attn_decode_step", [att] + [vp] * 8 + [sz, vp])):
+            ("ssd_attn_decode_step", [att] + [vp] * 8 + [sz, vp]),
+            ("ssd_attn_qk_norm_rope", [pag, rope] + [vp] * 5),
+            ("ssd_attn_paged_append", [pag, rope, cu] + [vp] * 12),
+            ("ssd_attn_paged_gather", [pag, cu, cu] + [vp] * 8),
+            ("ssd_attn_paged_decode_workspace_size", [pag, i64p]),
+            ("ssd_attn_paged_decode_step", [pag] + [vp] * 9 + [sz, vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
@@ -750,4 +764,221 @@ def ssd_attn_decode_step(q, k, v, k_cache, v_cache, lengths, scale=None, o=None,
         _check("ssd_attn_decode_step", lib.ssd_attn_decode_step(
             ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
             _ptr(lengths), _ptr(o), _ptr(workspace), ws_bytes, _stream(stream, dev)))
+    return o
+
+
+# --------------------------------------------------------------------------
+# Norm and rotation of queries and keys, paged caches
+# --------------------------------------------------------------------------
+class SsdPagedDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("q_heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_out_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("io_dtype", ctypes.c_int32), ("page_format", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class SsdQkRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+def _rope(dev, T, D, positions, inv_freq, q_weight, k_weight, eps, interleaved):
+    f32 = torch.float32
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError(f"inv_freq must be [rot_dim / 2], got shape {tuple(inv_freq.shape)}")
+        _need("inv_freq", inv_freq, dev, f32)
+    _need("q_weight", q_weight, dev, f32, (D,), optional=True)
+    _need("k_weight", k_weight, dev, f32, (D,), optional=True)
+    _need("positions", positions, dev, torch.int32, (T,), optional=True)
+    return SsdQkRope(_ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+                     0 if inv_freq is None else 2 * inv_freq.shape[0], int(interleaved), eps, 0)
+
+
+def _pages(dev, k_pages, v_pages, block_table, k_scales, v_scales, io, D=None, Hkv=None, B=None):
+    """Checks a paged cache of input type `io`; returns (page_format, num_pages, Hkv, page_size,
+    D, B, max_pages)."""
+    for name, t in (("k_pages", k_pages), ("block_table", block_table)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("pages must be [num_pages, Hkv, page_size, D] (D / 2 bytes in 4 bits) and "
+                         "block_table [B, max_pages]")
+    q4 = k_scales is not None or v_scales is not None
+    n, h, p, width = k_pages.shape
+    d = 2 * width if q4 else width
+    dtype = torch.uint8 if q4 else io
+    _need("k_pages", k_pages, dev, dtype)
+    if (D is not None and d != D) or (Hkv is not None and h != Hkv):
+        raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, which does not go with "
+                         f"{Hkv if Hkv is not None else h} key heads of {D if D is not None else d}")
+    _need("v_pages", v_pages, dev, dtype, k_pages.shape)
+    if q4:
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _need(name, t, dev, torch.float16, (n, h, p, d // 64, 2))
+    _need("block_table", block_table, dev, torch.int32, None if B is None else (B, block_table.shape[1]))
+    return (SSD_PAGES_4BIT if q4 else SSD_PAGES_IO, n, h, p, d, block_table.shape[0], block_table.shape[1])
+
+
+def ssd_attn_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                          interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norms every head of q [T, Hq, D] and k [T, Hkv, D] (x w / sqrt(mean(x^2) + eps) for the
+    weights that are given, [D] fp32) and rotates its first 2 len(inv_freq) values by
+    positions [T] int32 times inv_freq (fp32), pairing value i with i + len(inv_freq), or
+    neighbours with interleaved.  q and k may be slices of one projection, and q_out and
+    k_out may be q and k.  Returns (q_out, k_out)."""
+    dev = _device_of(q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if inv_freq is not None and positions is None:
+        raise ValueError("positions is required with inv_freq")
+    qs, ks = _row_stride("q", q, dev, q.dtype, q.shape), _row_stride("k", k, dev, q.dtype, (T, Hkv, D))
+    io = _io_dtype(q, "q/k")
+    rope = _rope(dev, T, D, positions, inv_freq, q_weight, k_weight, eps, interleaved)
+    with _guard(dev):
+        if q_out is None or k_out is None:
+            with _on(stream):
+                q_out = _empty_rows(q) if q_out is None else q_out
+                k_out = _empty_rows(k) if k_out is None else k_out
+        d = SsdPagedDims(0, T, Hq, Hkv, D, 0, 0, 0, qs, ks, 0, _row_stride("q_out", q_out, dev, q.dtype, q.shape),
+                         _row_stride("k_out", k_out, dev, q.dtype, k.shape), 1.0, io, 0, 0)
+        _check("ssd_attn_qk_norm_rope", load().ssd_attn_qk_norm_rope(
+            ctypes.byref(d), ctypes.byref(rope), _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
+            _stream(stream, dev)))
+    return q_out, k_out
+
+
+def ssd_attn_paged_append(q, k, v, k_pages, v_pages, block_table, lengths, cu_seqlens=None, k_scales=None,
+                          v_scales=None, positions=None, inv_freq=None, q_weight=None, k_weight=None,
+                          eps=1e-6, interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norms and rotates q [T, Hq, D] (returned as q_out; None: no queries) and k [T, Hkv, D] as
+    ssd_attn_qk_norm_rope does, and appends k and v [T, Hkv, D] to a paged cache: k_pages,
+    v_pages [num_pages, Hkv, page_size, D] of the input type, or with k_scales, v_scales
+    [num_pages, Hkv, page_size, D / 64, 2] float16 the 4-bit codes [.., D / 2] uint8.  Token j
+    of sequence b becomes row lengths[b] + j, line r % page_size of page block_table[b, r //
+    page_size]; that row is its position unless positions is given.  cu_seqlens: a host
+    sequence of B + 1 offsets, None for one token per sequence.  block_table [B, max_pages] and
+    lengths [B] are int32 device tensors, left as they are.  Tokens whose row has no page are
+    not stored.  k_out, if given, receives the keys as ssd_attn_prefill takes them."""
+    dev = _device_of(k)
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("q must be [T, Hq, D] and k, v [T, Hkv, D]")
+    T, Hkv, D = k.shape
+    Hq = Hkv if q is None else q.shape[1]
+    dt = k.dtype
+    io = _io_dtype(k, "q/k/v")
+    if cu_seqlens is None:
+        B, cup = T, None
+    else:
+        cu, cup = _offsets("cu_seqlens", cu_seqlens)
+        B = len(cu) - 1
+    qs = 0 if q is None else _row_stride("q", q, dev, dt, (T, Hq, D))
+    ks, vs = _row_stride("k", k, dev, dt, k.shape), _row_stride("v", v, dev, dt, k.shape)
+    fmt, n, _, p, _, _, m = _pages(dev, k_pages, v_pages, block_table, k_scales, v_scales, dt, D, Hkv, B)
+    _need("lengths", lengths, dev, torch.int32, (B,))
+    rope = _rope(dev, T, D, positions, inv_freq, q_weight, k_weight, eps, interleaved)
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
+    kos = 0 if k_out is None else _row_stride("k_out", k_out, dev, dt, k.shape)
+    with _guard(dev):
+        if q is not None and q_out is None:
+            with _on(stream):
+                q_out = _empty_rows(q)
+        qos = 0 if q is None else _row_stride("q_out", q_out, dev, dt, q.shape)
+        d = SsdPagedDims(B, T, Hq, Hkv, D, n, p, m, qs, ks, vs, qos, kos, 1.0, io, fmt, 0)
+        _check("ssd_attn_paged_append", load().ssd_attn_paged_append(
+            ctypes.byref(d), ctypes.byref(rope), cup, _ptr(q), _ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages),
+            _ptr(k_scales), _ptr(v_scales), _ptr(block_table), _ptr(lengths), _ptr(q_out), _ptr(k_out),
+            _stream(stream, dev)))
+    return q_out
+
+
+def ssd_attn_paged_gather(k_pages, v_pages, block_table, cu_seqlens, starts=None, k_scales=None, v_scales=None,
+                          dtype=None, k=None, v=None, stream=None):
+    """Rows starts[b] .. (None: 0 ..) of every sequence's pages as packed rows cu_seqlens[b] ..
+    cu_seqlens[b+1]-1 (host sequences), which ssd_attn_prefill attends with kv_starts =
+    cu_seqlens[:-1]: returns (k, v) [T, Hkv, D].  dtype: the values' type of 4-bit pages
+    (bfloat16 unless given).  Rows on no page are 0."""
+    dev = _device_of(k_pages)
+    if k_scales is None and v_scales is None:
+        dt = k_pages.dtype
+        if dtype is not None and dtype != dt:
+            raise TypeError(f"rows of {dt} pages are {dt}, not {dtype}")
+    else:
+        dt = torch.bfloat16 if dtype is None else dtype
+    cu, cup = _offsets("cu_seqlens", cu_seqlens)
+    B, T = len(cu) - 1, int(cu[-1])
+    st, stp = (None, None) if starts is None else _offsets("starts", starts, B)
+    fmt, n, Hkv, p, D, _, m = _pages(dev, k_pages, v_pages, block_table, k_scales, v_scales, dt, B=B)
+    _need("k", k, dev, dt, (T, Hkv, D), optional=True)
+    _need("v", v, dev, dt, (T, Hkv, D), optional=True)
+    io = SSD_BF16 if dt == torch.bfloat16 else SSD_F32 if dt == torch.float32 else None
+    if io is None:
+        raise TypeError(f"pages and rows must be bfloat16 or float32, got {dt}")
+    d = SsdPagedDims(B, T, Hkv, Hkv, D, n, p, m, 0, 0, 0, 0, 0, 1.0, io, fmt, 0)
+    with _guard(dev):
+        with _on(stream):
+            k = torch.empty((max(T, 0), Hkv, D), dtype=dt, device=k_pages.device) if k is None else k
+            v = torch.empty((max(T, 0), Hkv, D), dtype=dt, device=k_pages.device) if v is None else v
+        _check("ssd_attn_paged_gather", load().ssd_attn_paged_gather(
+            ctypes.byref(d), cup, stp, _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
+            _ptr(block_table), _ptr(k), _ptr(v), _stream(stream, dev)))
+    return k, v
+
+
+def ssd_attn_paged_decode_workspace_size(batch, q_heads, kv_heads, head_dim, num_pages, page_size, max_pages,
+                                         io_dtype=SSD_BF16, page_format=SSD_PAGES_IO) -> int:
+    d = SsdPagedDims(batch, 0, q_heads, kv_heads, head_dim, num_pages, page_size, max_pages, 0, 0, 0, 0, 0, 1.0,
+                     io_dtype, page_format, 0)
+    n = ctypes.c_size_t(0)
+    _check("ssd_attn_paged_decode_workspace_size",
+           load().ssd_attn_paged_decode_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return int(n.value)
+
+
+def ssd_attn_paged_decode_step(q, k_pages, v_pages, block_table, lengths, k_scales=None, v_scales=None,
+                               scale=None, o=None, workspace=None, stream=None):
+    """Softmax attention of one token per sequence over a paged cache (see
+    ssd_attn_paged_append, which has stored the token's own key and value): q [B, Hq, D]
+    attends rows 0 .. lengths[b].  A length outside [0, max_pages page_size) marks an unused
+    slot (o[b] = 0); rows on no page are not attended.  scale defaults to 1 / sqrt(D).
+    Returns o [B, Hq, D]."""
+    dev = _device_of(q)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    B, Hq, D = q.shape
+    io = _io_dtype(q, "q")
+    qs = _row_stride("q", q, dev, q.dtype, q.shape)
+    fmt, n, Hkv, p, _, _, m = _pages(dev, k_pages, v_pages, block_table, k_scales, v_scales, q.dtype, D, None, B)
+    _need("lengths", lengths, dev, torch.int32, (B,))
+    _need("o", o, dev, q.dtype, q.shape, optional=True)
+    _need("workspace", workspace, dev, optional=True)
+    lib = load()
+    d = SsdPagedDims(B, 0, Hq, Hkv, D, n, p, m, qs, 0, 0, 0, 0, _attn_scale(scale, D), io, fmt, 0)
+    need = 0
+    if workspace is None:
+        size = ctypes.c_size_t(0)
+        _check("ssd_attn_paged_decode_workspace_size",
+               lib.ssd_attn_paged_decode_workspace_size(ctypes.byref(d), ctypes.byref(size)))
+        need = size.value
+    with _guard(dev):
+        if o is None or need > 0:
+            with _on(stream):
+                if o is None:
+                    o = _empty_rows(q)
+                if need > 0:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check("ssd_attn_paged_decode_step", lib.ssd_attn_paged_decode_step(
+            ctypes.byref(d), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
+            _ptr(block_table), _ptr(lengths), _ptr(o), _ptr(workspace), ws_bytes, _stream(stream, dev)))
     return o

@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libssd.so")
 SOURCES = ["ssd_api.cpp", "ssd_decode.hip", "ssd_decode_steps.hip", "ssd_gdn.hip",
-           "ssd_scan_f32.hip", "ssd_scan_bf16.hip", "ssd_linattn.hip", "ssd_attn.hip"]
+           "ssd_scan_f32.hip", "ssd_scan_bf16.hip", "ssd_linattn.hip", "ssd_attn.hip",
+           "ssd_paged.hip", "ssd_paged_rows.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

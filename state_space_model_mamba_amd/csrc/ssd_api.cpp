@@ -11,6 +11,7 @@
 #include "ssd.h"
 #include "ssd_attn.h"
 #include "ssd_kernels.h"
+#include "ssd_paged.h"
 
 #define SSD_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -1289,4 +1290,337 @@ SSD_EXPORT ssd_status ssd_attn_decode_step(const ssd_attn_dims *dims, const void
         dims->io_dtype == SSD_BF16, dims->batch, dims->kv_rows, dims->q_heads, dims->kv_heads,
         dims->head_dim, sh.q.stride, sh.k.stride, sh.v.stride, dims->scale, q, k, v, k_cache,
         v_cache, lengths, o, workspace, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Norm and rotation of queries and keys, paged caches
+// ---------------------------------------------------------------------------
+namespace {
+
+// A tensor of rows that may lie further apart than they are wide.
+struct RowSpan {
+    Span s;
+    int64_t stride, width;    // bytes; stride 0: one block
+};
+
+RowSpan block(const void *p, int64_t bytes)
+{
+    return {span(p, p ? bytes : 0), 0, 0};
+}
+RowSpan rows_span(const void *p, const Rows &r, int64_t width, int64_t esz)
+{
+    return {span(p, p ? r.bytes : 0), r.stride * esz, width * esz};
+}
+// Whether two tensors share memory: slices of one projection whose spans interleave
+// (the same stride) do not if their rows lie side by side.
+bool share(const RowSpan &a, const RowSpan &b)
+{
+    if (!overlap(a.s, b.s))
+        return false;
+    if (a.stride == 0 || a.stride != b.stride)
+        return true;
+    const int64_t gap = (int64_t)((b.s.lo - a.s.lo) % (uintptr_t)a.stride);
+    const int64_t at = b.s.lo >= a.s.lo ? gap : (a.stride - (int64_t)((a.s.lo - b.s.lo) % (uintptr_t)a.stride)) % a.stride;
+    return at < a.width || at + b.width > a.stride;
+}
+
+struct PagedShape {
+    Rows q, k, v, qo, ko;
+    int64_t esz, wq, wk, cap, page_bytes, scale_bytes;
+    int shift;
+};
+
+// Heads, types and strides; `rows`: rows of q, k and v.
+ssd_status paged_rows_check(const ssd_paged_dims *d, int64_t rows, PagedShape *sh)
+{
+    if (!d)
+        return SSD_ERR_NULL;
+    if (d->batch < 0 || rows < 0 || d->q_heads < 1 || d->kv_heads < 1 ||
+        d->q_heads % d->kv_heads != 0 || d->reserved != 0)
+        return SSD_ERR_SHAPE;
+    if ((d->io_dtype != SSD_F32 && d->io_dtype != SSD_BF16) || !head_size(d->head_dim) ||
+        d->q_heads > kMaxHeads || rows > kMaxRows)
+        return SSD_ERR_UNSUPPORTED;
+    sh->wq = d->q_heads * d->head_dim;
+    sh->wk = d->kv_heads * d->head_dim;
+    if (sh->wq > kMaxStride)
+        return SSD_ERR_UNSUPPORTED;
+    sh->esz = d->io_dtype == SSD_BF16 ? 2 : 4;
+    ssd_status st;
+    if ((st = rows_of(d->q_stride, rows, sh->wq, sh->esz, true, &sh->q)) != SSD_OK ||
+        (st = rows_of(d->k_stride, rows, sh->wk, sh->esz, true, &sh->k)) != SSD_OK ||
+        (st = rows_of(d->v_stride, rows, sh->wk, sh->esz, true, &sh->v)) != SSD_OK ||
+        (st = rows_of(d->q_out_stride, rows, sh->wq, sh->esz, true, &sh->qo)) != SSD_OK ||
+        (st = rows_of(d->k_out_stride, rows, sh->wk, sh->esz, true, &sh->ko)) != SSD_OK)
+        return st;
+    return SSD_OK;
+}
+
+// Pages and table.
+ssd_status paged_cache_check(const ssd_paged_dims *d, PagedShape *sh)
+{
+    if (d->num_pages < 1 || d->max_pages < 1 || d->page_size < 1)
+        return SSD_ERR_SHAPE;
+    if (d->page_size < 16 || d->page_size > 1024 || (d->page_size & (d->page_size - 1)) != 0 ||
+        d->num_pages > INT32_MAX || (d->page_format != SSD_PAGES_IO && d->page_format != SSD_PAGES_4BIT))
+        return SSD_ERR_UNSUPPORTED;
+    sh->shift = __builtin_ctzll((unsigned long long)d->page_size);
+    if (!mul_ok(d->max_pages, d->page_size, &sh->cap))
+        return SSD_ERR_SHAPE;
+    if (sh->cap > kMaxRows)
+        return SSD_ERR_UNSUPPORTED;
+    int64_t lines, t;
+    if (!mul_ok(d->num_pages * d->page_size, sh->wk * 4, &t) || !mul_ok(d->batch, d->max_pages * 4, &t))
+        return SSD_ERR_SHAPE;
+    lines = d->num_pages * d->page_size * d->kv_heads;
+    const bool q4 = d->page_format == SSD_PAGES_4BIT;
+    sh->page_bytes = q4 ? lines * d->head_dim / 2 : lines * d->head_dim * sh->esz;
+    sh->scale_bytes = q4 ? lines * (d->head_dim / 64) * 4 : 0;
+    return SSD_OK;
+}
+
+// The cache of a call; its pointers' checks.
+ssd_status paged_cache_of(const ssd_paged_dims *d, const PagedShape &sh, const void *kp, const void *vp,
+                          const void *ks, const void *vs, const int32_t *table, ssd::PagedCache *c)
+{
+    const bool q4 = d->page_format == SSD_PAGES_4BIT;
+    if (!kp || !vp || !table || (q4 && (!ks || !vs)))
+        return SSD_ERR_NULL;
+    if (!aligned(kp, 16) || !aligned(vp, 16) || !aligned(table, 4) || (q4 && (!aligned(ks, 16) || !aligned(vs, 16))))
+        return SSD_ERR_ALIGNMENT;
+    c->k = const_cast<void *>(kp);
+    c->v = const_cast<void *>(vp);
+    c->ks = q4 ? static_cast<uint32_t *>(const_cast<void *>(ks)) : nullptr;
+    c->vs = q4 ? static_cast<uint32_t *>(const_cast<void *>(vs)) : nullptr;
+    c->table = table;
+    c->num_pages = d->num_pages;
+    c->max_pages = d->max_pages;
+    c->shift = sh.shift;
+    return SSD_OK;
+}
+
+ssd_status rope_check(const ssd_paged_dims *d, const ssd_qk_rope *r, bool positions, ssd::QkTurn *t)
+{
+    if (!r)
+        return SSD_ERR_NULL;
+    if (r->rot_dim < 0 || r->rot_dim > d->head_dim || r->reserved != 0 || (r->interleaved != 0 && r->interleaved != 1))
+        return SSD_ERR_SHAPE;
+    if (r->rot_dim % 8 != 0 || !std::isfinite(r->eps) || r->eps < 0.f)
+        return SSD_ERR_UNSUPPORTED;
+    if (r->rot_dim > 0 && (!r->inv_freq || (positions && !r->positions)))
+        return SSD_ERR_NULL;
+    if (!aligned(r->inv_freq, 4) || !aligned(r->q_weight, 4) || !aligned(r->k_weight, 4) || !aligned(r->positions, 4))
+        return SSD_ERR_ALIGNMENT;
+    t->inv_freq = r->rot_dim > 0 ? r->inv_freq : nullptr;
+    t->q_weight = r->q_weight;
+    t->k_weight = r->k_weight;
+    t->positions = r->rot_dim > 0 ? r->positions : nullptr;
+    t->rot = (int)r->rot_dim;
+    t->next = r->interleaved;
+    t->eps = r->eps;
+    return SSD_OK;
+}
+
+// Outputs share nothing with each other or with an input, but that out[i] may be in[i]
+// (i < same) as it lies: then each of its elements is read before it is written.
+bool clash(const RowSpan *outs, int nout, const RowSpan *ins, int nin, int same)
+{
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j) {
+            const bool in_place = i == j && i < same && outs[i].s.lo == ins[j].s.lo && outs[i].stride == ins[j].stride;
+            if (!in_place && share(outs[i], ins[j]))
+                return true;
+        }
+        for (int j = 0; j < i; ++j)
+            if (share(outs[i], outs[j]))
+                return true;
+    }
+    return false;
+}
+
+ssd_status host_offsets(const int64_t *cu, int64_t batch, int64_t rows)
+{
+    if (cu[0] != 0 || cu[batch] != rows)
+        return SSD_ERR_SHAPE;
+    for (int64_t i = 0; i < batch; ++i)
+        if (cu[i + 1] < cu[i])
+            return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
+ssd_status paged_decode_check(const ssd_paged_dims *d, PagedShape *sh)
+{
+    if (!d)
+        return SSD_ERR_NULL;
+    ssd_status st;
+    if ((st = paged_rows_check(d, d->batch, sh)) != SSD_OK || (st = paged_cache_check(d, sh)) != SSD_OK)
+        return st;
+    if (!std::isfinite(d->scale))
+        return SSD_ERR_UNSUPPORTED;
+    // (units of all items, 64 bits of them times the number of work-groups)
+    const int64_t rtiles = (d->q_heads / d->kv_heads + 31) / 32;
+    if (d->batch > kMaxGroups / (d->kv_heads * rtiles))
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+size_t paged_decode_need(const ssd_paged_dims *d)
+{
+    return ssd::paged_decode_workspace(d->io_dtype == SSD_BF16, d->page_format == SSD_PAGES_4BIT, d->batch,
+                                       d->q_heads, d->kv_heads, d->head_dim);
+}
+
+}  // namespace
+
+SSD_EXPORT ssd_status ssd_attn_qk_norm_rope(const ssd_paged_dims *dims, const ssd_qk_rope *rope,
+                                            const void *q, const void *k, void *q_out, void *k_out,
+                                            void *stream)
+{
+    PagedShape sh;
+    ssd::QkTurn turn;
+    ssd_status st = paged_rows_check(dims, dims ? dims->rows : 0, &sh);
+    if (st != SSD_OK || (st = rope_check(dims, rope, dims->rows > 0, &turn)) != SSD_OK || dims->rows == 0)
+        return st;
+    if (!q || !k || !q_out || !k_out)
+        return SSD_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16))
+        return SSD_ERR_ALIGNMENT;
+    const RowSpan outs[] = {rows_span(q_out, sh.qo, sh.wq, sh.esz), rows_span(k_out, sh.ko, sh.wk, sh.esz)};
+    const RowSpan ins[] = {rows_span(q, sh.q, sh.wq, sh.esz), rows_span(k, sh.k, sh.wk, sh.esz),
+                           block(turn.inv_freq, turn.rot * 2), block(turn.q_weight, dims->head_dim * 4),
+                           block(turn.k_weight, dims->head_dim * 4), block(turn.positions, dims->rows * 4)};
+    if (clash(outs, 2, ins, 6, 2))
+        return SSD_ERR_ALIAS;
+    const ssd::TurnRows r{q, k, nullptr, q_out, k_out, sh.q.stride, sh.k.stride, 0, sh.qo.stride, sh.ko.stride,
+                          dims->rows, dims->q_heads, dims->kv_heads, dims->head_dim};
+    return device_status(ssd::launch_qk_turn(dims->io_dtype == SSD_BF16, r, turn, static_cast<hipStream_t>(stream)));
+}
+
+SSD_EXPORT ssd_status ssd_attn_paged_append(const ssd_paged_dims *dims, const ssd_qk_rope *rope,
+                                            const int64_t *cu_seqlens, const void *q, const void *k,
+                                            const void *v, void *k_pages, void *v_pages,
+                                            void *k_scales, void *v_scales,
+                                            const int32_t *block_table, const int32_t *lengths,
+                                            void *q_out, void *k_out, void *stream)
+{
+    PagedShape sh;
+    ssd::QkTurn turn;
+    ssd::PagedCache cache;
+    ssd_status st = paged_rows_check(dims, dims ? dims->rows : 0, &sh);
+    if (st != SSD_OK || (st = paged_cache_check(dims, &sh)) != SSD_OK ||
+        (st = rope_check(dims, rope, false, &turn)) != SSD_OK)
+        return st;
+    if (cu_seqlens ? (st = host_offsets(cu_seqlens, dims->batch, dims->rows)) != SSD_OK
+                   : dims->rows != dims->batch)
+        return SSD_ERR_SHAPE;
+    if (dims->rows == 0)
+        return SSD_OK;
+    if (!q != !q_out || !k || !v || !lengths)
+        return SSD_ERR_NULL;
+    if ((st = paged_cache_of(dims, sh, k_pages, v_pages, k_scales, v_scales, block_table, &cache)) != SSD_OK)
+        return st;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+        !aligned(lengths, 4))
+        return SSD_ERR_ALIGNMENT;
+    const RowSpan outs[] = {rows_span(q_out, sh.qo, sh.wq, sh.esz), rows_span(k_out, sh.ko, sh.wk, sh.esz),
+                            block(k_pages, sh.page_bytes), block(v_pages, sh.page_bytes),
+                            block(cache.ks, sh.scale_bytes), block(cache.vs, sh.scale_bytes)};
+    const RowSpan ins[] = {rows_span(q, sh.q, sh.wq, sh.esz), rows_span(k, sh.k, sh.wk, sh.esz),
+                           rows_span(v, sh.v, sh.wk, sh.esz), block(turn.inv_freq, turn.rot * 2),
+                           block(turn.q_weight, dims->head_dim * 4), block(turn.k_weight, dims->head_dim * 4),
+                           block(turn.positions, dims->rows * 4), block(lengths, dims->batch * 4),
+                           block(block_table, dims->batch * dims->max_pages * 4)};
+    if (clash(outs, 6, ins, 9, 2))
+        return SSD_ERR_ALIAS;
+    const ssd::TurnRows r{q, k, v, q_out, k_out, sh.q.stride, sh.k.stride, sh.v.stride, sh.qo.stride, sh.ko.stride,
+                          dims->rows, q ? dims->q_heads : 0, dims->kv_heads, dims->head_dim};
+    return device_status(ssd::launch_paged_append(dims->io_dtype == SSD_BF16, dims->batch, cu_seqlens, r, turn, cache,
+                                                  lengths, static_cast<hipStream_t>(stream)));
+}
+
+SSD_EXPORT ssd_status ssd_attn_paged_gather(const ssd_paged_dims *dims, const int64_t *cu_seqlens,
+                                            const int64_t *starts, const void *k_pages,
+                                            const void *v_pages, const void *k_scales,
+                                            const void *v_scales, const int32_t *block_table, void *k,
+                                            void *v, void *stream)
+{
+    PagedShape sh;
+    ssd::PagedCache cache;
+    ssd_status st = paged_rows_check(dims, dims ? dims->rows : 0, &sh);
+    if (st != SSD_OK || (st = paged_cache_check(dims, &sh)) != SSD_OK)
+        return st;
+    if (!cu_seqlens)
+        return SSD_ERR_NULL;
+    if ((st = host_offsets(cu_seqlens, dims->batch, dims->rows)) != SSD_OK)
+        return st;
+    for (int64_t i = 0; i < dims->batch; ++i) {
+        const int64_t first = starts ? starts[i] : 0, n = cu_seqlens[i + 1] - cu_seqlens[i];
+        if (first < 0 || first > sh.cap || n > sh.cap - first)
+            return SSD_ERR_SHAPE;
+    }
+    if (dims->rows == 0)
+        return SSD_OK;
+    if (!k || !v)
+        return SSD_ERR_NULL;
+    if ((st = paged_cache_of(dims, sh, k_pages, v_pages, k_scales, v_scales, block_table, &cache)) != SSD_OK)
+        return st;
+    if (!aligned(k, 16) || !aligned(v, 16))
+        return SSD_ERR_ALIGNMENT;
+    const int64_t bytes = dims->rows * sh.wk * sh.esz;
+    const RowSpan outs[] = {block(k, bytes), block(v, bytes)};
+    const RowSpan ins[] = {block(k_pages, sh.page_bytes), block(v_pages, sh.page_bytes),
+                           block(cache.ks, sh.scale_bytes), block(cache.vs, sh.scale_bytes),
+                           block(block_table, dims->batch * dims->max_pages * 4)};
+    if (clash(outs, 2, ins, 5, 0))
+        return SSD_ERR_ALIAS;
+    return device_status(ssd::launch_paged_gather(dims->io_dtype == SSD_BF16, dims->batch, cu_seqlens, starts,
+                                                  dims->kv_heads, dims->head_dim, cache, k, v,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+SSD_EXPORT ssd_status ssd_attn_paged_decode_workspace_size(const ssd_paged_dims *dims, size_t *bytes)
+{
+    PagedShape sh;
+    const ssd_status st = paged_decode_check(dims, &sh);
+    if (st != SSD_OK)
+        return st;
+    if (!bytes)
+        return SSD_ERR_NULL;
+    *bytes = paged_decode_need(dims);
+    return SSD_OK;
+}
+
+SSD_EXPORT ssd_status ssd_attn_paged_decode_step(const ssd_paged_dims *dims, const void *q,
+                                                 const void *k_pages, const void *v_pages,
+                                                 const void *k_scales, const void *v_scales,
+                                                 const int32_t *block_table, const int32_t *lengths,
+                                                 void *o, void *workspace, size_t workspace_bytes,
+                                                 void *stream)
+{
+    PagedShape sh;
+    ssd::PagedCache cache;
+    ssd_status st = paged_decode_check(dims, &sh);
+    if (st != SSD_OK || dims->batch == 0)
+        return st;
+    if (!q || !lengths || !o)
+        return SSD_ERR_NULL;
+    if ((st = paged_cache_of(dims, sh, k_pages, v_pages, k_scales, v_scales, block_table, &cache)) != SSD_OK)
+        return st;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lengths, 4))
+        return SSD_ERR_ALIGNMENT;
+    const size_t need = paged_decode_need(dims);
+    if (!workspace || workspace_bytes < need)
+        return SSD_ERR_WORKSPACE;
+    if (!aligned(workspace, 16))
+        return SSD_ERR_ALIGNMENT;
+    const RowSpan outs[] = {block(o, dims->batch * sh.wq * sh.esz), block(workspace, (int64_t)need)};
+    const RowSpan ins[] = {rows_span(q, sh.q, sh.wq, sh.esz), block(k_pages, sh.page_bytes),
+                           block(v_pages, sh.page_bytes), block(cache.ks, sh.scale_bytes),
+                           block(cache.vs, sh.scale_bytes), block(lengths, dims->batch * 4),
+                           block(block_table, dims->batch * dims->max_pages * 4)};
+    if (clash(outs, 2, ins, 7, 0))
+        return SSD_ERR_ALIAS;
+    return device_status(ssd::launch_paged_decode(dims->io_dtype == SSD_BF16, dims->batch, dims->q_heads,
+                                                  dims->kv_heads, dims->head_dim, sh.q.stride, dims->scale, q, cache,
+                                                  lengths, o, workspace, static_cast<hipStream_t>(stream)));
 }

@@ -15,31 +15,12 @@
 
 #include "ssd_attn.h"
 #include "ssd_mma.h"
+#include "ssd_softmax.h"
 
 namespace ssd {
 namespace {
 
 using namespace mx;
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f;
-constexpr float kNoMax = -3e38f;   // m before the first visible key (finite: m - m is 0)
-// |scale| log2 e.  A scale of 0 weights all visible keys alike; it is kept off 0 so
-// that a masked score (-inf) times it stays -inf, and finite so that a score of 0 times
-// it stays 0.
-float score_factor(float scale)
-{
-    return std::clamp(std::abs(scale) * kLog2e, 1.17549435e-38f, 3.40282347e38f);
-}
-
-// s c - m, the product rounded before the difference as it is in m: for the largest
-// score of a row exactly 0 however large it is.  (Fused, the rounding of m remains;
-// the row's weights have it in common, but past 2^30 it overflows the exponential.)
-__device__ __forceinline__ float below_max(float s, float c, float m)
-{
-#pragma clang fp contract(off)
-    return s * c - m;
-}
 
 // A 32-key tile in a wave's own LDS, for 32 rows (score columns): updates (m, l,
 // acc).  Keys from `see` (per lane) on are masked if `masked` (wave-uniform).  The
@@ -202,17 +183,6 @@ struct PrefillArgs {
 };
 
 typedef const __attribute__((address_space(4))) PrefillArgs *PrefillArgsPtr;
-
-template <typename T> __device__ __forceinline__ typename Piece<T>::V flip(typename Piece<T>::V v);
-template <> __device__ __forceinline__ bf16x8 flip<__bf16>(bf16x8 v)
-{
-    u32x4 u = __builtin_bit_cast(u32x4, v);
-    return __builtin_bit_cast(bf16x8, u ^ 0x80008000u);
-}
-template <> __device__ __forceinline__ f32x4 flip<float>(f32x4 v)
-{
-    return -v;
-}
 
 template <typename T, int D, int NW>
 __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void attn_prefill_kernel(

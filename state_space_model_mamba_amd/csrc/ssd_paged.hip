@@ -1,0 +1,875 @@
+// Softmax attention of one query token per sequence over a paged key/value cache
+// (gfx950), the pages holding the input type or 4-bit codes.
+//
+// For query head h, key head h / (Hq / Hkv) and the rows s = 0 .. lengths[b]:
+//     a_s = scale q . k_s,   o = sum_s exp(a_s - m) v_s / sum_s exp(a_s - m)
+// in one pass with a running maximum, as in the kernels over padded caches.
+//
+// Work.  The host knows neither the lengths nor, therefore, the work: the launch has a
+// fixed number of work-groups W, and each takes an equal share of the units of all
+// (sequence, key head, 16 or 32 query heads) items laid end to end, a unit being kNW
+// tiles of kKT keys.  A share may end inside an item; what a work-group has of an item
+// that others continue goes to the workspace, and a second small kernel joins those.
+// So tables much wider than the sequences are long cost nothing, and sequences of any
+// mix of lengths spread evenly.
+//
+// Scores are formed transposed (keys x query heads, 16 x 16 blocks): lane c + 16 g holds
+// the scores of query head c for keys 16 kb + 4 g + i, its maximum and sums are per-lane
+// scalars, and the probabilities are the second product's operand as they stand.  Tiles
+// go from memory straight into LDS, two deep per wave, in parts of 16 rows: a part never
+// crosses a page, so pages of 16 rows and more need no care.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "ssd_attn.h"
+#include "ssd_mma.h"
+#include "ssd_paged.h"
+#include "ssd_softmax.h"
+
+namespace ssd {
+namespace {
+
+using namespace mx;
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) v2i lds_v2i;
+
+struct PagedArgs {
+    PagedCache c;
+    const void *q;
+    const int32_t *lengths;
+    void *o;
+    float *part;                              // [2 W][rows][D] sums of the items' pieces
+    float2 *ml;                               // [2 W][rows] (m, l)
+    int4 *rec;                                // [W] (sequence, item of it, last work-group, 0): to be joined
+    int64_t q_stride;
+    int64_t B, cap;                           // sequences; rows that a table has pages for
+    int Hq, Hkv, grp, rtiles, logw;
+    float scale;                              // |scale| log2 e
+    int neg;                                  // scale < 0
+};
+
+// Maximum / sum over the four lanes c, c + 16, c + 32, c + 48.  (The swaps' second
+// results go through an empty asm statement, as in half_max.)
+__device__ __forceinline__ float quad_sum(float v)
+{
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    unsigned b = s[1];
+    asm volatile("" : "+v"(b));
+    return half_sum(__builtin_bit_cast(float, (unsigned)s[0]) + __builtin_bit_cast(float, b));
+}
+__device__ __forceinline__ float quad_max(float v)
+{
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    unsigned b = s[1];
+    asm volatile("" : "+v"(b));
+    return half_max(fmaxf(__builtin_bit_cast(float, (unsigned)s[0]), __builtin_bit_cast(float, b)));
+}
+
+// Where the 16-row parts of a tile come from: the line of the first row, how many of the
+// part's rows exist (1 .. 16), and whether its table entry was no page.  A part past the
+// end stands for the tile's first.
+template <int kParts> struct Parts {
+    int64_t line[kParts];
+    int rows[kParts];
+    unsigned bad;
+};
+
+typedef const __attribute__((address_space(4))) int32_t *ConstInts;
+
+// The parts of the tile of keys t0 .. (scalar loads: vector ones would wait for the tiles
+// in flight).  0 <= t0 < len <= cap.
+template <int kParts>
+__device__ __forceinline__ Parts<kParts> parts_of(const PagedArgs &a, int64_t b, int hk, int t0, int len)
+{
+    Parts<kParts> p;
+    p.bad = 0;
+    const ConstInts tab = (ConstInts)(uintptr_t)(a.c.table + b * a.c.max_pages);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        const int r0 = uniform_int(t0 + 16 * i < len ? t0 + 16 * i : t0);
+        int page = tab[r0 >> a.c.shift];
+        if (page < 0 || page >= a.c.num_pages) {
+            page = 0;
+            p.bad |= 1u << i;
+        }
+        p.rows[i] = std::min(16, len - r0);
+        p.line[i] = (((int64_t)page * a.Hkv + hk) << a.c.shift) + (r0 & ((1 << a.c.shift) - 1));
+    }
+    return p;
+}
+
+// What a lane carries of its query heads (CB columns of a block each).
+template <int D, int CB> struct Sums {
+    f32x4 acc[CB][D / 16];                    // acc[.][d][i]: value 16 d + 4 g + i
+    float m[CB], l[CB];
+};
+
+// Raises the running maxima if a score of the tile passes one by kSlack, and turns the
+// scores into unnormalised probabilities.  more(cb, f): sums to be rescaled by f.
+template <int D, int CB, int KB, typename More>
+__device__ __forceinline__ void soften(f32x4 (&s)[CB][KB], float c, Sums<D, CB> &st, More more)
+{
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+        float t = s[cb][0][0];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                t = fmaxf(t, s[cb][kb][i]);
+        t *= c;
+        if (__any(t > st.m[cb] + kSlack)) {
+            const float mn = fmaxf(st.m[cb], quad_max(t)), al = exp2_fast(st.m[cb] - mn);
+            st.m[cb] = mn;
+            st.l[cb] *= al;
+            more(cb, al);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    st.acc[cb][d][i] *= al;
+        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = exp2_fast(below_max(s[cb][kb][i], c, st.m[cb]));
+                st.l[cb] += e;
+                s[cb][kb][i] = e;
+            }
+    }
+}
+
+// Scores of keys from `see` on and of parts in `bad` become -infinity.
+template <int CB, int KB>
+__device__ __forceinline__ void hide(f32x4 (&s)[CB][KB], int see, unsigned bad, int g)
+{
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+        const int lim = bad >> kb & 1u ? -64 : see - 16 * kb - 4 * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i >= lim)
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+                    s[cb][kb][i] = -__builtin_inff();
+    }
+}
+
+// x as kTerms bf16 numbers, the first its rounding and the others that of what is left.
+template <int kTerms> __device__ __forceinline__ void terms_of(const float (&x)[8], bf16x8 (&t)[kTerms])
+{
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        r[e] = x[e];
+#pragma unroll
+    for (int n = 0; n < kTerms; ++n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            t[n][e] = (__bf16)r[e];
+        if (n + 1 < kTerms)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                r[e] -= (float)t[n][e];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Pages of the input type
+// ---------------------------------------------------------------------------
+// bf16: tiles of 32 keys, probabilities as two bf16 numbers (the second product's rounding
+// is then 2^-17 of a term, below the output's).  fp32: tiles of 16, fp32 products.
+template <typename T_, int D, int CB> struct WideTile {
+    typedef T_ T;
+    typedef Tile<T, D> TL;
+    typedef typename Piece<T>::V V;
+    static constexpr bool kHalf = sizeof(T) == 2;
+    static constexpr int kKT = kHalf ? 32 : 16, kParts = kKT / 16, NP = TL::kPitch / 64;
+    static constexpr int kTileBytes = kKT * TL::kPitch, kBuf = 2 * kTileBytes;
+    static constexpr int kNW = 2 * kBuf * 4 <= 128 * 1024 ? 4 : 2;
+    static constexpr int kLoads = 2 * kParts * TileLoad<T, D, 16, 1>::kPer;
+
+    V qf[CB][NP];
+
+    __device__ __forceinline__ void begin(const PagedArgs &a, const T *q, int rows, int lane)
+    {
+        const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                qf[cb][p] = *reinterpret_cast<const V *>(
+                    q + (int64_t)std::min(16 * cb + c, rows - 1) * D + (4 * p + g) * Piece<T>::E);
+                if (a.neg)
+                    qf[cb][p] = flip<T>(qf[cb][p]);
+            }
+    }
+
+    static __device__ __forceinline__ void issue(const PagedArgs &a, unsigned dst, const Parts<kParts> &p, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const unsigned at = dst + (unsigned)(16 * i * TL::kPitch);
+            TileLoad<T, D, 16, 1>::issue(at, (const T *)a.c.k + p.line[i] * D, D, 0, p.rows[i], 0, lane);
+            TileLoad<T, D, 16, 1>::issue(at + kTileBytes, (const T *)a.c.v + p.line[i] * D, D, 0, p.rows[i], 0, lane);
+        }
+    }
+
+    // Values of parts that are no page: 0 (their scores are hidden, and 0 times them must be 0).
+    static __device__ __forceinline__ void clear(unsigned char *buf, unsigned bad, int lane)
+    {
+        for (int i = 0; i < kParts; ++i)
+            if (bad >> i & 1u)
+                for (int x = 16 * lane; x < 16 * TL::kPitch; x += 1024)
+                    *reinterpret_cast<uint4 *>(buf + kTileBytes + 16 * i * TL::kPitch + x) = make_uint4(0, 0, 0, 0);
+    }
+
+    __device__ __forceinline__ void tile(unsigned buf, bool masked, int see, unsigned bad, float c, int lane,
+                                         Sums<D, CB> &st)
+    {
+        typedef LaneBase<T, D> LB;
+        const int cl = lane & 15, g = lane >> 4;
+        f32x4 s[CB][kParts] = {};
+        const unsigned kr = opaque(LB::row16(cl, g));
+#pragma unroll
+        for (int kb = 0; kb < kParts; ++kb)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const V k = LB::piece16(buf + 16 * kb * TL::kPitch, kr, p);
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+                    s[cb][kb] = mma16(k, qf[cb][p], s[cb][kb]);
+            }
+        if (masked)
+            hide(s, see, bad, g);
+        soften<D, CB, kParts>(s, c, st, [](int, float) {});
+        const unsigned vt = buf + kTileBytes;
+        if constexpr (kHalf) {
+            bf16x8 pt[CB][2];
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[e] = s[cb][e >> 2][e & 3];
+                terms_of<2>(x, pt[cb]);
+            }
+            const int r = 4 * g + ((lane >> 2) & 3), q = lane & 3;
+            const unsigned vr = opaque((unsigned)TL::off(r, q >> 1) + (q & 1) * 8);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                const unsigned at = vt + (vr ^ ((unsigned)d << 5));
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s16x4 *)(uintptr_t)(at + 16 * TL::kPitch));
+                const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+                        st.acc[cb][d] = mma16(v, pt[cb][n], st.acc[cb][d]);
+            }
+        } else {
+            // row 4 g + i, column 16 d + c
+            const unsigned vr = opaque((unsigned)(4 * g * TL::kPitch + (((cl >> 2) ^ g) << 4) + (cl & 3) * 4));
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                f32x4 v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = *(const __attribute__((address_space(3))) float *)(uintptr_t)(
+                        vt + i * TL::kPitch + (vr ^ (unsigned)((d ^ i) << 6)));
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+                    st.acc[cb][d] = mma16(v, s[cb][0], st.acc[cb][d]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void finish(Sums<D, CB> &) {}
+};
+
+// ---------------------------------------------------------------------------
+// Pages of 4-bit codes
+// ---------------------------------------------------------------------------
+// Two codes n, n' of a dword's halves become the bf16 pair (16 + n, 16 + n') with a shift
+// and an and-or, and that is the products' operand: with step s and least value m of the
+// 64 values of group G,
+//     q . k_G = s (sum q (16 + n)) + (m - 16 s) sum q        (the 16s: the product's initial value)
+//     sum_t p_t v_t = sum_t (p_t s_t) (16 + n_t) + sum_t p_t (m_t - 16 s_t)
+// so that scales cost one multiply-add per score or probability and group instead of one
+// per value.  Keys are read as stored; values through the 4-bit transpose read, 16 keys
+// of one column at a time.  p s enters as two bf16 numbers (three, and q as three, where
+// queries are fp32).
+//
+// Tiles of 64 keys: [64][D / 2] bytes of keys, the same of values, then the scales
+// [part][group][16 keys] of both.  Rows are not padded; their 16-byte chunks are permuted
+// by an XOR with swz(row), so that reads of 16 rows cover the banks evenly.
+template <typename T_, int D, int CB> struct CodeTile {
+    typedef T_ T;
+    static constexpr int kKT = 64, kParts = 4, G = D / 64;
+    static constexpr int kRow = D / 2, kPart = 16 * kRow, kSide = 4 * kPart, kScales = 4 * 64 * G;
+    static constexpr int kBuf = 2 * kSide + 2 * kScales;
+    static constexpr int kNW = 4;
+    static constexpr int kPer = kPart > 1024 ? kPart / 1024 : 1;          // loads of a part's codes
+    static constexpr int kLoads = kParts * (2 * kPer + 2);
+    static constexpr int kQ = sizeof(T) == 2 ? 1 : 3, kP = sizeof(T) == 2 ? 2 : 3;
+
+    bf16x8 qf[CB][D / 32][kQ];                // queries, in the order of opened()
+    float qs[CB][G];                          // their sums over a group
+    float rest[CB][G];                        // sum of p (m - 16 s)
+
+    static __device__ __forceinline__ int swz(int row)
+    {
+        return D == 64 ? 0 : D == 128 ? (row >> 2) & 3 : (row >> 1) & 7;
+    }
+
+    // Codes 0 .. 7 of a dword as 16 + code, in the order 0, 4, 1, 5, 2, 6, 3, 7.
+    static __device__ __forceinline__ bf16x8 opened(unsigned w)
+    {
+        u32x4 v;
+        v[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
+        v[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
+        v[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
+        v[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+        return __builtin_bit_cast(bf16x8, v);
+    }
+
+    __device__ __forceinline__ void begin(const PagedArgs &a, const T *q, int rows, int lane)
+    {
+        const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int s = 0; s < G; ++s) {
+                float sum = 0.f;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const T *src = q + (int64_t)std::min(16 * cb + c, rows - 1) * D + 64 * s + 16 * g + 8 * p;
+                    float x[8], y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = a.neg ? -(float)src[e] : (float)src[e];
+                        sum += x[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = x[(e >> 1) + 4 * (e & 1)];
+                    terms_of<kQ>(y, qf[cb][2 * s + p]);
+                }
+                qs[cb][s] = quad_sum(sum);
+                rest[cb][s] = 0.f;
+            }
+    }
+
+    // kBytes (16 or 4) per lane of the first `lanes` lanes from the buffer into LDS.
+    static __device__ __forceinline__ void load16(unsigned dst, u32x4 rs, unsigned voff, int lanes, int lane)
+    {
+        if (lane < lanes)
+            lds_load16(dst, rs, voff, 0);
+    }
+    static __device__ __forceinline__ void load4(unsigned dst, u32x4 rs, unsigned voff, int lanes, int lane)
+    {
+        if (lane < lanes)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                         :: "s"(uniform_int((int)dst)), "v"(voff), "s"(rs) : "memory", "m0");
+    }
+
+    static __device__ __forceinline__ void issue(const PagedArgs &a, unsigned dst, const Parts<kParts> &p, int lane)
+    {
+        constexpr int CPR = kRow / 16;                       // chunks of a row
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const int last = p.rows[i] - 1;
+            const u32x4 kr = buffer_words((const unsigned char *)a.c.k + p.line[i] * kRow, (unsigned)(last + 1) * kRow);
+            const u32x4 vr = buffer_words((const unsigned char *)a.c.v + p.line[i] * kRow, (unsigned)(last + 1) * kRow);
+#pragma unroll
+            for (int n = 0; n < kPer; ++n) {
+                const int x = n * 64 + lane, row = x / CPR;
+                const unsigned off = (unsigned)(std::min(row, last) * kRow + (((x % CPR) ^ swz(row)) << 4));
+                load16(dst + i * kPart + n * 1024, kr, off, kPart / 16, lane);
+                load16(dst + kSide + i * kPart + n * 1024, vr, off, kPart / 16, lane);
+            }
+            // lane [group][key] <- dword [key][group]
+            const unsigned off = (unsigned)(std::min(lane & 15, last) * G + (lane >> 4)) * 4u;
+            const unsigned at = dst + 2 * kSide + i * 64 * G;
+            load4(at, buffer_words(a.c.ks + p.line[i] * G, (unsigned)(last + 1) * 4u * G), off, 16 * G, lane);
+            load4(at + kScales, buffer_words(a.c.vs + p.line[i] * G, (unsigned)(last + 1) * 4u * G), off, 16 * G, lane);
+        }
+    }
+
+    // Scales of values of parts that are no page: 0.
+    static __device__ __forceinline__ void clear(unsigned char *buf, unsigned bad, int lane)
+    {
+        for (int i = 0; i < kParts; ++i)
+            if ((bad >> i & 1u) && lane < 16 * G)
+                *reinterpret_cast<unsigned *>(buf + 2 * kSide + kScales + i * 64 * G + 4 * lane) = 0u;
+    }
+
+    static __device__ __forceinline__ u32x4 scales(unsigned at)
+    {
+        return *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)at;
+    }
+
+    __device__ __forceinline__ void tile(unsigned buf, bool masked, int see, unsigned bad, float c, int lane,
+                                         Sums<D, CB> &st)
+    {
+        const int cl = lane & 15, g = lane >> 4;
+        f32x4 sc[CB][kParts];
+        const unsigned kr = opaque((unsigned)(cl * kRow + ((((g >> 1)) ^ swz(cl)) << 4) + (g & 1) * 8));
+#pragma unroll
+        for (int kb = 0; kb < kParts; ++kb)
+#pragma unroll
+            for (int s = 0; s < G; ++s) {
+                const u32x2 w = *(const __attribute__((address_space(3))) u32x2 *)(uintptr_t)(
+                    buf + kb * kPart + (kr ^ (unsigned)(s << 5)));
+                const bf16x8 k0 = opened(w[0]), k1 = opened(w[1]);
+                const u32x4 ws = scales(buf + 2 * kSide + (unsigned)(kb * 64 * G + s * 64 + 16 * g));
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) {
+                    const float b0 = -16.f * qs[cb][s];
+                    f32x4 d = {b0, b0, b0, b0};
+#pragma unroll
+                    for (int n = 0; n < kQ; ++n) {
+                        d = mma16(k0, qf[cb][2 * s][n], d);
+                        d = mma16(k1, qf[cb][2 * s + 1][n], d);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f16x2 h = __builtin_bit_cast(f16x2, (unsigned)ws[i]);
+                        const float r = s == 0 ? (float)h[1] * qs[cb][s]
+                                               : __builtin_fmaf((float)h[1], qs[cb][s], sc[cb][kb][i]);
+                        sc[cb][kb][i] = __builtin_fmaf((float)h[0], d[i], r);
+                    }
+                }
+            }
+        if (masked)
+            hide(sc, see, bad, g);
+        soften<D, CB, kParts>(sc, c, st, [&](int cb, float al) {
+#pragma unroll
+            for (int s = 0; s < G; ++s)
+                rest[cb][s] *= al;
+        });
+        // within 16 lanes, lane r addresses the row of key 16 (r / 4) + 4 g + r % 4
+        const int r = 16 * (cl >> 2) + 4 * g + (cl & 3);
+        const unsigned vr = opaque((unsigned)(r * kRow + (swz(r) << 4)));
+#pragma unroll
+        for (int s = 0; s < G; ++s) {
+            bf16x8 pt[CB][2][kP];
+#pragma unroll
+            for (int kb = 0; kb < kParts; kb += 2) {
+                const u32x4 w0 = scales(buf + 2 * kSide + kScales + (unsigned)(kb * 64 * G + s * 64 + 16 * g));
+                const u32x4 w1 = scales(buf + 2 * kSide + kScales + (unsigned)((kb + 1) * 64 * G + s * 64 + 16 * g));
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const f16x2 h = __builtin_bit_cast(f16x2, (unsigned)(e & 1 ? w1 : w0)[e >> 1]);
+                        const float p = sc[cb][kb + (e & 1)][e >> 1];
+                        x[e] = p * (float)h[0];
+                        rest[cb][s] = __builtin_fmaf(p, (float)h[1], rest[cb][s]);
+                        rest[cb][s] = __builtin_fmaf(-16.f, x[e], rest[cb][s]);
+                    }
+                    terms_of<kP>(x, pt[cb][kb / 2]);
+                }
+            }
+#pragma unroll
+            for (int d = 4 * s; d < 4 * s + 4; ++d) {
+                const v2i w = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                    (lds_v2i *)(uintptr_t)(buf + kSide + (vr ^ (unsigned)((d >> 1) << 4)) + (d & 1) * 8));
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const bf16x8 v = opened((unsigned)w[x]);
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                        for (int n = 0; n < kP; ++n)
+                            st.acc[cb][d] = mma16(v, pt[cb][x][n], st.acc[cb][d]);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void finish(Sums<D, CB> &st)
+    {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int s = 0; s < G; ++s) {
+                const float r = quad_sum(rest[cb][s]);
+#pragma unroll
+                for (int d = 4 * s; d < 4 * s + 4; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        st.acc[cb][d][i] += r;
+            }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+// Tokens of sequence b, 0 for an unused slot.
+__device__ __forceinline__ int filled(const PagedArgs &a, int64_t b)
+{
+    const int at = a.lengths[b];
+    return at < 0 || at >= a.cap ? 0 : at + 1;
+}
+
+template <typename Eng, int D, int CB, int kOcc>
+__global__ __launch_bounds__(64 * Eng::kNW, kOcc * Eng::kNW / 4 > 0 ? kOcc * Eng::kNW / 4 : 1)
+void paged_decode_kernel(PagedArgs a)
+{
+    typedef typename Eng::T T;
+    constexpr int NW = Eng::kNW, NT = 64 * NW, KT = Eng::kKT, STEP = KT * NW;
+    constexpr unsigned kWave = 2u * Eng::kBuf;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ float sm[NW][16 * CB], sl[NW][16 * CB];
+    __shared__ int64_t wsum[NW], found[2];
+
+    const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int W = 1 << a.logw, HR = a.Hkv * a.rtiles;
+
+    // unused slots
+    for (int64_t b = blockIdx.x; b < a.B; b += W)
+        if (filled(a, b) == 0)
+            for (int64_t i = tid; i < (int64_t)a.Hq * D; i += NT)
+                ((T *)a.o)[b * a.Hq * D + i] = (T)0.f;
+
+    // this work-group's units [u0, u1) of all, and the sequence that u0 lies in
+    const int64_t per = (a.B + NT - 1) / NT, b0 = tid * per, b1 = std::min<int64_t>(a.B, b0 + per);
+    int64_t mine = 0;
+    for (int64_t b = b0; b < b1; ++b)
+        mine += (filled(a, b) + STEP - 1) / STEP;
+    int64_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int64_t up = __shfl_up(incl, off, 64);
+        if (lane >= off)
+            incl += up;
+    }
+    if (lane == 63)
+        wsum[w] = incl;
+    if (tid == 0)
+        found[0] = -1;
+    __syncthreads();
+    int64_t total = 0, excl = incl - mine;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        if (i < w)
+            excl += wsum[i];
+        total += wsum[i];
+    }
+    const int64_t all = total * HR;
+    // (few units: one each, so that every work-group of an item has a piece of it)
+    const bool few = all <= W;
+    const int64_t u0 = few ? std::min<int64_t>(all, blockIdx.x) : (all * blockIdx.x) >> a.logw;
+    const int64_t u1 = few ? std::min<int64_t>(all, blockIdx.x + 1) : (all * (blockIdx.x + 1)) >> a.logw;
+    if (u0 >= excl * HR && u0 < (excl + mine) * HR) {
+        int64_t b = b0;
+        for (; b + 1 < b1; ++b) {
+            const int64_t n = (filled(a, b) + STEP - 1) / STEP;
+            if (u0 < (excl + n) * HR)
+                break;
+            excl += n;
+        }
+        found[0] = b;
+        found[1] = excl;
+    }
+    __syncthreads();
+    if (tid == 0)
+        a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (u0 >= u1 || found[0] < 0)
+        return;
+    int64_t b = found[0], first = found[1] * HR;              // first unit of the sequence
+    int len = uniform_int(filled(a, b));
+    int units = (len + STEP - 1) / STEP;
+    if (u0 >= first + (int64_t)units * HR)                    // (lengths that change under the kernel end it)
+        return;
+    int item = (int)((u0 - first) / units);
+    int from = (int)((u0 - first) % units);
+
+    unsigned char *own = smem + w * kWave;
+    const unsigned lds0 = lds_addr(own);
+
+    for (int64_t u = u0; u < u1;) {
+        const int to = (int)std::min<int64_t>(units, from + (u1 - u));
+        const int rt = item % a.rtiles, hk = item / a.rtiles;
+        const int rows = std::min(16 * CB, a.grp - 16 * CB * rt);
+        const int64_t h0 = (int64_t)hk * a.grp + 16 * CB * rt;
+        const int kend = (int)std::min<int64_t>((int64_t)to * STEP, len);
+
+        Eng eng;
+        eng.begin(a, (const T *)a.q + b * a.q_stride + h0 * D, rows, lane);
+        Sums<D, CB> st;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            st.m[cb] = kNoMax;
+            st.l[cb] = 0.f;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+                st.acc[cb][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        wait_vmcnt<0>();                                      // (stores of the item before, too)
+        int t0 = from * STEP + KT * w;
+        Parts<Eng::kParts> cur = {}, nxt = {};
+        if (t0 < kend) {
+            cur = parts_of<Eng::kParts>(a, b, hk, t0, len);
+            Eng::issue(a, lds0, cur, lane);
+            if (t0 + STEP < kend)
+                nxt = parts_of<Eng::kParts>(a, b, hk, t0 + STEP, len);
+        }
+        for (int n = 0; t0 < kend; ++n, t0 += STEP) {
+            const unsigned slot = (unsigned)(n & 1) * Eng::kBuf;
+            // the slot issued next was read by this wave before: its reads are done
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            const unsigned bad = cur.bad;
+            if (t0 + STEP < kend) {
+                Eng::issue(a, lds0 + (Eng::kBuf - slot), nxt, lane);
+                cur = nxt;
+                if (t0 + 2 * STEP < kend)
+                    nxt = parts_of<Eng::kParts>(a, b, hk, t0 + 2 * STEP, len);
+                wait_vmcnt<Eng::kLoads>();
+            } else {
+                wait_vmcnt<0>();
+            }
+            if (bad) {
+                Eng::clear(own + slot, bad, lane);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+            eng.tile(lds0 + slot, t0 + KT > len || bad != 0, len - t0, bad, a.scale, lane, st);
+        }
+        eng.finish(st);
+
+        // the waves' sums to a common maximum
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            const float l = quad_sum(st.l[cb]);
+            if (g == 0) {
+                sm[w][16 * cb + c] = st.m[cb];
+                sl[w][16 * cb + c] = l;
+            }
+        }
+        __syncthreads();
+        float *wp = reinterpret_cast<float *>(own);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            float mt = sm[0][16 * cb + c];
+#pragma unroll
+            for (int i = 1; i < NW; ++i)
+                mt = fmaxf(mt, sm[i][16 * cb + c]);
+            const float f = exp2_fast(st.m[cb] - mt);
+            if (16 * cb + c < rows)
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d)
+                    *reinterpret_cast<f32x4 *>(wp + (16 * cb + c) * D + 16 * d + 4 * g) =
+                        f32x4{st.acc[cb][d][0] * f, st.acc[cb][d][1] * f, st.acc[cb][d][2] * f, st.acc[cb][d][3] * f};
+        }
+        __syncthreads();
+        const bool whole = from == 0 && to == units;
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0)) * 16 * CB;
+        T *op = (T *)a.o + (b * a.Hq + h0) * D;
+        for (int i = 4 * tid; i < rows * D; i += 4 * NT) {
+            const int row = i / D;
+            f32x4 v = *reinterpret_cast<const f32x4 *>(smem + i * 4);
+#pragma unroll
+            for (int k = 1; k < NW; ++k)
+                v += *reinterpret_cast<const f32x4 *>(smem + k * kWave + i * 4);
+            float mr = sm[0][row], lr = 0.f;
+#pragma unroll
+            for (int k = 1; k < NW; ++k)
+                mr = fmaxf(mr, sm[k][row]);
+#pragma unroll
+            for (int k = 0; k < NW; ++k)
+                lr += sl[k][row] * exp2_fast(sm[k][row] - mr);
+            if (whole) {
+                const float inv = lr > 0.f ? 1.f / lr : 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    op[i + e] = (T)(v[e] * inv);
+            } else {
+                *reinterpret_cast<f32x4 *>(a.part + slot * D + i) = v;
+                if (i % D == 0)
+                    a.ml[slot + row] = make_float2(mr, lr);
+            }
+        }
+        if (!whole && from == 0 && tid == 0) {
+            // units [first + item units, + units): the work-group of the last one
+            const int64_t last = first + (int64_t)(item + 1) * units - 1;
+            const int64_t wl = few ? last : (((last + 1) << a.logw) - 1) / all;
+            a.rec[blockIdx.x] = make_int4((int)b, item, (int)wl, 0);
+        }
+        __syncthreads();                                      // (the LDS is written again)
+
+        u += to - from;
+        from = 0;
+        if (u < u1 && ++item == HR) {
+            // the next sequence that has tokens
+            item = 0;
+            first += (int64_t)HR * units;
+            for (b += 1; b < a.B; b += 64) {
+                const uint64_t some = __ballot(b + lane < a.B && filled(a, std::min(a.B - 1, b + lane)) > 0);
+                if (some) {
+                    b += __builtin_ctzll(some);
+                    break;
+                }
+            }
+            len = b < a.B ? uniform_int(filled(a, b)) : 0;
+            units = (len + STEP - 1) / STEP;
+            if (units == 0)
+                return;
+        }
+    }
+}
+
+// Joins the pieces of the item that work-group blockIdx.x began and others ended.
+template <typename T, int D, int CB> __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a)
+{
+    constexpr int LPR = D / 4, G = 256 / LPR;
+    __shared__ float4 sacc[G][LPR];
+    __shared__ float sl[G];
+    const int4 rec = a.rec[blockIdx.x];
+    if (rec.x < 0)
+        return;
+    const int tid = threadIdx.x, gr = tid / LPR, d4 = tid % LPR;
+    const int w0 = blockIdx.x, n = rec.z - w0 + 1;
+    const int rt = rec.y % a.rtiles, hk = rec.y / a.rtiles, row = blockIdx.y;
+    if (row >= std::min(16 * CB, a.grp - 16 * CB * rt))
+        return;
+    const int64_t h = (int64_t)hk * a.grp + 16 * CB * rt + row;
+    // piece 0: the second slot of w0; piece i: the first of w0 + i
+    auto at = [&](int i) { return (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * 16 * CB + row; };
+    float mx = kNoMax;
+    for (int i = tid & 63; i < n; i += 64)
+        mx = fmaxf(mx, a.ml[at(i)].x);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    constexpr int U = 4;
+    for (int i0 = gr; i0 < n; i0 += G * U) {
+        float2 ml[U];
+        float4 p[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t s = at(std::min(i0 + u * G, n - 1));
+            ml[u] = a.ml[s];
+            p[u] = *reinterpret_cast<const float4 *>(a.part + s * D + 4 * d4);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = i0 + u * G < n ? exp2_fast(ml[u].x - mx) : 0.f;
+            v.x += f * p[u].x; v.y += f * p[u].y; v.z += f * p[u].z; v.w += f * p[u].w;
+            l += f * ml[u].y;
+        }
+    }
+    sacc[gr][d4] = v;
+    if (d4 == 0)
+        sl[gr] = l;
+    __syncthreads();
+    if (tid < LPR) {
+        for (int i = 1; i < G; ++i) {
+            const float4 p = sacc[i][d4];
+            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+            l += sl[i];
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        T *op = (T *)a.o + ((int64_t)rec.x * a.Hq + h) * D + 4 * d4;
+        op[0] = (T)(v.x * inv);
+        op[1] = (T)(v.y * inv);
+        op[2] = (T)(v.z * inv);
+        op[3] = (T)(v.w * inv);
+    }
+}
+
+// Work-groups that fit a CU by their LDS, and as many times 256 CUs of them.
+template <typename Eng> constexpr int occupancy()
+{
+    const int n = 160 * 1024 / (Eng::kNW * 2 * Eng::kBuf + 1024);
+    return n >= 4 ? 4 : n >= 2 ? 2 : 1;
+}
+template <typename Eng> constexpr int log_groups()
+{
+    return occupancy<Eng>() == 4 ? 10 : occupancy<Eng>() == 2 ? 9 : 8;
+}
+
+// Calls f(engine, D, CB) for the call's types and sizes.
+template <typename F> auto with_engine(int bf16, int q4, int64_t D, bool two, F f)
+{
+#define SSD_PAGED(T, D_)                                                                                 \
+    (q4 ? (two ? f((CodeTile<T, D_, 2> *)nullptr, std::integral_constant<int, D_>(), std::integral_constant<int, 2>()) \
+               : f((CodeTile<T, D_, 1> *)nullptr, std::integral_constant<int, D_>(), std::integral_constant<int, 1>())) \
+        : (two ? f((WideTile<T, D_, 2> *)nullptr, std::integral_constant<int, D_>(), std::integral_constant<int, 2>()) \
+               : f((WideTile<T, D_, 1> *)nullptr, std::integral_constant<int, D_>(), std::integral_constant<int, 1>())))
+    if (bf16)
+        return D == 64 ? SSD_PAGED(__bf16, 64) : D == 128 ? SSD_PAGED(__bf16, 128) : SSD_PAGED(__bf16, 256);
+    return D == 64 ? SSD_PAGED(float, 64) : D == 128 ? SSD_PAGED(float, 128) : SSD_PAGED(float, 256);
+#undef SSD_PAGED
+}
+
+}  // namespace
+
+// (Up to 16 query heads of a key head are one block of columns, more are items of 32.)
+size_t paged_decode_workspace(int bf16, int q4, int64_t B, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    if (B == 0)
+        return 0;
+    return with_engine(bf16, q4, D, Hq / Hkv > 16, [D](auto *e, auto, auto cb) {
+        const size_t W = size_t(1) << log_groups<std::remove_pointer_t<decltype(e)>>();
+        return W * (2 * 16 * decltype(cb)::value * (size_t)(D * 4 + 8) + 16);
+    });
+}
+
+hipError_t launch_paged_decode(int bf16, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                               int64_t q_stride, float scale, const void *q, const PagedCache &cache,
+                               const int32_t *lengths, void *o, void *ws, hipStream_t s)
+{
+    PagedArgs a = {};
+    a.c = cache;
+    a.q = q;
+    a.lengths = lengths;
+    a.o = o;
+    a.q_stride = q_stride;
+    a.B = B;
+    a.cap = cache.max_pages << cache.shift;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.grp = (int)(Hq / Hkv);
+    a.scale = score_factor(scale);
+    a.neg = scale < 0.f;
+    return with_engine(bf16, cache.ks != nullptr, D, a.grp > 16, [&](auto *e, auto dim, auto cols) {
+        typedef std::remove_pointer_t<decltype(e)> Eng;
+        constexpr int kD = decltype(dim)::value, CB = decltype(cols)::value, kOcc = occupancy<Eng>();
+        constexpr unsigned kSmem = Eng::kNW * 2u * Eng::kBuf;
+        static_assert(16 * CB * kD * 4 <= 2 * Eng::kBuf, "a wave's sums fit its tiles");
+        a.rtiles = (a.grp + 16 * CB - 1) / (16 * CB);
+        a.logw = log_groups<Eng>();
+        const unsigned W = 1u << a.logw;
+        a.part = static_cast<float *>(ws);
+        a.ml = reinterpret_cast<float2 *>(a.part + (size_t)2 * W * 16 * CB * kD);
+        a.rec = reinterpret_cast<int4 *>(a.ml + (size_t)2 * W * 16 * CB);
+        static std::atomic<uint64_t> allowed{0};
+        const auto kernel = &paged_decode_kernel<Eng, kD, CB, kOcc>;
+        hipError_t err = allow_lds(reinterpret_cast<const void *>(kernel), (int)kSmem, allowed);
+        if (err != hipSuccess)
+            return err;
+        kernel<<<dim3(W), dim3(64 * Eng::kNW), kSmem, s>>>(a);
+        if ((err = hipGetLastError()) != hipSuccess || a.cap <= Eng::kNW * Eng::kKT)
+            return err;                       // (items of one unit are never cut)
+        paged_join_kernel<typename Eng::T, kD, CB>
+            <<<dim3(W, (unsigned)std::min(a.grp, 16 * CB)), dim3(256), 0, s>>>(a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace ssd
