@@ -1457,9 +1457,11 @@ ssd_status paged_decode_check(const ssd_paged_dims *d, PagedShape *sh)
         return st;
     if (!std::isfinite(d->scale))
         return SSD_ERR_UNSUPPORTED;
-    // (units of all items, 64 bits of them times the number of work-groups)
-    const int64_t rtiles = (d->q_heads / d->kv_heads + 31) / 32;
-    if (d->batch > kMaxGroups / (d->kv_heads * rtiles))
+    // (units of at least 32 rows are counted in 32 bits: those of all sequences, and those of
+    // all heads of one)
+    const int64_t rtiles = (d->q_heads / d->kv_heads + 31) / 32, most = int64_t(1) << 36;
+    if (d->batch > kMaxGroups / (d->kv_heads * rtiles) || sh->cap + 32 > most / (2 * d->kv_heads * rtiles) ||
+        d->batch * 2 > most / (sh->cap + 32))
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }

@@ -71,9 +71,9 @@ __device__ __forceinline__ float quad_max(float v)
     return half_max(fmaxf(__builtin_bit_cast(float, (unsigned)s[0]), __builtin_bit_cast(float, b)));
 }
 
-// Where the 16-row parts of a tile come from: the line of the first row, how many of the
-// part's rows exist (1 .. 16), and whether its table entry was no page.  A part past the
-// end stands for the tile's first.
+// Where the 16-row parts of a tile come from: the line of the first row among all pages'
+// (of all heads), how many of the part's rows exist (1 .. 16), and whether its table entry
+// was no page.  A part past the end stands for the tile's first.
 template <int kParts> struct Parts {
     int64_t line[kParts];
     int rows[kParts];
@@ -82,24 +82,46 @@ template <int kParts> struct Parts {
 
 typedef const __attribute__((address_space(4))) int32_t *ConstInts;
 
+__device__ __forceinline__ int64_t first_line(const PagedArgs &a, int page, int hk, int row)
+{
+    return (int64_t)(((uint64_t)(unsigned)page * (unsigned)a.Hkv + (unsigned)hk) << a.c.shift) +
+           (row & ((1 << a.c.shift) - 1));
+}
+
 // The parts of the tile of keys t0 .. (scalar loads: vector ones would wait for the tiles
-// in flight).  0 <= t0 < len <= cap.
+// in flight).  0 <= t0 < len <= cap.  A tile that lies in one page needs one entry.
 template <int kParts>
 __device__ __forceinline__ Parts<kParts> parts_of(const PagedArgs &a, int64_t b, int hk, int t0, int len)
 {
     Parts<kParts> p;
     p.bad = 0;
     const ConstInts tab = (ConstInts)(uintptr_t)(a.c.table + b * a.c.max_pages);
+    const unsigned npages = (unsigned)a.c.num_pages;
+    if ((16 * kParts) >> a.c.shift <= 1) {
+        int page = tab[uniform_int(t0) >> a.c.shift];
+        if ((unsigned)page >= npages) {
+            page = 0;
+            p.bad = (1u << kParts) - 1;
+        }
+        const int64_t line = first_line(a, page, hk, t0);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const bool there = t0 + 16 * i < len;
+            p.line[i] = there ? line + 16 * i : line;
+            p.rows[i] = std::min(16, len - (there ? t0 + 16 * i : t0));
+        }
+        return p;
+    }
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
         const int r0 = uniform_int(t0 + 16 * i < len ? t0 + 16 * i : t0);
         int page = tab[r0 >> a.c.shift];
-        if (page < 0 || page >= a.c.num_pages) {
+        if ((unsigned)page >= npages) {
             page = 0;
             p.bad |= 1u << i;
         }
         p.rows[i] = std::min(16, len - r0);
-        p.line[i] = (((int64_t)page * a.Hkv + hk) << a.c.shift) + (r0 & ((1 << a.c.shift) - 1));
+        p.line[i] = first_line(a, page, hk, r0);
     }
     return p;
 }
@@ -135,11 +157,22 @@ __device__ __forceinline__ void soften(f32x4 (&s)[CB][KB], float c, Sums<D, CB> 
                 for (int i = 0; i < 4; ++i)
                     st.acc[cb][d][i] *= al;
         }
+        // the exponents as one fused operation each, but for huge scores
+        float ec = c, em = st.m[cb];
+        if (__builtin_expect(__any(fabsf(em) > 16777216.f && em != kNoMax), 0)) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[cb][kb][i] = below_max(s[cb][kb][i], c, st.m[cb]);
+            ec = 1.f;
+            em = 0.f;
+        }
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float e = exp2_fast(below_max(s[cb][kb][i], c, st.m[cb]));
+                const float e = exp2_fast(__builtin_fmaf(s[cb][kb][i], ec, -em));
                 st.l[cb] += e;
                 s[cb][kb][i] = e;
             }
@@ -150,6 +183,7 @@ __device__ __forceinline__ void soften(f32x4 (&s)[CB][KB], float c, Sums<D, CB> 
 template <int CB, int KB>
 __device__ __forceinline__ void hide(f32x4 (&s)[CB][KB], int see, unsigned bad, int g)
 {
+    asm volatile("" : "+v"(g));               // (nothing of this ahead of the branch that leads here)
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
         const int lim = bad >> kb & 1u ? -64 : see - 16 * kb - 4 * g;
@@ -171,13 +205,16 @@ template <int kTerms> __device__ __forceinline__ void terms_of(const float (&x)[
         r[e] = x[e];
 #pragma unroll
     for (int n = 0; n < kTerms; ++n) {
+        u32x4 u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            t[n][e] = (__bf16)r[e];
-        if (n + 1 < kTerms)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                r[e] -= (float)t[n][e];
+        for (int e = 0; e < 4; ++e) {
+            u[e] = opaque(pack_bf16(r[2 * e], r[2 * e + 1]));
+            if (n + 1 < kTerms) {
+                r[2 * e] -= __uint_as_float(u[e] << 16);
+                r[2 * e + 1] -= __uint_as_float(u[e] & 0xffff0000u);
+            }
+        }
+        t[n] = __builtin_bit_cast(bf16x8, u);
     }
 }
 
@@ -212,7 +249,14 @@ template <typename T_, int D, int CB> struct WideTile {
             }
     }
 
-    static __device__ __forceinline__ void issue(const PagedArgs &a, unsigned dst, const Parts<kParts> &p, int lane)
+    static constexpr int kWhole = kLoads;
+    static __device__ __forceinline__ bool whole(const PagedArgs &, int, int)
+    {
+        return false;
+    }
+
+    static __device__ __forceinline__ void issue(const PagedArgs &a, unsigned dst, const Parts<kParts> &p, bool,
+                                                 int lane)
     {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
@@ -323,21 +367,25 @@ template <typename T_, int D, int CB> struct CodeTile {
     static constexpr int kPer = kPart > 1024 ? kPart / 1024 : 1;          // loads of a part's codes
     static constexpr int kLoads = kParts * (2 * kPer + 2);
     static constexpr int kQ = sizeof(T) == 2 ? 1 : 3, kP = sizeof(T) == 2 ? 2 : 3;
+    static constexpr bool kCentred = sizeof(T) == 4;
 
+    // (constants kept in registers: as literals they would split and-or into two instructions)
+    unsigned mask, sixteen, low, hundred;
+    float zero;
     bf16x8 qf[CB][D / 32][kQ];                // queries, in the order of opened()
-    float qs[CB][G];                          // their sums over a group
-    float rest[CB][G];                        // sum of p (m - 16 s)
+    float qs[CB][G], qb[CB][G];               // their sums over a group, as they are and times the keys' biases
+    float rest[CB][G];                        // sum of p m (centred: p (m + 8 s))
+    f32x4 over[kCentred ? 1 : CB][kCentred ? 1 : G];   // the values' biases times p s, summed
 
     static __device__ __forceinline__ int swz(int row)
     {
         return D == 64 ? 0 : D == 128 ? (row >> 2) & 3 : (row >> 1) & 7;
     }
 
-    static constexpr bool kCentred = sizeof(T) == 4;
-
     // Codes 0 .. 7 of a dword as 16 + code (centred: (code - 8) / 16), in the order 0, 4, 1,
-    // 5, 2, 6, 3, 7.
-    static __device__ __forceinline__ bf16x8 opened(unsigned w)
+    // 5, 2, 6, 3, 7.  kKey: the first two as 128 + code, which saves a shift; sums over values
+    // keep to 16, their biases being part of a sum over all rows.
+    template <bool kKey> __device__ __forceinline__ bf16x8 opened(unsigned w) const
     {
         u32x4 v;
         if constexpr (kCentred) {
@@ -348,21 +396,27 @@ template <typename T_, int D, int CB> struct CodeTile {
                                  __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * i + 16))));
             return __builtin_bit_cast(bf16x8, v);
         }
-        v[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-        v[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-        v[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-        v[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+        v[0] = kKey ? (w & low) | hundred : ((w << 3) & mask) | sixteen;
+        v[1] = ((w >> 1) & mask) | sixteen;
+        v[2] = ((w >> 5) & mask) | sixteen;
+        v[3] = ((w >> 9) & mask) | sixteen;
         return __builtin_bit_cast(bf16x8, v);
     }
 
     __device__ __forceinline__ void begin(const PagedArgs &a, const T *q, int rows, int lane)
     {
         const int c = lane & 15, g = lane >> 4;
+        mask = 0x00780078u;
+        sixteen = 0x41804180u;
+        low = 0x000f000fu;
+        hundred = 0x43004300u;                // 128
+        zero = 0.f;
+        asm volatile("" : "+s"(mask), "+v"(sixteen), "+s"(low), "+v"(hundred), "+v"(zero));
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int s = 0; s < G; ++s) {
-                float sum = 0.f;
+                float sum = 0.f, first = 0.f;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     const T *src = q + (int64_t)std::min(16 * cb + c, rows - 1) * D + 64 * s + 16 * g + 8 * p;
@@ -372,49 +426,85 @@ template <typename T_, int D, int CB> struct CodeTile {
                         x[e] = a.neg ? -(float)src[e] : (float)src[e];
                         sum += x[e];
                     }
+                    first += x[0] + x[4];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         y[e] = x[(e >> 1) + 4 * (e & 1)];
                     terms_of<kQ>(y, qf[cb][2 * s + p]);
                 }
                 qs[cb][s] = quad_sum(sum);
+                qb[cb][s] = kCentred ? 0.f : __builtin_fmaf(-112.f, quad_sum(first), -16.f * qs[cb][s]);
                 rest[cb][s] = 0.f;
+                if constexpr (!kCentred)
+                    over[cb][s] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
     }
 
-    // kBytes (16 or 4) per lane of the first `lanes` lanes from the buffer into LDS.
-    static __device__ __forceinline__ void load16(unsigned dst, u32x4 rs, unsigned voff, int lanes, int lane)
+    // 16 or 4 bytes per lane of the first kLanes lanes from base + voff into LDS (assembly for
+    // the reasons given at lds_load16).
+    template <int kLanes> static __device__ __forceinline__ void load16(unsigned dst, const unsigned char *base, unsigned voff, int lane)
     {
-        if (lane < lanes)
-            lds_load16(dst, rs, voff, 0);
+        if (kLanes >= 64 || lane < kLanes)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                         :: "s"(uniform_int((int)dst)), "v"(voff), "s"(base) : "memory", "m0");
     }
-    static __device__ __forceinline__ void load4(unsigned dst, u32x4 rs, unsigned voff, int lanes, int lane)
+    template <int kLanes> static __device__ __forceinline__ void load4(unsigned dst, const unsigned char *base, unsigned voff, int lane)
     {
-        if (lane < lanes)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                         :: "s"(uniform_int((int)dst)), "v"(voff), "s"(rs) : "memory", "m0");
+        if (kLanes >= 64 || lane < kLanes)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                         :: "s"(uniform_int((int)dst)), "v"(voff), "s"(base) : "memory", "m0");
     }
 
-    static __device__ __forceinline__ void issue(const PagedArgs &a, unsigned dst, const Parts<kParts> &p, int lane)
+    // A tile's loads: kWhole where its 64 rows exist and lie in one page, else part by part.
+    static constexpr int kWhole = 2 * (kSide / 1024) + 2 * G;
+    static __device__ __forceinline__ bool whole(const PagedArgs &a, int t0, int len)
+    {
+        return a.c.shift >= 6 && t0 + kKT <= len;
+    }
+
+    static __device__ __forceinline__ void issue(const PagedArgs &a, unsigned dst, const Parts<kParts> &p, bool all,
+                                                 int lane)
     {
         constexpr int CPR = kRow / 16;                       // chunks of a row
+        // (kRow is 32 G and a row's scales take 4 G bytes)
+        if (all) {
+            const unsigned char *kp = (const unsigned char *)a.c.k + p.line[0] * kRow;
+            const unsigned char *vp = (const unsigned char *)a.c.v + p.line[0] * kRow;
+            const unsigned char *ks = (const unsigned char *)a.c.ks + p.line[0] * (4 * G);
+            const unsigned char *vs = (const unsigned char *)a.c.vs + p.line[0] * (4 * G);
+#pragma unroll
+            for (int n = 0; n < kSide / 1024; ++n) {
+                const int x = n * 64 + lane, row = x / CPR;
+                const unsigned off = (unsigned)(row * kRow + (((x % CPR) ^ swz(row)) << 4));
+                load16<64>(dst + n * 1024, kp, off, lane);
+                load16<64>(dst + kSide + n * 1024, vp, off, lane);
+            }
+#pragma unroll
+            for (int n = 0; n < G; ++n) {
+                // dword [part][group][key] <- [key][group]
+                const int x = n * 64 + lane, key = 16 * (x / (16 * G)) + x % 16, grp = x % (16 * G) / 16;
+                const unsigned off = (unsigned)(key * G + grp) * 4u;
+                load4<64>(dst + 2 * kSide + n * 256, ks, off, lane);
+                load4<64>(dst + 2 * kSide + kScales + n * 256, vs, off, lane);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             const int last = p.rows[i] - 1;
-            const u32x4 kr = buffer_words((const unsigned char *)a.c.k + p.line[i] * kRow, (unsigned)(last + 1) * kRow);
-            const u32x4 vr = buffer_words((const unsigned char *)a.c.v + p.line[i] * kRow, (unsigned)(last + 1) * kRow);
+            const unsigned char *kp = (const unsigned char *)a.c.k + p.line[i] * kRow;
+            const unsigned char *vp = (const unsigned char *)a.c.v + p.line[i] * kRow;
 #pragma unroll
             for (int n = 0; n < kPer; ++n) {
                 const int x = n * 64 + lane, row = x / CPR;
                 const unsigned off = (unsigned)(std::min(row, last) * kRow + (((x % CPR) ^ swz(row)) << 4));
-                load16(dst + i * kPart + n * 1024, kr, off, kPart / 16, lane);
-                load16(dst + kSide + i * kPart + n * 1024, vr, off, kPart / 16, lane);
+                load16<kPart / 16>(dst + i * kPart + n * 1024, kp, off, lane);
+                load16<kPart / 16>(dst + kSide + i * kPart + n * 1024, vp, off, lane);
             }
-            // lane [group][key] <- dword [key][group]
             const unsigned off = (unsigned)(std::min(lane & 15, last) * G + (lane >> 4)) * 4u;
             const unsigned at = dst + 2 * kSide + i * 64 * G;
-            load4(at, buffer_words(a.c.ks + p.line[i] * G, (unsigned)(last + 1) * 4u * G), off, 16 * G, lane);
-            load4(at + kScales, buffer_words(a.c.vs + p.line[i] * G, (unsigned)(last + 1) * 4u * G), off, 16 * G, lane);
+            load4<16 * G>(at, (const unsigned char *)a.c.ks + p.line[i] * (4 * G), off, lane);
+            load4<16 * G>(at + kScales, (const unsigned char *)a.c.vs + p.line[i] * (4 * G), off, lane);
         }
     }
 
@@ -443,12 +533,11 @@ template <typename T_, int D, int CB> struct CodeTile {
             for (int s = 0; s < G; ++s) {
                 const u32x2 w = *(const __attribute__((address_space(3))) u32x2 *)(uintptr_t)(
                     buf + kb * kPart + (kr ^ (unsigned)(s << 5)));
-                const bf16x8 k0 = opened(w[0]), k1 = opened(w[1]);
+                const bf16x8 k0 = opened<true>(w[0]), k1 = opened<true>(w[1]);
                 const u32x4 ws = scales(buf + 2 * kSide + (unsigned)(kb * 64 * G + s * 64 + 16 * g));
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb) {
-                    const float b0 = kCentred ? 0.f : -16.f * qs[cb][s];
-                    f32x4 d = {b0, b0, b0, b0};
+                    f32x4 d = {qb[cb][s], qb[cb][s], qb[cb][s], qb[cb][s]};
 #pragma unroll
                     for (int n = 0; n < kQ; ++n) {
                         d = mma16(k0, qf[cb][2 * s][n], d);
@@ -459,7 +548,7 @@ template <typename T_, int D, int CB> struct CodeTile {
                         const f16x2 h = __builtin_bit_cast(f16x2, (unsigned)ws[i]);
                         const float step = kCentred ? 16.f * (float)h[0] : (float)h[0];
                         const float least = kCentred ? __builtin_fmaf(8.f, (float)h[0], (float)h[1]) : (float)h[1];
-                        const float r = s == 0 ? least * qs[cb][s] : __builtin_fmaf(least, qs[cb][s], sc[cb][kb][i]);
+                        const float r = __builtin_fmaf(least, qs[cb][s], s == 0 ? zero : sc[cb][kb][i]);
                         sc[cb][kb][i] = __builtin_fmaf(step, d[i], r);
                     }
                 }
@@ -468,8 +557,11 @@ template <typename T_, int D, int CB> struct CodeTile {
             hide(sc, see, bad, g);
         soften<D, CB, kParts>(sc, c, st, [&](int cb, float al) {
 #pragma unroll
-            for (int s = 0; s < G; ++s)
+            for (int s = 0; s < G; ++s) {
                 rest[cb][s] *= al;
+                if constexpr (!kCentred)
+                    over[cb][s] *= al;
+            }
         });
         // within 16 lanes, lane r addresses the row of key 16 (r / 4) + 4 g + r % 4
         const int r = 16 * (cl >> 2) + 4 * g + (cl & 3);
@@ -492,12 +584,15 @@ template <typename T_, int D, int CB> struct CodeTile {
                             x[e] = p * (16.f * (float)h[0]);
                             rest[cb][s] = __builtin_fmaf(p, __builtin_fmaf(8.f, (float)h[0], (float)h[1]), rest[cb][s]);
                         } else {
-                            x[e] = p * (float)h[0];
+                            x[e] = __builtin_fmaf(p, (float)h[0], zero);
                             rest[cb][s] = __builtin_fmaf(p, (float)h[1], rest[cb][s]);
-                            rest[cb][s] = __builtin_fmaf(-16.f, x[e], rest[cb][s]);
                         }
                     }
                     terms_of<kP>(x, pt[cb][kb / 2]);
+                    if constexpr (!kCentred)
+#pragma unroll
+                        for (int n = 0; n < kP; ++n)
+                            over[cb][s] = mma16(opened<false>(0u), pt[cb][kb / 2][n], over[cb][s]);
                 }
             }
 #pragma unroll
@@ -506,7 +601,7 @@ template <typename T_, int D, int CB> struct CodeTile {
                     (lds_v2i *)(uintptr_t)(buf + kSide + (vr ^ (unsigned)((d >> 1) << 4)) + (d & 1) * 8));
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const bf16x8 v = opened((unsigned)w[x]);
+                    const bf16x8 v = opened<false>((unsigned)w[x]);
 #pragma unroll
                     for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
@@ -523,7 +618,9 @@ template <typename T_, int D, int CB> struct CodeTile {
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int s = 0; s < G; ++s) {
-                const float r = quad_sum(rest[cb][s]);
+                float r = quad_sum(rest[cb][s]);
+                if constexpr (!kCentred)
+                    r -= over[cb][s][0];          // (all rows of it are alike)
 #pragma unroll
                 for (int d = 4 * s; d < 4 * s + 4; ++d)
 #pragma unroll
@@ -552,81 +649,113 @@ void paged_decode_kernel(PagedArgs a)
     constexpr unsigned kWave = 2u * Eng::kBuf;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float sm[NW][16 * CB], sl[NW][16 * CB];
-    __shared__ int64_t wsum[NW], found[2];
+    __shared__ int wsum[NW], where[2];
 
     const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int W = 1 << a.logw, HR = a.Hkv * a.rtiles;
 
-    // unused slots
-    for (int64_t b = blockIdx.x; b < a.B; b += W)
-        if (filled(a, b) == 0)
-            for (int64_t i = tid; i < (int64_t)a.Hq * D; i += NT)
-                ((T *)a.o)[b * a.Hq * D + i] = (T)0.f;
-
-    // this work-group's units [u0, u1) of all, and the sequence that u0 lies in
-    const int64_t per = (a.B + NT - 1) / NT, b0 = tid * per, b1 = std::min<int64_t>(a.B, b0 + per);
-    int64_t mine = 0;
-    for (int64_t b = b0; b < b1; ++b)
-        mine += (filled(a, b) + STEP - 1) / STEP;
-    int64_t incl = mine;
+    // this work-group's units [u0, u1) of all, and the sequence b that u0 lies in with the
+    // units before it.  Up to 64 sequences: every wave finds them from its own lanes.
+    int before = 0, total, found;
+    int64_t all, u0, u1;
+    const auto share = [&]() {
+        all = (int64_t)total * HR;
+        // (few units: one each, so that every work-group of an item has a piece of it)
+        u0 = all <= W ? std::min<int64_t>(all, blockIdx.x) : (all * blockIdx.x) >> a.logw;
+        u1 = all <= W ? std::min<int64_t>(all, blockIdx.x + 1) : (all * (blockIdx.x + 1)) >> a.logw;
+    };
+    if (a.B <= 64) {
+        const int mine = lane < a.B ? (filled(a, lane) + STEP - 1) / STEP : 0;
+        int incl = mine;
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xf, 0xf, false);
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xf, 0xf, false);
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xf, 0xf, false);
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xa, 0xf, false);   // row_bcast 15, 31
+        incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xc, 0xf, false);
+        total = __builtin_amdgcn_readlane(incl, 63);
+        share();
+        const uint64_t past = __ballot((int64_t)incl * HR > u0);
+        found = past ? __builtin_ctzll(past) : -1;
+        before = __builtin_amdgcn_readlane(incl - mine, past ? found : 0);
+    } else {
+        const int per = (int)((a.B + NT - 1) / NT), b0 = tid * per, b1 = std::min((int)a.B, b0 + per);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b)
+            mine += (filled(a, b) + STEP - 1) / STEP;
+        int incl = mine;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int64_t up = __shfl_up(incl, off, 64);
-        if (lane >= off)
-            incl += up;
-    }
-    if (lane == 63)
-        wsum[w] = incl;
-    if (tid == 0)
-        found[0] = -1;
-    __syncthreads();
-    int64_t total = 0, excl = incl - mine;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        if (i < w)
-            excl += wsum[i];
-        total += wsum[i];
-    }
-    const int64_t all = total * HR;
-    // (few units: one each, so that every work-group of an item has a piece of it)
-    const bool few = all <= W;
-    const int64_t u0 = few ? std::min<int64_t>(all, blockIdx.x) : (all * blockIdx.x) >> a.logw;
-    const int64_t u1 = few ? std::min<int64_t>(all, blockIdx.x + 1) : (all * (blockIdx.x + 1)) >> a.logw;
-    if (u0 >= excl * HR && u0 < (excl + mine) * HR) {
-        int64_t b = b0;
-        for (; b + 1 < b1; ++b) {
-            const int64_t n = (filled(a, b) + STEP - 1) / STEP;
-            if (u0 < (excl + n) * HR)
-                break;
-            excl += n;
+        for (int off = 1; off < 64; off <<= 1) {
+            const int up = __shfl_up(incl, off, 64);
+            if (lane >= off)
+                incl += up;
         }
-        found[0] = b;
-        found[1] = excl;
+        if (lane == 63)
+            wsum[w] = incl;
+        if (tid == 0)
+            where[0] = -1;
+        __syncthreads();
+        int excl = incl - mine;
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            if (i < w)
+                excl += wsum[i];
+            total += wsum[i];
+        }
+        total = uniform_int(total);
+        share();
+        if (u0 >= (int64_t)excl * HR && u0 < (int64_t)(excl + mine) * HR) {
+            int b = b0;
+            for (; b + 1 < b1; ++b) {
+                const int n = (filled(a, b) + STEP - 1) / STEP;
+                if (u0 < (int64_t)(excl + n) * HR)
+                    break;
+                excl += n;
+            }
+            where[0] = b;
+            where[1] = excl;
+        }
+        __syncthreads();
+        found = uniform_int(where[0]);
+        before = uniform_int(where[1]);
     }
-    __syncthreads();
     if (tid == 0)
         a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (u0 >= u1 || found[0] < 0)
-        return;
-    int64_t b = found[0], first = found[1] * HR;              // first unit of the sequence
-    int len = uniform_int(filled(a, b));
-    int units = (len + STEP - 1) / STEP;
-    if (u0 >= first + (int64_t)units * HR)                    // (lengths that change under the kernel end it)
-        return;
-    int item = (int)((u0 - first) / units);
-    int from = (int)((u0 - first) % units);
 
     unsigned char *own = smem + w * kWave;
     const unsigned lds0 = lds_addr(own);
+    // (lengths that change under the kernel end it early)
+    int64_t b = found;
+    int64_t first = (int64_t)before * HR;                     // first unit of the sequence
+    int len = u0 < u1 && found >= 0 ? uniform_int(filled(a, b)) : 0;
+    int units = (len + STEP - 1) / STEP;
+    int item = 0, from = 0;
+    if (units > 0) {
+        const unsigned at = (unsigned)(u0 - first);           // (below 2^31: checked on the host)
+        item = (int)(at / (unsigned)units);
+        from = (int)(at % (unsigned)units);
+        if (item >= HR)
+            units = 0;
+    }
 
-    for (int64_t u = u0; u < u1;) {
+    for (int64_t u = u0; u < u1 && units > 0;) {
         const int to = (int)std::min<int64_t>(units, from + (u1 - u));
         const int rt = item % a.rtiles, hk = item / a.rtiles;
         const int rows = std::min(16 * CB, a.grp - 16 * CB * rt);
         const int64_t h0 = (int64_t)hk * a.grp + 16 * CB * rt;
         const int kend = (int)std::min<int64_t>((int64_t)to * STEP, len);
 
+        wait_vmcnt<0>();                                      // (stores of the item before)
+        int t0 = from * STEP + KT * w;
+        Parts<Eng::kParts> cur = {}, nxt = {};
+        if (t0 < kend) {
+            cur = parts_of<Eng::kParts>(a, b, hk, t0, len);
+            Eng::issue(a, lds0, cur, Eng::whole(a, t0, len), lane);
+            if (t0 + STEP < kend)
+                nxt = parts_of<Eng::kParts>(a, b, hk, t0 + STEP, len);
+        }
         Eng eng;
         eng.begin(a, (const T *)a.q + b * a.q_stride + h0 * D, rows, lane);
         Sums<D, CB> st;
@@ -638,26 +767,21 @@ void paged_decode_kernel(PagedArgs a)
             for (int d = 0; d < D / 16; ++d)
                 st.acc[cb][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        wait_vmcnt<0>();                                      // (stores of the item before, too)
-        int t0 = from * STEP + KT * w;
-        Parts<Eng::kParts> cur = {}, nxt = {};
-        if (t0 < kend) {
-            cur = parts_of<Eng::kParts>(a, b, hk, t0, len);
-            Eng::issue(a, lds0, cur, lane);
-            if (t0 + STEP < kend)
-                nxt = parts_of<Eng::kParts>(a, b, hk, t0 + STEP, len);
-        }
         for (int n = 0; t0 < kend; ++n, t0 += STEP) {
             const unsigned slot = (unsigned)(n & 1) * Eng::kBuf;
             // the slot issued next was read by this wave before: its reads are done
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             const unsigned bad = cur.bad;
             if (t0 + STEP < kend) {
-                Eng::issue(a, lds0 + (Eng::kBuf - slot), nxt, lane);
+                const bool all_rows = Eng::whole(a, t0 + STEP, len);
+                Eng::issue(a, lds0 + (Eng::kBuf - slot), nxt, all_rows, lane);
                 cur = nxt;
                 if (t0 + 2 * STEP < kend)
                     nxt = parts_of<Eng::kParts>(a, b, hk, t0 + 2 * STEP, len);
-                wait_vmcnt<Eng::kLoads>();
+                if (all_rows)
+                    wait_vmcnt<Eng::kWhole>();
+                else
+                    wait_vmcnt<Eng::kLoads>();
             } else {
                 wait_vmcnt<0>();
             }
@@ -724,7 +848,7 @@ void paged_decode_kernel(PagedArgs a)
         if (!whole && from == 0 && tid == 0) {
             // units [first + item units, + units): the work-group of the last one
             const int64_t last = first + (int64_t)(item + 1) * units - 1;
-            const int64_t wl = few ? last : (((last + 1) << a.logw) - 1) / all;
+            const int64_t wl = all <= W ? last : (((last + 1) << a.logw) - 1) / all;
             a.rec[blockIdx.x] = make_int4((int)b, item, (int)wl, 0);
         }
         __syncthreads();                                      // (the LDS is written again)
@@ -744,10 +868,14 @@ void paged_decode_kernel(PagedArgs a)
             }
             len = b < a.B ? uniform_int(filled(a, b)) : 0;
             units = (len + STEP - 1) / STEP;
-            if (units == 0)
-                return;
         }
     }
+
+    // unused slots
+    for (int64_t i = blockIdx.x; i < a.B; i += W)
+        if (filled(a, i) == 0)
+            for (int64_t j = tid; j < (int64_t)a.Hq * D; j += NT)
+                ((T *)a.o)[i * a.Hq * D + j] = (T)0.f;
 }
 
 // Joins the pieces of the item that work-group blockIdx.x began and others ended.
