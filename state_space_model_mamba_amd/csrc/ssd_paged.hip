@@ -235,15 +235,16 @@ template <typename T_, int D, int CB> struct WideTile {
 
     V qf[CB][NP];
 
-    __device__ __forceinline__ void begin(const PagedArgs &a, const T *q, int rows, int lane)
+    // The queries, out of the LDS tiles at `at`.
+    __device__ __forceinline__ void begin(const PagedArgs &a, unsigned at, int lane)
     {
-        const int c = lane & 15, g = lane >> 4;
+        typedef LaneBase<T, D> LB;
+        const unsigned qr = LB::row16(lane & 15, lane >> 4);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                qf[cb][p] = *reinterpret_cast<const V *>(
-                    q + (int64_t)std::min(16 * cb + c, rows - 1) * D + (4 * p + g) * Piece<T>::E);
+                qf[cb][p] = LB::piece16(at + 16 * cb * TL::kPitch, qr, p);
                 if (a.neg)
                     qf[cb][p] = flip<T>(qf[cb][p]);
             }
@@ -403,8 +404,10 @@ template <typename T_, int D, int CB> struct CodeTile {
         return __builtin_bit_cast(bf16x8, v);
     }
 
-    __device__ __forceinline__ void begin(const PagedArgs &a, const T *q, int rows, int lane)
+    __device__ __forceinline__ void begin(const PagedArgs &a, unsigned at, int lane)
     {
+        typedef Tile<T, D> TL;
+        constexpr int kRaw = sizeof(T) == 2 ? 1 : 2;             // 16-byte pieces of eight queries
         const int c = lane & 15, g = lane >> 4;
         mask = 0x00780078u;
         sixteen = 0x41804180u;
@@ -412,25 +415,32 @@ template <typename T_, int D, int CB> struct CodeTile {
         hundred = 0x43004300u;                // 128
         zero = 0.f;
         asm volatile("" : "+s"(mask), "+v"(sixteen), "+s"(low), "+v"(hundred), "+v"(zero));
+        const unsigned sign = a.neg ? 0x80000000u : 0u;
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int s = 0; s < G; ++s) {
                 float sum = 0.f, first = 0.f;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const T *src = q + (int64_t)std::min(16 * cb + c, rows - 1) * D + 64 * s + 16 * g + 8 * p;
+                for (int p = 2 * s; p < 2 * s + 2; ++p) {
                     float x[8], y[8];
+                    u32x4 raw[kRaw];
+#pragma unroll
+                    for (int n = 0; n < kRaw; ++n)
+                        raw[n] = *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)(
+                            at + 16 * cb * TL::kPitch + TL::off(c, ((p / 2 * 8 + 2 * g + p % 2) * kRaw) + n));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        x[e] = a.neg ? -(float)src[e] : (float)src[e];
+                        const unsigned u = sizeof(T) == 4 ? raw[e / 4 % kRaw][e % 4]
+                                           : e & 1 ? raw[0][e / 2] & 0xffff0000u : raw[0][e / 2] << 16;
+                        x[e] = __uint_as_float(u ^ sign);
                         sum += x[e];
                     }
                     first += x[0] + x[4];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         y[e] = x[(e >> 1) + 4 * (e & 1)];
-                    terms_of<kQ>(y, qf[cb][2 * s + p]);
+                    terms_of<kQ>(y, qf[cb][p]);
                 }
                 qs[cb][s] = quad_sum(sum);
                 qb[cb][s] = kCentred ? 0.f : __builtin_fmaf(-112.f, quad_sum(first), -16.f * qs[cb][s]);
@@ -747,17 +757,42 @@ void paged_decode_kernel(PagedArgs a)
         const int64_t h0 = (int64_t)hk * a.grp + 16 * CB * rt;
         const int kend = (int)std::min<int64_t>((int64_t)to * STEP, len);
 
+        // The queries go through LDS as the tiles do (loads into registers would wait for the
+        // tiles in flight): they land in the second slot while the first tile is on its way, and
+        // the second tile follows them.
+        constexpr bool kBeside = 16 * CB * D * (int)sizeof(T) <= Eng::kBuf;
         wait_vmcnt<0>();                                      // (stores of the item before)
-        int t0 = from * STEP + KT * w;
-        Parts<Eng::kParts> cur = {}, nxt = {};
-        if (t0 < kend) {
-            cur = parts_of<Eng::kParts>(a, b, hk, t0, len);
-            Eng::issue(a, lds0, cur, Eng::whole(a, t0, len), lane);
-            if (t0 + STEP < kend)
-                nxt = parts_of<Eng::kParts>(a, b, hk, t0 + STEP, len);
-        }
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+            TileLoad<T, D, 16, 1>::issue(lds0 + (kBeside ? Eng::kBuf : 0) + 16 * cb * D * (int)sizeof(T),
+                                         (const T *)a.q + b * a.q_stride + h0 * D, D, std::min(16 * cb, rows - 1), rows,
+                                         0, lane);
         Eng eng;
-        eng.begin(a, (const T *)a.q + b * a.q_stride + h0 * D, rows, lane);
+        int t0 = from * STEP + KT * w;
+        Parts<Eng::kParts> nxt = {}, second = {};
+        if (t0 < kend)
+            nxt = parts_of<Eng::kParts>(a, b, hk, t0, len);
+        if (t0 + STEP < kend)
+            second = parts_of<Eng::kParts>(a, b, hk, t0 + STEP, len);
+        unsigned bad = nxt.bad, bad_next = second.bad;
+        if (kBeside && t0 < kend) {
+            const bool all_rows = Eng::whole(a, t0, len);
+            Eng::issue(a, lds0, nxt, all_rows, lane);
+            if (all_rows)
+                wait_vmcnt<Eng::kWhole>();
+            else
+                wait_vmcnt<Eng::kLoads>();
+        } else {
+            wait_vmcnt<0>();
+        }
+        eng.begin(a, lds0 + (kBeside ? Eng::kBuf : 0), lane);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (!kBeside && t0 < kend)
+            Eng::issue(a, lds0, nxt, Eng::whole(a, t0, len), lane);
+        if (t0 + STEP < kend)
+            Eng::issue(a, lds0 + Eng::kBuf, second, Eng::whole(a, t0 + STEP, len), lane);
+        if (t0 + 2 * STEP < kend)
+            nxt = parts_of<Eng::kParts>(a, b, hk, t0 + 2 * STEP, len);
         Sums<D, CB> st;
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
@@ -769,27 +804,26 @@ void paged_decode_kernel(PagedArgs a)
         }
         for (int n = 0; t0 < kend; ++n, t0 += STEP) {
             const unsigned slot = (unsigned)(n & 1) * Eng::kBuf;
-            // the slot issued next was read by this wave before: its reads are done
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            const unsigned bad = cur.bad;
-            if (t0 + STEP < kend) {
-                const bool all_rows = Eng::whole(a, t0 + STEP, len);
-                Eng::issue(a, lds0 + (Eng::kBuf - slot), nxt, all_rows, lane);
-                cur = nxt;
-                if (t0 + 2 * STEP < kend)
-                    nxt = parts_of<Eng::kParts>(a, b, hk, t0 + 2 * STEP, len);
-                if (all_rows)
-                    wait_vmcnt<Eng::kWhole>();
-                else
-                    wait_vmcnt<Eng::kLoads>();
-            } else {
+            // this tile has landed (the next may be in flight)
+            if (t0 + STEP >= kend)
                 wait_vmcnt<0>();
-            }
+            else if (Eng::whole(a, t0 + STEP, len))
+                wait_vmcnt<Eng::kWhole>();
+            else
+                wait_vmcnt<Eng::kLoads>();
             if (bad) {
                 Eng::clear(own + slot, bad, lane);
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             }
             eng.tile(lds0 + slot, t0 + KT > len || bad != 0, len - t0, bad, a.scale, lane, st);
+            bad = bad_next;
+            if (t0 + 2 * STEP < kend) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // the slot's reads are done
+                Eng::issue(a, lds0 + slot, nxt, Eng::whole(a, t0 + 2 * STEP, len), lane);
+                bad_next = nxt.bad;
+                if (t0 + 3 * STEP < kend)
+                    nxt = parts_of<Eng::kParts>(a, b, hk, t0 + 3 * STEP, len);
+            }
         }
         eng.finish(st);
 
@@ -818,7 +852,7 @@ void paged_decode_kernel(PagedArgs a)
                         f32x4{st.acc[cb][d][0] * f, st.acc[cb][d][1] * f, st.acc[cb][d][2] * f, st.acc[cb][d][3] * f};
         }
         __syncthreads();
-        const bool whole = from == 0 && to == units;
+        const bool complete = from == 0 && to == units;
         const int64_t slot = (2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0)) * 16 * CB;
         T *op = (T *)a.o + (b * a.Hq + h0) * D;
         for (int i = 4 * tid; i < rows * D; i += 4 * NT) {
@@ -834,7 +868,7 @@ void paged_decode_kernel(PagedArgs a)
 #pragma unroll
             for (int k = 0; k < NW; ++k)
                 lr += sl[k][row] * exp2_fast(sm[k][row] - mr);
-            if (whole) {
+            if (complete) {
                 const float inv = lr > 0.f ? 1.f / lr : 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -845,7 +879,7 @@ void paged_decode_kernel(PagedArgs a)
                     a.ml[slot + row] = make_float2(mr, lr);
             }
         }
-        if (!whole && from == 0 && tid == 0) {
+        if (!complete && from == 0 && tid == 0) {
             // units [first + item units, + units): the work-group of the last one
             const int64_t last = first + (int64_t)(item + 1) * units - 1;
             const int64_t wl = all <= W ? last : (((last + 1) << a.logw) - 1) / all;
@@ -998,7 +1032,7 @@ hipError_t launch_paged_decode(int bf16, int64_t B, int64_t Hq, int64_t Hkv, int
         typedef std::remove_pointer_t<decltype(e)> Eng;
         constexpr int kD = decltype(dim)::value, CB = decltype(cols)::value, kOcc = occupancy<Eng>();
         constexpr unsigned kSmem = Eng::kNW * 2u * Eng::kBuf;
-        static_assert(16 * CB * kD * 4 <= 2 * Eng::kBuf, "a wave's sums fit its tiles");
+        static_assert(16 * CB * kD * 4 <= 2 * Eng::kBuf, "a wave's sums, and its queries, fit its tiles");
         a.rtiles = (a.grp + 16 * CB - 1) / (16 * CB);
         a.logw = log_groups<Eng>();
         const unsigned W = 1u << a.logw;
