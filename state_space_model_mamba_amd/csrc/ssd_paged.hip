@@ -44,7 +44,9 @@ struct PagedArgs {
     void *o;
     float *part;                              // [2 W][rows][D] sums of the items' pieces
     float2 *ml;                               // [2 W][rows] (m, l)
-    int4 *rec;                                // [W] (sequence, item of it, last work-group, 0): to be joined
+    int4 *rec;                                // (sequence or -1, item of it, first and last work-group) of what is
+                                              // to be joined: [B HR] by item where that is no more than W
+    int by_item;                              // .. else [W] by the work-group that began it
     int64_t q_stride;
     int64_t B, cap;                           // sequences; rows that a table has pages for
     int Hq, Hkv, grp, rtiles, logw;
@@ -731,7 +733,7 @@ void paged_decode_kernel(PagedArgs a)
         found = uniform_int(where[0]);
         before = uniform_int(where[1]);
     }
-    if (tid == 0)
+    if (!a.by_item && tid == 0)
         a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
     unsigned char *own = smem + w * kWave;
@@ -879,11 +881,12 @@ void paged_decode_kernel(PagedArgs a)
                     a.ml[slot + row] = make_float2(mr, lr);
             }
         }
-        if (!complete && from == 0 && tid == 0) {
+        if (from == 0 && tid == 0 && (!complete || a.by_item)) {
             // units [first + item units, + units): the work-group of the last one
             const int64_t last = first + (int64_t)(item + 1) * units - 1;
             const int64_t wl = all <= W ? last : (((last + 1) << a.logw) - 1) / all;
-            a.rec[blockIdx.x] = make_int4((int)b, item, (int)wl, 0);
+            a.rec[a.by_item ? b * HR + item : blockIdx.x] =
+                make_int4(complete ? -1 : (int)b, item, (int)blockIdx.x, (int)wl);
         }
         __syncthreads();                                      // (the LDS is written again)
 
@@ -907,36 +910,35 @@ void paged_decode_kernel(PagedArgs a)
 
     // unused slots
     for (int64_t i = blockIdx.x; i < a.B; i += W)
-        if (filled(a, i) == 0)
+        if (filled(a, i) == 0) {
             for (int64_t j = tid; j < (int64_t)a.Hq * D; j += NT)
                 ((T *)a.o)[i * a.Hq * D + j] = (T)0.f;
+            if (a.by_item && tid < HR)
+                for (int j = tid; j < HR; j += NT)
+                    a.rec[i * HR + j] = make_int4(-1, 0, 0, 0);
+        }
 }
 
-// Joins the pieces of the item that work-group blockIdx.x began and others ended.
-template <typename T, int D, int CB> __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a)
+// Joins the pieces of an item that several work-groups have: one row per work-group, the
+// loads of up to 16 kT / D pieces in flight together.
+template <typename T, int D, int CB, int kT> __global__ __launch_bounds__(kT) void paged_join_kernel(PagedArgs a)
 {
-    constexpr int LPR = D / 4, G = 256 / LPR;
+    constexpr int LPR = D / 4, G = kT / LPR;
     __shared__ float4 sacc[G][LPR];
     __shared__ float sl[G];
     const int4 rec = a.rec[blockIdx.x];
     if (rec.x < 0)
         return;
     const int tid = threadIdx.x, gr = tid / LPR, d4 = tid % LPR;
-    const int w0 = blockIdx.x, n = rec.z - w0 + 1;
+    const int w0 = rec.z, n = rec.w - w0 + 1;
     const int rt = rec.y % a.rtiles, hk = rec.y / a.rtiles, row = blockIdx.y;
     if (row >= std::min(16 * CB, a.grp - 16 * CB * rt))
         return;
     const int64_t h = (int64_t)hk * a.grp + 16 * CB * rt + row;
     // piece 0: the second slot of w0; piece i: the first of w0 + i
     auto at = [&](int i) { return (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * 16 * CB + row; };
-    float mx = kNoMax;
-    for (int i = tid & 63; i < n; i += 64)
-        mx = fmaxf(mx, a.ml[at(i)].x);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1)
-        mx = fmaxf(mx, __shfl_xor(mx, off, 64));
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
+    float l = 0.f, m = kNoMax;
     constexpr int U = 4;
     for (int i0 = gr; i0 < n; i0 += G * U) {
         float2 ml[U];
@@ -947,18 +949,37 @@ template <typename T, int D, int CB> __global__ __launch_bounds__(256) void page
             ml[u] = a.ml[s];
             p[u] = *reinterpret_cast<const float4 *>(a.part + s * D + 4 * d4);
         }
+        float mn = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            mn = fmaxf(mn, ml[u].x);
+        const float old = exp2_fast(m - mn);
+        v.x *= old; v.y *= old; v.z *= old; v.w *= old;
+        l *= old;
+        m = mn;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float f = i0 + u * G < n ? exp2_fast(ml[u].x - mx) : 0.f;
+            const float f = i0 + u * G < n ? exp2_fast(ml[u].x - m) : 0.f;
             v.x += f * p[u].x; v.y += f * p[u].y; v.z += f * p[u].z; v.w += f * p[u].w;
             l += f * ml[u].y;
         }
     }
-    sacc[gr][d4] = v;
+    // to a common maximum over the groups that had pieces
+    __shared__ float smax[G];
     if (d4 == 0)
-        sl[gr] = l;
+        smax[gr] = m;
+    __syncthreads();
+    float mx = kNoMax;
+    for (int i = 0; i < G; ++i)
+        mx = fmaxf(mx, smax[i]);
+    const float f = exp2_fast(m - mx);
+    sacc[gr][d4] = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    if (d4 == 0)
+        sl[gr] = l * f;
     __syncthreads();
     if (tid < LPR) {
+        v = sacc[0][d4];
+        l = sl[0];
         for (int i = 1; i < G; ++i) {
             const float4 p = sacc[i][d4];
             v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
@@ -1039,6 +1060,8 @@ hipError_t launch_paged_decode(int bf16, int64_t B, int64_t Hq, int64_t Hkv, int
         a.part = static_cast<float *>(ws);
         a.ml = reinterpret_cast<float2 *>(a.part + (size_t)2 * W * 16 * CB * kD);
         a.rec = reinterpret_cast<int4 *>(a.ml + (size_t)2 * W * 16 * CB);
+        const int64_t items = B * Hkv * a.rtiles;
+        a.by_item = items <= W;
         static std::atomic<uint64_t> allowed{0};
         const auto kernel = &paged_decode_kernel<Eng, kD, CB, kOcc>;
         hipError_t err = allow_lds(reinterpret_cast<const void *>(kernel), (int)kSmem, allowed);
@@ -1047,8 +1070,14 @@ hipError_t launch_paged_decode(int bf16, int64_t B, int64_t Hq, int64_t Hkv, int
         kernel<<<dim3(W), dim3(64 * Eng::kNW), kSmem, s>>>(a);
         if ((err = hipGetLastError()) != hipSuccess || a.cap <= Eng::kNW * Eng::kKT)
             return err;                       // (items of one unit are never cut)
-        paged_join_kernel<typename Eng::T, kD, CB>
-            <<<dim3(W, (unsigned)std::min(a.grp, 16 * CB)), dim3(256), 0, s>>>(a);
+        // (few items have many pieces each; starting many large work-groups takes longer than
+        // they save: 6 us for 512 items of 4 heads)
+        const int64_t heads = std::min(a.grp, 16 * CB), groups = (a.by_item ? items : W) * heads;
+        const dim3 grid((unsigned)(a.by_item ? items : W), (unsigned)heads);
+        if (groups <= 256)
+            paged_join_kernel<typename Eng::T, kD, CB, 1024><<<grid, dim3(1024), 0, s>>>(a);
+        else
+            paged_join_kernel<typename Eng::T, kD, CB, 256><<<grid, dim3(256), 0, s>>>(a);
         return hipGetLastError();
     });
 }
