@@ -233,6 +233,8 @@ template <typename T_, int D, int CB> struct WideTile {
     static constexpr int kKT = kHalf ? 32 : 16, kParts = kKT / 16, NP = TL::kPitch / 64;
     static constexpr int kTileBytes = kKT * TL::kPitch, kBuf = 2 * kTileBytes;
     static constexpr int kNW = 2 * kBuf * 4 <= 128 * 1024 ? 4 : 2;
+    static constexpr int kMost = 4;
+    static constexpr bool kTurns = false;
     static constexpr int kLoads = 2 * kParts * TileLoad<T, D, 16, 1>::kPer;
 
     V qf[CB][NP];
@@ -358,15 +360,26 @@ template <typename T_, int D, int CB> struct WideTile {
 // nearly cancel, are then a few times smaller (3.6e-6 off against 64 bits otherwise), for
 // 2.5 instructions a value instead of one.
 //
-// Tiles of 64 keys: [64][D / 2] bytes of keys, the same of values, then the scales
-// [part][group][16 keys] of both.  Rows are not padded; their 16-byte chunks are permuted
-// by an XOR with swz(row), so that reads of 16 rows cover the banks evenly.
+// Tiles of 64 keys, or 32 where one is 5 KB and more (shorter chains in front of a wave's
+// first result and fewer registers; 131000 keys of 128: 43 -> 40 us): [keys][D / 2] bytes
+// of keys, the same of values, then the scales [part][group][16 keys] of both.  Rows are not
+// padded; their 16-byte chunks are permuted by an XOR with swz(row), so that reads of 16
+// rows cover the banks evenly.
 template <typename T_, int D, int CB> struct CodeTile {
     typedef T_ T;
-    static constexpr int kKT = 64, kParts = 4, G = D / 64;
-    static constexpr int kRow = D / 2, kPart = 16 * kRow, kSide = 4 * kPart, kScales = 4 * 64 * G;
+    static constexpr bool kShort = D > 64 && CB == 1;
+    static constexpr int kKT = kShort ? 32 : 64, kParts = kKT / 16, G = D / 64;
+    static constexpr int kRow = D / 2, kPart = 16 * kRow, kSide = kParts * kPart, kScales = kKT * 4 * G;
     static constexpr int kBuf = 2 * kSide + 2 * kScales;
     static constexpr int kNW = 4;
+    // Work-groups of a CU: 256 registers a wave, or 512 where two blocks of columns of wide heads
+    // need them (with fewer the kernels spill: 8192 keys of 60 heads over 3 of 128 take 77 us
+    // instead of 64; 32 heads of 64 over one 55 instead of 25 at 128 registers).
+    static constexpr int kMost = CB == 2 && D > 64 ? 1 : 2;
+    // Work-groups of a CU raise their priority in every other tile, in turn: the older one would
+    // otherwise finish first and leave the other alone (2 - 5% of the time; the reverse with two
+    // blocks of columns).
+    static constexpr bool kTurns = CB == 1;
     static constexpr int kPer = kPart > 1024 ? kPart / 1024 : 1;          // loads of a part's codes
     static constexpr int kLoads = kParts * (2 * kPer + 2);
     static constexpr int kQ = sizeof(T) == 2 ? 1 : 3, kP = sizeof(T) == 2 ? 2 : 3;
@@ -468,10 +481,10 @@ template <typename T_, int D, int CB> struct CodeTile {
     }
 
     // A tile's loads: kWhole where its 64 rows exist and lie in one page, else part by part.
-    static constexpr int kWhole = 2 * (kSide / 1024) + 2 * G;
+    static constexpr int kWhole = 2 * (kSide / 1024) + 2 * (kScales / 256);
     static __device__ __forceinline__ bool whole(const PagedArgs &a, int t0, int len)
     {
-        return a.c.shift >= 6 && t0 + kKT <= len;
+        return kKT >> a.c.shift <= 1 && t0 + kKT <= len;
     }
 
     static __device__ __forceinline__ void issue(const PagedArgs &a, unsigned dst, const Parts<kParts> &p, bool all,
@@ -492,7 +505,7 @@ template <typename T_, int D, int CB> struct CodeTile {
                 load16<64>(dst + kSide + n * 1024, vp, off, lane);
             }
 #pragma unroll
-            for (int n = 0; n < G; ++n) {
+            for (int n = 0; n < kScales / 256; ++n) {
                 // dword [part][group][key] <- [key][group]
                 const int x = n * 64 + lane, key = 16 * (x / (16 * G)) + x % 16, grp = x % (16 * G) / 16;
                 const unsigned off = (unsigned)(key * G + grp) * 4u;
@@ -575,12 +588,14 @@ template <typename T_, int D, int CB> struct CodeTile {
                     over[cb][s] *= al;
             }
         });
-        // within 16 lanes, lane r addresses the row of key 16 (r / 4) + 4 g + r % 4
-        const int r = 16 * (cl >> 2) + 4 * g + (cl & 3);
-        const unsigned vr = opaque((unsigned)(r * kRow + (swz(r) << 4)));
+        // within 16 lanes, lane r addresses the row of key 16 (r / 4) + 4 g + r % 4 (of tiles of 32
+        // keys: r % 8, and the upper eight lanes the next 16 columns)
+        constexpr bool kTall = kKT == 64;
+        const int r = 16 * (kTall ? cl >> 2 : cl >> 2 & 1) + 4 * g + (cl & 3);
+        const unsigned vr = opaque((unsigned)(r * kRow + (swz(r) << 4) + (kTall ? 0 : (cl >> 3) * 8)));
 #pragma unroll
         for (int s = 0; s < G; ++s) {
-            bf16x8 pt[CB][2][kP];
+            bf16x8 pt[CB][kParts / 2][kP];
 #pragma unroll
             for (int kb = 0; kb < kParts; kb += 2) {
                 const u32x4 w0 = scales(buf + 2 * kSide + kScales + (unsigned)(kb * 64 * G + s * 64 + 16 * g));
@@ -608,7 +623,7 @@ template <typename T_, int D, int CB> struct CodeTile {
                 }
             }
 #pragma unroll
-            for (int d = 4 * s; d < 4 * s + 4; ++d) {
+            for (int d = 4 * s; d < 4 * s + 4; d += kTall ? 1 : 2) {
                 const v2i w = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
                     (lds_v2i *)(uintptr_t)(buf + kSide + (vr ^ (unsigned)((d >> 1) << 4)) + (d & 1) * 8));
 #pragma unroll
@@ -617,8 +632,10 @@ template <typename T_, int D, int CB> struct CodeTile {
 #pragma unroll
                     for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-                        for (int n = 0; n < kP; ++n)
-                            st.acc[cb][d] = mma16(v, pt[cb][x][n], st.acc[cb][d]);
+                        for (int n = 0; n < kP; ++n) {
+                            f32x4 &acc = st.acc[cb][kTall ? d : d + x];
+                            acc = mma16(v, pt[cb][kTall ? x : 0][n], acc);
+                        }
                 }
             }
         }
@@ -653,7 +670,7 @@ __device__ __forceinline__ int filled(const PagedArgs &a, int64_t b)
 }
 
 template <typename Eng, int D, int CB, int kOcc>
-__global__ __launch_bounds__(64 * Eng::kNW, kOcc * Eng::kNW / 4 > 0 ? kOcc * Eng::kNW / 4 : 1)
+__global__ __launch_bounds__((64 * Eng::kNW), (kOcc * Eng::kNW / 4 > 0 ? kOcc * Eng::kNW / 4 : 1))
 void paged_decode_kernel(PagedArgs a)
 {
     typedef typename Eng::T T;
@@ -817,6 +834,11 @@ void paged_decode_kernel(PagedArgs a)
                 Eng::clear(own + slot, bad, lane);
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             }
+            if constexpr (Eng::kTurns)                        // (two work-groups to a CU: W / 2 apart)
+                if (((unsigned)n + (blockIdx.x >> (a.logw - 1))) & 1u)
+                    __builtin_amdgcn_s_setprio(1);
+                else
+                    __builtin_amdgcn_s_setprio(0);
             eng.tile(lds0 + slot, t0 + KT > len || bad != 0, len - t0, bad, a.scale, lane, st);
             bad = bad_next;
             if (t0 + 2 * STEP < kend) {
@@ -994,10 +1016,10 @@ template <typename T, int D, int CB, int kT> __global__ __launch_bounds__(kT) vo
     }
 }
 
-// Work-groups that fit a CU by their LDS, and as many times 256 CUs of them.
+// Work-groups of a CU: as many as fit by their LDS and registers; and 256 CUs of them.
 template <typename Eng> constexpr int occupancy()
 {
-    const int n = 160 * 1024 / (Eng::kNW * 2 * Eng::kBuf + 1024);
+    const int n = std::min(Eng::kMost, 160 * 1024 / (Eng::kNW * 2 * Eng::kBuf + 2048));
     return n >= 4 ? 4 : n >= 2 ? 2 : 1;
 }
 template <typename Eng> constexpr int log_groups()
