@@ -124,12 +124,13 @@ enum { kNoPages, kPages, kPages4 };
 // lanes to a head, 8 values to a lane: for halves paired over R / 2 the four at 4 j and
 // the four at R / 2 + 4 j, so that a lane has both of a pair and nothing moves between
 // lanes but the sum of squares; otherwise 8 j .. 8 j + 7.  The angles' sines and cosines
-// are formed once per token and wave.
+// are formed once per token and wave, one or two angles to a lane.
 template <typename T, int D, int kKind>
 __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
 {
     constexpr int LPH = D / 8, HW = 64 / LPH; // lanes of a head, heads at once
-    constexpr int U = 2;                      // head groups whose loads are in flight together
+    constexpr int U = 4;                      // head groups of a round; the next round's loads are in flight
+    constexpr int NA = D > 128 ? D / 128 : 1; // angles a lane forms
     typedef Four<T> F;
     __shared__ float ex[kKind == kPages4 ? 4 : 1][kKind == kPages4 ? 512 : 1];
 
@@ -150,10 +151,11 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
         wq[e] = qw ? qw[d] : 1.f;
         wk[e] = kw ? kw[d] : 1.f;
     }
-    double freq[4];
+    // angles i = lane + 64 n, each formed by one lane
+    double freq[NA];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        freq[e] = turned ? (double)a->turn.inv_freq[4 * j + e] * 0.15915494309189535 : 0.0;
+    for (int n = 0; n < NA; ++n)
+        freq[n] = lane + 64 * n < rot / 2 ? (double)a->turn.inv_freq[lane + 64 * n] * 0.15915494309189535 : 0.0;
     const float eps = a->turn.eps;
 
     const int64_t nunit = a->ntok * a->chunks;
@@ -164,25 +166,8 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
         const int64_t t = a->tab.tok[0] + rel;
         const T *qp = (const T *)a->r.q + t * a->r.q_stride, *kp = (const T *)a->r.k + t * a->r.k_stride;
         const T *vp = (const T *)a->r.v + t * a->r.v_stride;
-        // where the token goes
-        int64_t pos = 0, line = 0;
-        bool stored = false;
-        if constexpr (kKind != kNoPages) {
-            const int si = a->one ? 0 : seq_of(a->tab, (int)rel, lane);
-            const int64_t b = a->one ? a->seq0 + rel : a->seq0 + si;
-            const int64_t row = (int64_t)a->lengths[b] + (a->one ? 0 : rel - a->tab.pre[si]);
-            const int page = a->lengths[b] < 0 ? -1 : page_of(*(const PagedCache *)&a->c, b, row);
-            stored = page >= 0;
-            line = ((int64_t)std::max(page, 0) * Hkv << a->c.shift) + (row & ((1 << a->c.shift) - 1));
-            pos = row;
-        }
-        if (a->turn.positions)
-            pos = a->turn.positions[t];
-
-        bool have = false;
-        float cs[4], sn[4];
-        for (int hb = h0; hb < h1; hb += U * HW) {
-            typename F::V raw[U][2];
+        typename F::V raw[U][2];
+        const auto fetch = [&](int hb) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int h = hb + u * HW + hl;
@@ -194,15 +179,54 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
                     raw[u][1] = *reinterpret_cast<const typename F::V *>(src + (isv ? 8 * j + 4 : ob));
                 }
             }
-            if (!have) {                      // (after the first loads are on their way)
-                have = true;
+        };
+        fetch(h0);                            // (ahead of the look-ups, which wait for one another)
+        __builtin_amdgcn_sched_barrier(0);
+        // where the token goes
+        int64_t pos = 0, line = 0;
+        bool stored = false;
+        if constexpr (kKind != kNoPages) {
+            const int si = a->one ? 0 : seq_of(a->tab, (int)rel, lane);
+            const int64_t b = a->one ? a->seq0 + rel : a->seq0 + si;
+            const int length = a->lengths[b];
+            const int64_t row = (int64_t)length + (a->one ? 0 : rel - a->tab.pre[si]);
+            const int page = length < 0 ? -1 : page_of(*(const PagedCache *)&a->c, b, row);
+            stored = page >= 0;
+            line = ((int64_t)std::max(page, 0) * Hkv << a->c.shift) + (row & ((1 << a->c.shift) - 1));
+            pos = row;
+        }
+        if (a->turn.positions)
+            pos = a->turn.positions[t];
+        float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {};
+        if (rot > 0) {
+            float c1[NA], s1[NA];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const double turns = (double)pos * freq[e];
-                    const float half = (float)(2.0 * (turns - __builtin_rint(turns)));
-                    sincospif(half, &sn[e], &cs[e]);
+            for (int n = 0; n < NA; ++n) {
+                const double turns = (double)pos * freq[n];
+                sincospif((float)(2.0 * (turns - __builtin_rint(turns))), &s1[n], &c1[n]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int from = (4 * j + e) & 63;
+                cs[e] = __shfl(c1[0], from, 64);
+                sn[e] = __shfl(s1[0], from, 64);
+                if constexpr (NA == 2) {
+                    const float c2 = __shfl(c1[1], from, 64), s2 = __shfl(s1[1], from, 64);
+                    cs[e] = j < 16 ? cs[e] : c2;
+                    sn[e] = j < 16 ? sn[e] : s2;
                 }
             }
+        }
+
+        for (int hb = h0; hb < h1; hb += U * HW) {
+            typename F::V now[U][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                now[u][0] = raw[u][0];
+                now[u][1] = raw[u][1];
+            }
+            if (hb + U * HW < h1)
+                fetch(hb + U * HW);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (hb + u * HW >= h1)
@@ -210,8 +234,8 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
                 const int h = hb + u * HW + hl;
                 const bool live = h < h1, isq = h < Hq, isv = h >= Hq + Hkv;
                 float x[8];
-                F::open(raw[u][0], x);
-                F::open(raw[u][1], x + 4);
+                F::open(now[u][0], x);
+                F::open(now[u][1], x + 4);
                 if (live ? (isq ? qw : isv ? nullptr : kw) != nullptr : false) {
                     float ss = 0.f;
 #pragma unroll
