@@ -791,23 +791,38 @@ class SsdQkRope(ctypes.Structure):
 
 def _rope(dev, T, D, positions, inv_freq, q_weight, k_weight, eps, interleaved):
     f32 = torch.float32
+    rot, fp, qp, kp, pp = 0, None, None, None, None
     if inv_freq is not None:
+        _need("inv_freq", inv_freq, dev, f32)
         if inv_freq.dim() != 1:
             raise ValueError(f"inv_freq must be [rot_dim / 2], got shape {tuple(inv_freq.shape)}")
-        _need("inv_freq", inv_freq, dev, f32)
-    _need("q_weight", q_weight, dev, f32, (D,), optional=True)
-    _need("k_weight", k_weight, dev, f32, (D,), optional=True)
-    _need("positions", positions, dev, torch.int32, (T,), optional=True)
-    return SsdQkRope(_ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-                     0 if inv_freq is None else 2 * inv_freq.shape[0], int(interleaved), eps, 0)
+        rot, fp = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+    if q_weight is not None:
+        _need("q_weight", q_weight, dev, f32, (D,))
+        qp = q_weight.data_ptr()
+    if k_weight is not None:
+        _need("k_weight", k_weight, dev, f32, (D,))
+        kp = k_weight.data_ptr()
+    if positions is not None:
+        _need("positions", positions, dev, torch.int32, (T,))
+        pp = positions.data_ptr()
+    return SsdQkRope(fp, qp, kp, pp, rot, int(interleaved), eps, 0)
+
+
+def _out_rows(name, t, like, dev, stream):
+    """An output of rows like `like`, given or new: (tensor, distance between its rows)."""
+    if t is not None:
+        return t, _row_stride(name, t, dev, like.dtype, like.shape)
+    with _on(stream):
+        return _empty_rows(like), 0
 
 
 def _pages(dev, k_pages, v_pages, block_table, k_scales, v_scales, io, D=None, Hkv=None, B=None):
     """Checks a paged cache of input type `io`; returns (page_format, num_pages, Hkv, page_size,
     D, B, max_pages)."""
-    for name, t in (("k_pages", k_pages), ("block_table", block_table)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if not (isinstance(k_pages, torch.Tensor) and isinstance(block_table, torch.Tensor)):
+        raise TypeError("k_pages and block_table must be torch.Tensors, got "
+                        f"{type(k_pages).__name__} and {type(block_table).__name__}")
     if k_pages.dim() != 4 or block_table.dim() != 2:
         raise ValueError("pages must be [num_pages, Hkv, page_size, D] (D / 2 bytes in 4 bits) and "
                          "block_table [B, max_pages]")
@@ -845,15 +860,12 @@ def ssd_attn_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_
     io = _io_dtype(q, "q/k")
     rope = _rope(dev, T, D, positions, inv_freq, q_weight, k_weight, eps, interleaved)
     with _guard(dev):
-        if q_out is None or k_out is None:
-            with _on(stream):
-                q_out = _empty_rows(q) if q_out is None else q_out
-                k_out = _empty_rows(k) if k_out is None else k_out
-        d = SsdPagedDims(0, T, Hq, Hkv, D, 0, 0, 0, qs, ks, 0, _row_stride("q_out", q_out, dev, q.dtype, q.shape),
-                         _row_stride("k_out", k_out, dev, q.dtype, k.shape), 1.0, io, 0, 0)
+        q_out, qos = _out_rows("q_out", q_out, q, dev, stream)
+        k_out, kos = _out_rows("k_out", k_out, k, dev, stream)
+        d = SsdPagedDims(0, T, Hq, Hkv, D, 0, 0, 0, qs, ks, 0, qos, kos, 1.0, io, 0, 0)
         _check("ssd_attn_qk_norm_rope", load().ssd_attn_qk_norm_rope(
-            ctypes.byref(d), ctypes.byref(rope), _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
-            _stream(stream, dev)))
+            ctypes.byref(d), ctypes.byref(rope), q.data_ptr(), k.data_ptr(), q_out.data_ptr(),
+            k_out.data_ptr(), _stream(stream, dev)))
     return q_out, k_out
 
 
@@ -890,15 +902,14 @@ def ssd_attn_paged_append(q, k, v, k_pages, v_pages, block_table, lengths, cu_se
         raise ValueError("q_out needs q")
     kos = 0 if k_out is None else _row_stride("k_out", k_out, dev, dt, k.shape)
     with _guard(dev):
-        if q is not None and q_out is None:
-            with _on(stream):
-                q_out = _empty_rows(q)
-        qos = 0 if q is None else _row_stride("q_out", q_out, dev, dt, q.shape)
+        qos = 0
+        if q is not None:
+            q_out, qos = _out_rows("q_out", q_out, q, dev, stream)
         d = SsdPagedDims(B, T, Hq, Hkv, D, n, p, m, qs, ks, vs, qos, kos, 1.0, io, fmt, 0)
         _check("ssd_attn_paged_append", load().ssd_attn_paged_append(
-            ctypes.byref(d), ctypes.byref(rope), cup, _ptr(q), _ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages),
-            _ptr(k_scales), _ptr(v_scales), _ptr(block_table), _ptr(lengths), _ptr(q_out), _ptr(k_out),
-            _stream(stream, dev)))
+            ctypes.byref(d), ctypes.byref(rope), cup, _ptr(q), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(),
+            v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), block_table.data_ptr(), lengths.data_ptr(),
+            _ptr(q_out), _ptr(k_out), _stream(stream, dev)))
     return q_out
 
 
@@ -979,6 +990,7 @@ def ssd_attn_paged_decode_step(q, k_pages, v_pages, block_table, lengths, k_scal
                     workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check("ssd_attn_paged_decode_step", lib.ssd_attn_paged_decode_step(
-            ctypes.byref(d), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
-            _ptr(block_table), _ptr(lengths), _ptr(o), _ptr(workspace), ws_bytes, _stream(stream, dev)))
+            ctypes.byref(d), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales),
+            block_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), _ptr(workspace), ws_bytes,
+            _stream(stream, dev)))
     return o

@@ -373,9 +373,10 @@ template <typename T_, int D, int CB> struct CodeTile {
     static constexpr int kBuf = 2 * kSide + 2 * kScales;
     static constexpr int kNW = 4;
     // Work-groups of a CU: 256 registers a wave, or 512 where two blocks of columns of wide heads
-    // need them (with fewer the kernels spill: 8192 keys of 60 heads over 3 of 128 take 77 us
-    // instead of 64; 32 heads of 64 over one 55 instead of 25 at 128 registers).
-    static constexpr int kMost = CB == 2 && D > 64 ? 1 : 2;
+    // or fp32 queries of 256 need them.  With fewer the kernels spill: 32 sequences of 8000, 60
+    // heads over 3 of 128, take 77 us instead of 64; 16 of them, 16 heads over 4 of 256 in fp32,
+    // 91 instead of 78; 64 of 100 - 8190, 32 heads over one of 64, 55 instead of 25 at 128.
+    static constexpr int kMost = (CB == 2 && D > 64) || (D == 256 && sizeof(T) == 4) ? 1 : 2;
     // Work-groups of a CU raise their priority in every other tile, in turn: the older one would
     // otherwise finish first and leave the other alone (2 - 5% of the time; the reverse with two
     // blocks of columns).
@@ -686,7 +687,7 @@ void paged_decode_kernel(PagedArgs a)
 
     // this work-group's units [u0, u1) of all, and the sequence b that u0 lies in with the
     // units before it.  Up to 64 sequences: every wave finds them from its own lanes.
-    int before = 0, total, found;
+    int before = 0, total, found, mylen = 0;
     int64_t all, u0, u1;
     const auto share = [&]() {
         all = (int64_t)total * HR;
@@ -695,7 +696,8 @@ void paged_decode_kernel(PagedArgs a)
         u1 = all <= W ? std::min<int64_t>(all, blockIdx.x + 1) : (all * (blockIdx.x + 1)) >> a.logw;
     };
     if (a.B <= 64) {
-        const int mine = lane < a.B ? (filled(a, lane) + STEP - 1) / STEP : 0;
+        mylen = lane < a.B ? filled(a, lane) : 0;
+        const int mine = (mylen + STEP - 1) / STEP;
         int incl = mine;
         incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
         incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xf, 0xf, false);
@@ -758,7 +760,10 @@ void paged_decode_kernel(PagedArgs a)
     // (lengths that change under the kernel end it early)
     int64_t b = found;
     int64_t first = (int64_t)before * HR;                     // first unit of the sequence
-    int len = u0 < u1 && found >= 0 ? uniform_int(filled(a, b)) : 0;
+    const auto len_of = [&](int64_t i) {
+        return a.B <= 64 ? __builtin_amdgcn_readlane(mylen, (int)i) : uniform_int(filled(a, i));
+    };
+    int len = u0 < u1 && found >= 0 ? len_of(b) : 0;
     int units = (len + STEP - 1) / STEP;
     int item = 0, from = 0;
     if (units > 0) {
@@ -919,13 +924,14 @@ void paged_decode_kernel(PagedArgs a)
             item = 0;
             first += (int64_t)HR * units;
             for (b += 1; b < a.B; b += 64) {
-                const uint64_t some = __ballot(b + lane < a.B && filled(a, std::min(a.B - 1, b + lane)) > 0);
+                const uint64_t some = a.B <= 64 ? __ballot(mylen > 0) >> b
+                                                : __ballot(b + lane < a.B && filled(a, std::min(a.B - 1, b + lane)) > 0);
                 if (some) {
                     b += __builtin_ctzll(some);
                     break;
                 }
             }
-            len = b < a.B ? uniform_int(filled(a, b)) : 0;
+            len = b < a.B ? len_of(b) : 0;
             units = (len + STEP - 1) / STEP;
         }
     }

@@ -213,9 +213,9 @@ def test_refusals():
             (ValueError, "v_pages has shape", lambda: step(q[:1], kp, vp[:, :, :8].contiguous(), tab, n)),
             (ValueError, "q_out needs q", lambda: app(None, k[:1], v[:1], kp, vp, tab, n, q_out=q[:1])),
             (ValueError, "block_table has shape", lambda: app(q, k, v, kp, vp, tab, n)),
-            (ssd.SsdError, "", lambda: app(q, k, v, kp, vp, tab, n, cu_seqlens=[0, 3])),
-            (ssd.SsdError, "", lambda: ssd.ssd_attn_paged_gather(kp, vp, tab, [0, L.width * 16 + 1])),
-            (ssd.SsdError, "", lambda: ssd.ssd_attn_paged_gather(kp, vp, tab, [0, 4], starts=[-1])),
+            (ssd.SsdError, "failed", lambda: app(q, k, v, kp, vp, tab, n, cu_seqlens=[0, 3])),
+            (ssd.SsdError, "failed", lambda: ssd.ssd_attn_paged_gather(kp, vp, tab, [0, L.width * 16 + 1])),
+            (ssd.SsdError, "failed", lambda: ssd.ssd_attn_paged_gather(kp, vp, tab, [0, 4], starts=[-1])),
             (TypeError, "rows of", lambda: ssd.ssd_attn_paged_gather(kp, vp, tab, [0, 4], dtype=torch.float32)),
             (TypeError, "float32, got", lambda: ssd.ssd_attn_paged_gather(k4, v4, tab, [0, 4], dtype=torch.half, **s4))):
         with pytest.raises(err, match=match):

@@ -61,6 +61,27 @@ def test_many_sequences(io, bits):
 
 
 @pytest.mark.parametrize("io,bits", FORMATS)
+def test_more_items_than_work_groups(io, bits):
+    """600 items of 2 key heads, a few of them cut between work-groups."""
+    rng = np.random.default_rng(23)
+    rows = [int(n) for n in rng.integers(1, 30, 300)]
+    rows[7], rows[8], rows[150], rows[299] = 1500, 0, 2100, 900
+    c = Cache(24, io, bits, rows, 2, 64, 32)
+    lengths = [n - 1 for n in rows]
+    q = queries(25, 300, 6, 64, io)
+    check_decode(c, step(c, q[0], lengths), q[1], lengths, 0.125, "items")
+
+
+@pytest.mark.parametrize("io,bits", FORMATS)
+@pytest.mark.parametrize("D", [128, 256])
+def test_one_long_sequence_of_many_heads(io, bits, D):
+    """Two tiles of query heads (32 and 8) of a key head, cut between work-groups."""
+    c = Cache(26, io, bits, [2500, 40], 1, D, 64)
+    q = queries(27, 2, 40, D, io)
+    check_decode(c, step(c, q[0], [2499, 39]), q[1], [2499, 39], D ** -0.5, "heads")
+
+
+@pytest.mark.parametrize("io,bits", FORMATS)
 def test_entries_that_are_no_page(io, bits):
     """Rows on no page are left out, at the start, in the middle and at the end of a table; a
     sequence with no page at all gets 0.  (Page 0, which stands in for them, is NaN.)"""

@@ -311,3 +311,41 @@ def test_gather_of_no_pages_and_of_many_sequences(bits):
         within(got, want, U["bf16"] * 1.01 * np.abs(want), x)
     k, v = ssd.ssd_attn_paged_gather(pos[0], pos[1], dev(c.table), [0] * 301, **kw)
     assert k.shape == v.shape == (0, 1, 64)
+
+
+# --------------------------------------------------------------------------
+# More work than one pass of the largest launch, arrays past 2^31 elements
+# --------------------------------------------------------------------------
+def test_norm_rope_of_millions_of_tokens():
+    T = 4_200_000
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(T, 1, 64, generator=gen, device="cuda", dtype=torch.bfloat16)
+    k = torch.randn(T, 1, 64, generator=gen, device="cuda", dtype=torch.bfloat16)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    f = dev(freqs(8))
+    qo, ko = ssd.ssd_attn_qk_norm_rope(q, k, pos, f)
+    a = pos.double()[:, None] * f.double()
+    c, s = torch.cos(a), torch.sin(a)
+    for x, y in ((q, qo), (k, ko)):
+        assert torch.equal(x[:, 0, 8:], y[:, 0, 8:])
+        u, v = x[:, 0, :4].double(), x[:, 0, 4:8].double()
+        for want, got in ((u * c - v * s, y[:, 0, :4]), (v * c + u * s, y[:, 0, 4:8])):
+            # (24 F of the two values and one rounding, as turn_bound)
+            tol = (24 * F + pos.double()[:, None] * 2.0 ** -51) * (u.abs() + v.abs()) * 1.01 + U["bf16"] * want.abs() + 1e-30
+            assert ((got.double() - want).abs() <= tol).all()
+
+
+def test_gather_past_2_to_31_elements():
+    rows, Hkv, D, page = 540_000, 64, 64, 1024
+    n = -(-rows // page)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    kp = torch.randint(0, 1 << 15, (n, Hkv, page, D), generator=gen, device="cuda", dtype=torch.int16).view(torch.bfloat16)
+    vp = kp.flip(0).contiguous()
+    table = torch.randperm(n, generator=gen, device="cuda").int()[None]
+    k, v = ssd.ssd_attn_paged_gather(kp, vp, table, [0, rows])
+    assert k.numel() > 2 ** 31
+    for got, p in ((k, kp), (v, vp)):
+        for i in range(0, n, 16):
+            want = p[table[0, i:i + 16].long()].transpose(1, 2).reshape(-1, Hkv, D)
+            at = slice(i * page, min(rows, (i + 16) * page))
+            assert torch.equal(got[at].view(torch.int16), want[:at.stop - at.start].view(torch.int16))
