@@ -136,8 +136,8 @@ def load(path: str | None = None):
             ("ssd_attn_decode_workspace_size", [att, i64p]),
             ("ssd_attn_decode_step", [att] + [vp] * 8 + [sz, vp]),
             ("ssd_attn_qk_norm_rope", [pag, rope] + [vp] * 5),
-            ("ssd_attn_paged_append", [pag, rope, cu] + [vp] * 12),
-            ("ssd_attn_paged_gather", [pag, cu, cu] + [vp] * 8),
+            ("ssd_attn_paged_append", [pag, rope] + [vp] * 13),
+            ("ssd_attn_paged_gather", [pag] + [vp] * 10),
             ("ssd_attn_paged_decode_workspace_size", [pag, i64p]),
             ("ssd_attn_paged_decode_step", [pag] + [vp] * 9 + [sz, vp])):
         getattr(lib, name).argtypes = args
@@ -169,11 +169,14 @@ def _stream(stream, di):
     return _current_raw_stream(di) if stream is None else stream.cuda_stream
 
 
+_HERE = contextlib.nullcontext()   # (holds nothing: one for all calls)
+
+
 def _on(stream):
     """Allocation context of a call: the caller's stream when one is given (the
     current stream is the allocator's default otherwise), so that blocks
     allocated for the call are not handed to other work while its kernels run."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _io_dtype(t, names="x/B/C"):
@@ -525,9 +528,13 @@ def _offsets(name, x, n=None):
     return a, p
 
 
+# (the plain query: the tensors at hand have initialised the device)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _guard(di):
     """The tensors' device as the current one for a call's launches."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == di else torch.cuda.device(di)
+    return _HERE if _current_device() == di else torch.cuda.device(di)
 
 
 def _row_stride(name, t, di, dtype, shape):
@@ -813,8 +820,19 @@ def _out_rows(name, t, like, dev, stream):
     """An output of rows like `like`, given or new: (tensor, distance between its rows)."""
     if t is not None:
         return t, _row_stride(name, t, dev, like.dtype, like.shape)
+    if stream is None:
+        return _empty_rows(like), 0
     with _on(stream):
         return _empty_rows(like), 0
+
+
+def _host_rows(name, x, n=None):
+    """_offsets with the array's address."""
+    import numpy as np
+    a = np.ascontiguousarray(x, dtype=np.int64)
+    if a.ndim != 1 or (len(a) < 1 if n is None else len(a) != n):
+        raise ValueError(f"{name} must hold " + ("B + 1 offsets" if n is None else "one entry per sequence"))
+    return a, a.__array_interface__["data"][0]
 
 
 def _pages(dev, k_pages, v_pages, block_table, k_scales, v_scales, io, D=None, Hkv=None, B=None):
@@ -891,7 +909,7 @@ def ssd_attn_paged_append(q, k, v, k_pages, v_pages, block_table, lengths, cu_se
     if cu_seqlens is None:
         B, cup = T, None
     else:
-        cu, cup = _offsets("cu_seqlens", cu_seqlens)
+        cu, cup = _host_rows("cu_seqlens", cu_seqlens)
         B = len(cu) - 1
     qs = 0 if q is None else _row_stride("q", q, dev, dt, (T, Hq, D))
     ks, vs = _row_stride("k", k, dev, dt, k.shape), _row_stride("v", v, dev, dt, k.shape)
@@ -926,23 +944,27 @@ def ssd_attn_paged_gather(k_pages, v_pages, block_table, cu_seqlens, starts=None
             raise TypeError(f"rows of {dt} pages are {dt}, not {dtype}")
     else:
         dt = torch.bfloat16 if dtype is None else dtype
-    cu, cup = _offsets("cu_seqlens", cu_seqlens)
+    cu, cup = _host_rows("cu_seqlens", cu_seqlens)
     B, T = len(cu) - 1, int(cu[-1])
-    st, stp = (None, None) if starts is None else _offsets("starts", starts, B)
+    st, stp = (None, None) if starts is None else _host_rows("starts", starts, B)
     fmt, n, Hkv, p, D, _, m = _pages(dev, k_pages, v_pages, block_table, k_scales, v_scales, dt, B=B)
-    _need("k", k, dev, dt, (T, Hkv, D), optional=True)
-    _need("v", v, dev, dt, (T, Hkv, D), optional=True)
     io = SSD_BF16 if dt == torch.bfloat16 else SSD_F32 if dt == torch.float32 else None
     if io is None:
         raise TypeError(f"pages and rows must be bfloat16 or float32, got {dt}")
     d = SsdPagedDims(B, T, Hkv, Hkv, D, n, p, m, 0, 0, 0, 0, 0, 1.0, io, fmt, 0)
     with _guard(dev):
         with _on(stream):
-            k = torch.empty((max(T, 0), Hkv, D), dtype=dt, device=k_pages.device) if k is None else k
-            v = torch.empty((max(T, 0), Hkv, D), dtype=dt, device=k_pages.device) if v is None else v
+            if k is None:
+                k = k_pages.new_empty((max(T, 0), Hkv, D), dtype=dt)
+            else:
+                _need("k", k, dev, dt, (T, Hkv, D))
+            if v is None:
+                v = torch.empty_like(k)
+            else:
+                _need("v", v, dev, dt, (T, Hkv, D))
         _check("ssd_attn_paged_gather", load().ssd_attn_paged_gather(
-            ctypes.byref(d), cup, stp, _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
-            _ptr(block_table), _ptr(k), _ptr(v), _stream(stream, dev)))
+            ctypes.byref(d), cup, stp, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales),
+            block_table.data_ptr(), k.data_ptr(), v.data_ptr(), _stream(stream, dev)))
     return k, v
 
 
@@ -987,7 +1009,7 @@ def ssd_attn_paged_decode_step(q, k_pages, v_pages, block_table, lengths, k_scal
                 if o is None:
                     o = _empty_rows(q)
                 if need > 0:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+                    workspace = lengths.new_empty(need // 4)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check("ssd_attn_paged_decode_step", lib.ssd_attn_paged_decode_step(
             ctypes.byref(d), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales),
