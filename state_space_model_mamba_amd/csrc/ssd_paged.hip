@@ -46,6 +46,7 @@ struct PagedArgs {
     float2 *ml;                               // [2 W][rows] (m, l)
     int4 *rec;                                // (sequence or -1, item of it, first and last work-group) of what is
                                               // to be joined: [B HR] by item where that is no more than W
+    int spare;                                // bytes of a wave's sums beside its tiles, 0: in their place
     int by_item;                              // .. else [W] by the work-group that began it
     int64_t q_stride;
     int64_t B, cap;                           // sequences; rows that a table has pages for
@@ -774,6 +775,28 @@ void paged_decode_kernel(PagedArgs a)
             units = 0;
     }
 
+    // The queries go through LDS as the tiles do (loads into registers would wait for the tiles
+    // in flight): they land in the second slot while the first tile is on its way, and the
+    // second tile follows them.  Where the LDS has room for the waves' sums beside their tiles
+    // (a.spare), both are sent for ahead of the end of the item before.
+    constexpr bool kBeside = 16 * CB * D * (int)sizeof(T) <= Eng::kBuf;
+    const bool ahead = kBeside && a.spare > 0;
+    Parts<Eng::kParts> nxt = {};
+    bool sent = false;
+    const auto send = [&](int64_t b_, int item_, int t_, int kend_, int len_) {
+        const int rt_ = item_ % a.rtiles, hk_ = item_ / a.rtiles, rows_ = std::min(16 * CB, a.grp - 16 * CB * rt_);
+        const T *qp = (const T *)a.q + b_ * a.q_stride + ((int64_t)hk_ * a.grp + 16 * CB * rt_) * D;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+            TileLoad<T, D, 16, 1>::issue(lds0 + (kBeside ? Eng::kBuf : 0) + 16 * cb * D * (int)sizeof(T), qp, D,
+                                         std::min(16 * cb, rows_ - 1), rows_, 0, lane);
+        if (t_ < kend_) {
+            nxt = parts_of<Eng::kParts>(a, b_, hk_, t_, len_);
+            if (kBeside)
+                Eng::issue(a, lds0, nxt, Eng::whole(a, t_, len_), lane);
+        }
+    };
+
     for (int64_t u = u0; u < u1 && units > 0;) {
         const int to = (int)std::min<int64_t>(units, from + (u1 - u));
         const int rt = item % a.rtiles, hk = item / a.rtiles;
@@ -781,34 +804,22 @@ void paged_decode_kernel(PagedArgs a)
         const int64_t h0 = (int64_t)hk * a.grp + 16 * CB * rt;
         const int kend = (int)std::min<int64_t>((int64_t)to * STEP, len);
 
-        // The queries go through LDS as the tiles do (loads into registers would wait for the
-        // tiles in flight): they land in the second slot while the first tile is on its way, and
-        // the second tile follows them.
-        constexpr bool kBeside = 16 * CB * D * (int)sizeof(T) <= Eng::kBuf;
-        wait_vmcnt<0>();                                      // (stores of the item before)
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-            TileLoad<T, D, 16, 1>::issue(lds0 + (kBeside ? Eng::kBuf : 0) + 16 * cb * D * (int)sizeof(T),
-                                         (const T *)a.q + b * a.q_stride + h0 * D, D, std::min(16 * cb, rows - 1), rows,
-                                         0, lane);
         Eng eng;
         int t0 = from * STEP + KT * w;
-        Parts<Eng::kParts> nxt = {}, second = {};
-        if (t0 < kend)
-            nxt = parts_of<Eng::kParts>(a, b, hk, t0, len);
+        if (!sent) {
+            wait_vmcnt<0>();                                  // (stores of the item before)
+            send(b, item, t0, kend, len);
+        }
+        Parts<Eng::kParts> second = {};
         if (t0 + STEP < kend)
             second = parts_of<Eng::kParts>(a, b, hk, t0 + STEP, len);
-        unsigned bad = nxt.bad, bad_next = second.bad;
-        if (kBeside && t0 < kend) {
-            const bool all_rows = Eng::whole(a, t0, len);
-            Eng::issue(a, lds0, nxt, all_rows, lane);
-            if (all_rows)
-                wait_vmcnt<Eng::kWhole>();
-            else
-                wait_vmcnt<Eng::kLoads>();
-        } else {
+        unsigned bad = t0 < kend ? nxt.bad : 0u, bad_next = second.bad;
+        if (!kBeside || sent || t0 >= kend)
             wait_vmcnt<0>();
-        }
+        else if (Eng::whole(a, t0, len))
+            wait_vmcnt<Eng::kWhole>();
+        else
+            wait_vmcnt<Eng::kLoads>();
         eng.begin(a, lds0 + (kBeside ? Eng::kBuf : 0), lane);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         if (!kBeside && t0 < kend)
@@ -856,6 +867,33 @@ void paged_decode_kernel(PagedArgs a)
         }
         eng.finish(st);
 
+        // what comes next: the next item, of the next sequence that has tokens if need be
+        const bool complete = from == 0 && to == units;
+        const bool began = from == 0;
+        const int64_t ob = b, first_unit = first + (int64_t)item * units;
+        const int oitem = item, ounits = units;
+        u += to - from;
+        from = 0;
+        if (u < u1 && ++item == HR) {
+            item = 0;
+            first += (int64_t)HR * units;
+            for (b += 1; b < a.B; b += 64) {
+                const uint64_t some = a.B <= 64 ? __ballot(mylen > 0) >> b
+                                                : __ballot(b + lane < a.B && filled(a, std::min(a.B - 1, b + lane)) > 0);
+                if (some) {
+                    b += __builtin_ctzll(some);
+                    break;
+                }
+            }
+            len = b < a.B ? len_of(b) : 0;
+            units = (len + STEP - 1) / STEP;
+        }
+        sent = ahead && u < u1 && units > 0;
+        if (sent) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");        // the slots' reads are done
+            send(b, item, KT * w, (int)std::min<int64_t>(std::min<int64_t>(units, u1 - u) * STEP, len), len);
+        }
+
         // the waves' sums to a common maximum
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
@@ -866,7 +904,9 @@ void paged_decode_kernel(PagedArgs a)
             }
         }
         __syncthreads();
-        float *wp = reinterpret_cast<float *>(own);
+        unsigned char *sums = ahead ? smem + NW * kWave : smem;
+        const unsigned pitch = ahead ? (unsigned)a.spare : kWave;     // between the waves' sums
+        float *wp = reinterpret_cast<float *>(sums + w * pitch);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
             float mt = sm[0][16 * cb + c];
@@ -881,15 +921,14 @@ void paged_decode_kernel(PagedArgs a)
                         f32x4{st.acc[cb][d][0] * f, st.acc[cb][d][1] * f, st.acc[cb][d][2] * f, st.acc[cb][d][3] * f};
         }
         __syncthreads();
-        const bool complete = from == 0 && to == units;
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0)) * 16 * CB;
-        T *op = (T *)a.o + (b * a.Hq + h0) * D;
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (began ? 1 : 0)) * 16 * CB;
+        T *op = (T *)a.o + (ob * a.Hq + h0) * D;
         for (int i = 4 * tid; i < rows * D; i += 4 * NT) {
             const int row = i / D;
-            f32x4 v = *reinterpret_cast<const f32x4 *>(smem + i * 4);
+            f32x4 v = *reinterpret_cast<const f32x4 *>(sums + i * 4);
 #pragma unroll
             for (int k = 1; k < NW; ++k)
-                v += *reinterpret_cast<const f32x4 *>(smem + k * kWave + i * 4);
+                v += *reinterpret_cast<const f32x4 *>(sums + k * pitch + i * 4);
             float mr = sm[0][row], lr = 0.f;
 #pragma unroll
             for (int k = 1; k < NW; ++k)
@@ -908,32 +947,14 @@ void paged_decode_kernel(PagedArgs a)
                     a.ml[slot + row] = make_float2(mr, lr);
             }
         }
-        if (from == 0 && tid == 0 && (!complete || a.by_item)) {
-            // units [first + item units, + units): the work-group of the last one
-            const int64_t last = first + (int64_t)(item + 1) * units - 1;
+        if (began && tid == 0 && (!complete || a.by_item)) {
+            // units [first_unit, + ounits): the work-group of the last one
+            const int64_t last = first_unit + ounits - 1;
             const int64_t wl = all <= W ? last : (((last + 1) << a.logw) - 1) / all;
-            a.rec[a.by_item ? b * HR + item : blockIdx.x] =
-                make_int4(complete ? -1 : (int)b, item, (int)blockIdx.x, (int)wl);
+            a.rec[a.by_item ? ob * HR + oitem : blockIdx.x] =
+                make_int4(complete ? -1 : (int)ob, oitem, (int)blockIdx.x, (int)wl);
         }
         __syncthreads();                                      // (the LDS is written again)
-
-        u += to - from;
-        from = 0;
-        if (u < u1 && ++item == HR) {
-            // the next sequence that has tokens
-            item = 0;
-            first += (int64_t)HR * units;
-            for (b += 1; b < a.B; b += 64) {
-                const uint64_t some = a.B <= 64 ? __ballot(mylen > 0) >> b
-                                                : __ballot(b + lane < a.B && filled(a, std::min(a.B - 1, b + lane)) > 0);
-                if (some) {
-                    b += __builtin_ctzll(some);
-                    break;
-                }
-            }
-            len = b < a.B ? len_of(b) : 0;
-            units = (len + STEP - 1) / STEP;
-        }
     }
 
     // unused slots
@@ -1080,7 +1101,10 @@ hipError_t launch_paged_decode(int bf16, int64_t B, int64_t Hq, int64_t Hkv, int
     return with_engine(bf16, cache.ks != nullptr, D, a.grp > 16, [&](auto *e, auto dim, auto cols) {
         typedef std::remove_pointer_t<decltype(e)> Eng;
         constexpr int kD = decltype(dim)::value, CB = decltype(cols)::value, kOcc = occupancy<Eng>();
-        constexpr unsigned kSmem = Eng::kNW * 2u * Eng::kBuf;
+        constexpr unsigned kTiles = Eng::kNW * 2u * Eng::kBuf, kMost = 157u * 1024u / occupancy<Eng>();
+        const unsigned sums = (unsigned)std::min(a.grp, 16 * CB) * kD * 4u;
+        a.spare = kTiles + Eng::kNW * sums <= kMost ? (int)sums : 0;
+        const unsigned smem = kTiles + Eng::kNW * (unsigned)a.spare;
         static_assert(16 * CB * kD * 4 <= 2 * Eng::kBuf, "a wave's sums, and its queries, fit its tiles");
         a.rtiles = (a.grp + 16 * CB - 1) / (16 * CB);
         a.logw = log_groups<Eng>();
@@ -1092,10 +1116,10 @@ hipError_t launch_paged_decode(int bf16, int64_t B, int64_t Hq, int64_t Hkv, int
         a.by_item = items <= W;
         static std::atomic<uint64_t> allowed{0};
         const auto kernel = &paged_decode_kernel<Eng, kD, CB, kOcc>;
-        hipError_t err = allow_lds(reinterpret_cast<const void *>(kernel), (int)kSmem, allowed);
+        hipError_t err = allow_lds(reinterpret_cast<const void *>(kernel), (int)kMost, allowed);
         if (err != hipSuccess)
             return err;
-        kernel<<<dim3(W), dim3(64 * Eng::kNW), kSmem, s>>>(a);
+        kernel<<<dim3(W), dim3(64 * Eng::kNW), smem, s>>>(a);
         if ((err = hipGetLastError()) != hipSuccess || a.cap <= Eng::kNW * Eng::kKT)
             return err;                       // (items of one unit are never cut)
         // (few items have many pieces each; starting many large work-groups takes longer than
