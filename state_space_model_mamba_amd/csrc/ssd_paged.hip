@@ -8,7 +8,7 @@
 // Work.  The host knows neither the lengths nor, therefore, the work: the launch has a
 // fixed number of work-groups W, and each takes an equal share of the units of all
 // (sequence, key head, 16 or 32 query heads) items laid end to end, a unit being kNW
-// tiles of kKT keys.  A share may end inside an item; what a work-group has of an item
+// tiles of kKT keys or the start of an item.  A share may end inside an item; what a work-group has of an item
 // that others continue goes to the workspace, and a second small kernel joins those.
 // So tables much wider than the sequences are long cost nothing, and sequences of any
 // mix of lengths spread evenly.
@@ -680,21 +680,29 @@ void paged_decode_kernel(PagedArgs a)
     constexpr unsigned kWave = 2u * Eng::kBuf;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float sm[NW][16 * CB], sl[NW][16 * CB];
-    __shared__ int wsum[NW], where[2];
+    __shared__ int64_t wsum[NW];
+    __shared__ int where[2];
 
     const int tid = threadIdx.x, lane = tid & 63, w = uniform_int(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int W = 1 << a.logw, HR = a.Hkv * a.rtiles;
 
-    // this work-group's units [u0, u1) of all, and the sequence b that u0 lies in with the
-    // units before it.  Up to 64 sequences: every wave finds them from its own lanes.
-    int before = 0, total, found, mylen = 0;
+    // This work-group's units [u0, u1) of all, and the sequence b that u0 lies in with the
+    // units before it.  Beginning an item takes about as long as a unit (`extra`, its first unit
+    // then: without it work-groups with many short sequences end last, 88 us instead of 80 for 64
+    // sequences of 100 - 8190 rows in 4 bits).  Up to 64 sequences of the same number of units do
+    // without: their items divide evenly more often (16 of 8000 rows, 32 heads over one of 256: 40
+    // us, 46 with).  Where there are no more units than work-groups each gets one, so that every
+    // work-group of an item has a piece of it.  Up to 64 sequences: every wave finds its share from
+    // its own lanes.
+    int before = 0, found, mylen = 0, extra;
     int64_t all, u0, u1;
-    const auto share = [&]() {
-        all = (int64_t)total * HR;
-        // (few units: one each, so that every work-group of an item has a piece of it)
-        u0 = all <= W ? std::min<int64_t>(all, blockIdx.x) : (all * blockIdx.x) >> a.logw;
-        u1 = all <= W ? std::min<int64_t>(all, blockIdx.x + 1) : (all * (blockIdx.x + 1)) >> a.logw;
+    const auto share = [&](int total, int count, bool alike) {
+        const bool few = (int64_t)total * HR <= W;
+        extra = few || alike ? 0 : 1;
+        all = (int64_t)(total + extra * count) * HR;
+        u0 = few ? std::min<int64_t>(all, blockIdx.x) : (all * blockIdx.x) >> a.logw;
+        u1 = few ? std::min<int64_t>(all, blockIdx.x + 1) : (all * (blockIdx.x + 1)) >> a.logw;
     };
     if (a.B <= 64) {
         mylen = lane < a.B ? filled(a, lane) : 0;
@@ -706,20 +714,27 @@ void paged_decode_kernel(PagedArgs a)
         incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xf, 0xf, false);
         incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xa, 0xf, false);   // row_bcast 15, 31
         incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xc, 0xf, false);
-        total = __builtin_amdgcn_readlane(incl, 63);
-        share();
+        const uint64_t some = __ballot(mylen > 0);
+        const int one = __builtin_amdgcn_readlane(mine, some ? __builtin_ctzll(some) : 0);
+        share(__builtin_amdgcn_readlane(incl, 63), __popcll(some), __all(mine == 0 || mine == one));
+        incl += extra * __popcll(some & (~uint64_t(0) >> (63 - lane)));
         const uint64_t past = __ballot((int64_t)incl * HR > u0);
         found = past ? __builtin_ctzll(past) : -1;
-        before = __builtin_amdgcn_readlane(incl - mine, past ? found : 0);
+        before = __builtin_amdgcn_readlane(incl - mine - (mylen > 0 ? extra : 0), past ? found : 0);
     } else {
+        // (units below 2^32, and sequences above)
         const int per = (int)((a.B + NT - 1) / NT), b0 = tid * per, b1 = std::min((int)a.B, b0 + per);
-        int mine = 0;
+        const auto units_of = [&](int b) {
+            const int n = (filled(a, b) + STEP - 1) / STEP;
+            return n > 0 ? (int64_t(1) << 32) + n : 0;
+        };
+        int64_t mine = 0;
         for (int b = b0; b < b1; ++b)
-            mine += (filled(a, b) + STEP - 1) / STEP;
-        int incl = mine;
+            mine += units_of(b);
+        int64_t incl = mine;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
-            const int up = __shfl_up(incl, off, 64);
+            const int64_t up = __shfl_up(incl, off, 64);
             if (lane >= off)
                 incl += up;
         }
@@ -728,26 +743,25 @@ void paged_decode_kernel(PagedArgs a)
         if (tid == 0)
             where[0] = -1;
         __syncthreads();
-        int excl = incl - mine;
-        total = 0;
+        int64_t excl = incl - mine, total = 0;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
             if (i < w)
                 excl += wsum[i];
             total += wsum[i];
         }
-        total = uniform_int(total);
-        share();
-        if (u0 >= (int64_t)excl * HR && u0 < (int64_t)(excl + mine) * HR) {
+        share(uniform_int((int)total), uniform_int((int)(total >> 32)), false);
+        const auto weight = [&](int64_t x) { return (int64_t)((int)x + extra * (int)(x >> 32)) * HR; };
+        if (u0 >= weight(excl) && u0 < weight(excl + mine)) {
             int b = b0;
             for (; b + 1 < b1; ++b) {
-                const int n = (filled(a, b) + STEP - 1) / STEP;
-                if (u0 < (int64_t)(excl + n) * HR)
+                const int64_t n = units_of(b);
+                if (u0 < weight(excl + n))
                     break;
                 excl += n;
             }
             where[0] = b;
-            where[1] = excl;
+            where[1] = (int)excl + extra * (int)(excl >> 32);
         }
         __syncthreads();
         found = uniform_int(where[0]);
@@ -766,11 +780,11 @@ void paged_decode_kernel(PagedArgs a)
     };
     int len = u0 < u1 && found >= 0 ? len_of(b) : 0;
     int units = (len + STEP - 1) / STEP;
-    int item = 0, from = 0;
+    int item = 0, from = 0;                                   // from: among units + extra
     if (units > 0) {
         const unsigned at = (unsigned)(u0 - first);           // (below 2^31: checked on the host)
-        item = (int)(at / (unsigned)units);
-        from = (int)(at % (unsigned)units);
+        item = (int)(at / (unsigned)(units + extra));
+        from = (int)(at % (unsigned)(units + extra));
         if (item >= HR)
             units = 0;
     }
@@ -798,14 +812,17 @@ void paged_decode_kernel(PagedArgs a)
     };
 
     for (int64_t u = u0; u < u1 && units > 0;) {
-        const int to = (int)std::min<int64_t>(units, from + (u1 - u));
+        const int end = (int)std::min<int64_t>(units + extra, from + (u1 - u));
+        const int begin = std::max(0, from - extra), to = end - extra;    // units of keys
+        if (begin >= to)
+            break;
         const int rt = item % a.rtiles, hk = item / a.rtiles;
         const int rows = std::min(16 * CB, a.grp - 16 * CB * rt);
         const int64_t h0 = (int64_t)hk * a.grp + 16 * CB * rt;
         const int kend = (int)std::min<int64_t>((int64_t)to * STEP, len);
 
         Eng eng;
-        int t0 = from * STEP + KT * w;
+        int t0 = begin * STEP + KT * w;
         if (!sent) {
             wait_vmcnt<0>();                                  // (stores of the item before)
             send(b, item, t0, kend, len);
@@ -868,15 +885,14 @@ void paged_decode_kernel(PagedArgs a)
         eng.finish(st);
 
         // what comes next: the next item, of the next sequence that has tokens if need be
-        const bool complete = from == 0 && to == units;
-        const bool began = from == 0;
-        const int64_t ob = b, first_unit = first + (int64_t)item * units;
-        const int oitem = item, ounits = units;
-        u += to - from;
+        const bool began = begin == 0, complete = began && to == units;
+        const int64_t ob = b, last = first + (int64_t)(item + 1) * (units + extra) - 1;
+        const int oitem = item;
+        u += end - from;
         from = 0;
         if (u < u1 && ++item == HR) {
             item = 0;
-            first += (int64_t)HR * units;
+            first += (int64_t)HR * (units + extra);
             for (b += 1; b < a.B; b += 64) {
                 const uint64_t some = a.B <= 64 ? __ballot(mylen > 0) >> b
                                                 : __ballot(b + lane < a.B && filled(a, std::min(a.B - 1, b + lane)) > 0);
@@ -888,10 +904,10 @@ void paged_decode_kernel(PagedArgs a)
             len = b < a.B ? len_of(b) : 0;
             units = (len + STEP - 1) / STEP;
         }
-        sent = ahead && u < u1 && units > 0;
+        sent = ahead && u1 - u > extra && units > 0;
         if (sent) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");        // the slots' reads are done
-            send(b, item, KT * w, (int)std::min<int64_t>(std::min<int64_t>(units, u1 - u) * STEP, len), len);
+            send(b, item, KT * w, (int)std::min<int64_t>(std::min<int64_t>(units, u1 - u - extra) * STEP, len), len);
         }
 
         // the waves' sums to a common maximum
@@ -948,8 +964,7 @@ void paged_decode_kernel(PagedArgs a)
             }
         }
         if (began && tid == 0 && (!complete || a.by_item)) {
-            // units [first_unit, + ounits): the work-group of the last one
-            const int64_t last = first_unit + ounits - 1;
+            // the work-group of the item's last unit
             const int64_t wl = all <= W ? last : (((last + 1) << a.logw) - 1) / all;
             a.rec[a.by_item ? ob * HR + oitem : blockIdx.x] =
                 make_int4(complete ? -1 : (int)ob, oitem, (int)blockIdx.x, (int)wl);
