@@ -18,6 +18,16 @@
 // scalars, and the probabilities are the second product's operand as they stand.  Tiles
 // go from memory straight into LDS, two deep per wave, in parts of 16 rows: a part never
 // crosses a page, so pages of 16 rows and more need no care.
+//
+// Bound by memory over pages of the input type: one sequence of 131000 rows, 32 heads over
+// 8 of 128 in bf16, 98 us and the join's 5 (537 MB at 5.5 TB/s; a large copy reaches 5.08
+// on the same card); 64 of 100 - 8190 rows 193 with the append in front.  Over 4-bit pages
+// the instructions of a tile take about as long as its bytes: vector units 48% busy, matrix
+// units 15%, 33 us for the long sequence's 151 MB (4.5 TB/s) and 4 for the join, 70 and 5 for
+// the 64.  Small calls take 6 - 12 us: the look-ups in front of the first tile, a tile, and
+// the join's launch.  Tried and no better: twice and four times as many work-groups (8 and 25
+// us more: each starts with look-ups and an empty pipeline), a second round of small
+// work-groups for the end (4 - 8 us more for even batches).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -349,7 +359,8 @@ template <typename T_, int D, int CB> struct WideTile {
 // ---------------------------------------------------------------------------
 // Pages of 4-bit codes
 // ---------------------------------------------------------------------------
-// Two codes n, n' of a dword's halves become the bf16 pair (16 + n, 16 + n') with a shift
+// A value costs one instruction to unpack where a bf16 page costs none, so the work around it
+// is kept off the vector units.  Two codes n, n' of a dword's halves become the bf16 pair (16 + n, 16 + n') with a shift
 // and an and-or, and that is the products' operand: with step s and least value m of the
 // 64 values of group G,
 //     q . k_G = s (sum q (16 + n)) + (m - 16 s) sum q        (the 16s: the product's initial value)
@@ -689,7 +700,7 @@ void paged_decode_kernel(PagedArgs a)
 
     // This work-group's units [u0, u1) of all, and the sequence b that u0 lies in with the
     // units before it.  Beginning an item takes about as long as a unit (`extra`, its first unit
-    // then: without it work-groups with many short sequences end last, 88 us instead of 80 for 64
+    // then: without it work-groups with many short sequences end last, 88 us instead of 77 for 64
     // sequences of 100 - 8190 rows in 4 bits).  Up to 64 sequences of the same number of units do
     // without: their items divide evenly more often (16 of 8000 rows, 32 heads over one of 256: 40
     // us, 46 with).  Where there are no more units than work-groups each gets one, so that every
@@ -991,7 +1002,7 @@ template <typename T, int D, int CB, int kT> __global__ __launch_bounds__(kT) vo
     __shared__ float4 sacc[G][LPR];
     __shared__ float sl[G];
     const int4 rec = a.rec[blockIdx.x];
-    if (rec.x < 0)
+    if (rec.x < 0 || rec.x >= a.B || rec.z < 0 || rec.w >= 1 << a.logw)   // (lengths that changed under the kernel)
         return;
     const int tid = threadIdx.x, gr = tid / LPR, d4 = tid % LPR;
     const int w0 = rec.z, n = rec.w - w0 + 1;

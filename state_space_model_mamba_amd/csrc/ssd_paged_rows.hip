@@ -124,7 +124,13 @@ enum { kNoPages, kPages, kPages4 };
 // lanes to a head, 8 values to a lane: for halves paired over R / 2 the four at 4 j and
 // the four at R / 2 + 4 j, so that a lane has both of a pair and nothing moves between
 // lanes but the sum of squares; otherwise 8 j .. 8 j + 7.  The angles' sines and cosines
-// are formed once per token and wave, one or two angles to a lane.
+// are formed once per token and wave, one or two angles to a lane (each lane its own four
+// took 8 us more in 138).
+//
+// Bound by memory: 32768 tokens of 32 + 8 heads of 128 in bf16 take 130 us, 5.2 TB/s (a large
+// copy 5.08); with the append of 21150 tokens 105 us, 4.9 TB/s.  Into 4 bits 116 us for 12%
+// fewer bytes: the vector units are 71% busy, and rows of 64 bytes are written one by one.
+// One token takes 4.6 us, most of it the look-ups, one after the other.
 template <typename T, int D, int kKind>
 __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
 {
@@ -362,7 +368,8 @@ struct GatherArgs {
 typedef const __attribute__((address_space(4))) GatherArgs *GatherArgsPtr;
 
 // A wave takes 16 consecutive lines of a page (lines 16 n .., of one head) of k or of v:
-// contiguous there, one segment per line in the output.
+// contiguous there, one segment per line in the output.  26300 rows of 8 heads of 128 from
+// 4 bits to bf16: 26 us, 5.2 TB/s.
 template <typename T, int D, bool kQ4>
 __global__ __launch_bounds__(256) void gather_kernel(GatherArgs args_in_kernarg)
 {

@@ -186,6 +186,57 @@ def test_rows_on_a_stream():
     assert torch.equal(q, q2) and torch.equal(q, q3) and torch.equal(k2, k3) and torch.equal(v2, L.prompt[2][0])
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+def test_prompts_captured_and_given_outputs(bits):
+    """Append of prompts and reading back captured in a graph with all outputs given, replayed on
+    other inputs; the same calls eagerly in between."""
+    L = Layer(7, "bf16", [33, 0, 70], 0, D=128)
+    cu = L.cu
+    (kp, vp, tab), sc = L.cache(bits)
+    (ke, ve, _), sce = L.cache(bits)
+    n = L.lengths()
+    q, k, v = (x[0].clone() for x in L.prompt)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    kr, vr = torch.empty_like(k), torch.empty_like(k)
+
+    def run(kp, vp, sc, qo, ko, kr, vr):
+        ssd.ssd_attn_paged_append(q, k, v, kp, vp, tab, n, cu_seqlens=cu, q_out=qo, k_out=ko, **sc, **L.turn)
+        return ssd.ssd_attn_paged_gather(kp, vp, tab, cu, k=kr, v=vr, **sc)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(kp, vp, sc, qo, ko, kr, vr)
+    assert got[0] is kr and got[1] is vr
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    for _ in range(3):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+        g.replay()
+        torch.cuda.synchronize()
+        want = [torch.empty_like(x) for x in (qo, ko, kr, vr)]
+        run(ke, ve, sce, *want)
+        assert all(torch.equal(x, y) for x, y in zip((qo, ko, kr, vr), want))
+    for a, b in zip((kp, vp, *sc.values()), (ke, ve, *sce.values())):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_empty_batches_and_prompts(bits):
+    L = Layer(9, "bf16", [5], 0, D=128)
+    (kp, vp, tab), sc = L.cache(bits)
+    before = [x.clone() for x in (kp, vp, *sc.values())]
+    q, k, v = (x[0] for x in L.prompt)
+    none = tab[:0]
+    n = L.lengths()
+    ssd.ssd_attn_paged_append(q[:0], k[:0], v[:0], kp, vp, none, n[:0], **sc, **L.turn)
+    ssd.ssd_attn_paged_append(q[:0], k[:0], v[:0], kp, vp, tab, n, cu_seqlens=[0, 0], **sc, **L.turn)
+    assert ssd.ssd_attn_paged_decode_step(q[:0], kp, vp, none, n[:0], **sc).shape == (0, L.Hq, L.D)
+    kr, vr = ssd.ssd_attn_paged_gather(kp, vp, none, [0], **sc)
+    assert kr.shape == vr.shape == (0, L.Hkv, L.D)
+    o = ssd.ssd_attn_paged_decode_step(q[:1], kp, vp, tab, n - 1, **sc)
+    assert not o.any() and all(torch.equal(x, y) for x, y in zip((kp, vp, *sc.values()), before))
+
+
 def test_refusals():
     """Wrong types, shapes and devices are refused by name before anything runs."""
     L = Layer(6, "bf16", [4], 0)
