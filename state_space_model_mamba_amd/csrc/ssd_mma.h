@@ -293,11 +293,13 @@ __device__ __forceinline__ u32x4 buffer_words(const void *base, unsigned bytes)
 
 // 16 bytes per lane from the buffer into LDS at dst + 16 lane.  Written as
 // assembly because the compiler waits for every such load before any LDS read;
-// the reader waits with wait_vmcnt and a barrier instead.  (One wait state
-// between writing m0 and the load that reads it.)
+// the reader waits with wait_vmcnt and a barrier instead.  (Five wait states
+// between a vector instruction that writes a scalar register, as the ones before
+// this statement may, and a load that reads it, which the compiler does not see
+// to inside the statement; one after writing m0.)
 __device__ __forceinline__ void lds_load16(unsigned dst, u32x4 rsrc, unsigned voff, unsigned soff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(uniform_int((int)dst)), "v"(voff), "s"(rsrc), "s"(uniform_int((int)soff)) : "memory", "m0");
 }
 

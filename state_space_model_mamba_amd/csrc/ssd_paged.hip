@@ -483,13 +483,13 @@ template <typename T_, int D, int CB> struct CodeTile {
     template <int kLanes> static __device__ __forceinline__ void load16(unsigned dst, const unsigned char *base, unsigned voff, int lane)
     {
         if (kLanes >= 64 || lane < kLanes)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                          :: "s"(uniform_int((int)dst)), "v"(voff), "s"(base) : "memory", "m0");
     }
     template <int kLanes> static __device__ __forceinline__ void load4(unsigned dst, const unsigned char *base, unsigned voff, int lane)
     {
         if (kLanes >= 64 || lane < kLanes)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2"
                          :: "s"(uniform_int((int)dst)), "v"(voff), "s"(base) : "memory", "m0");
     }
 
