@@ -282,8 +282,8 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
                 if (kKind == kPages && live && !isq && stored) {
                     const int64_t at = line + ((int64_t)(isv ? h - Hq - Hkv : h - Hq) << a->c.shift);
                     T *dst = (T *)(isv ? a->c.v : a->c.k) + at * D;
-                    *reinterpret_cast<typename F::V *>(dst + da) = F::close(x);
-                    *reinterpret_cast<typename F::V *>(dst + db) = F::close(x + 4);
+                    *reinterpret_cast<typename F::V *>(dst + da) = isv ? now[u][0] : F::close(x);
+                    *reinterpret_cast<typename F::V *>(dst + db) = isv ? now[u][1] : F::close(x + 4);
                 }
                 if constexpr (kKind == kPages4) {
                     if (!stored || hb + (u + 1) * HW <= Hq)

@@ -249,6 +249,21 @@ def test_append_without_queries_and_in_place():
     assert np.array_equal(host(v), vv)
 
 
+@pytest.mark.parametrize("dt,it", [(torch.bfloat16, torch.int16), (torch.float32, torch.int32)])
+def test_values_are_copied_bit_by_bit(dt, it):
+    """Any bits of v reach the pages as they are: subnormal numbers, signed zeros, infinities, NaN."""
+    gen = torch.Generator().manual_seed(10)
+    bits = torch.randint(torch.iinfo(it).min, torch.iinfo(it).max, (30, 2, 64), generator=gen, dtype=torch.int64).to(it)
+    bits[0, 0, :8] = torch.tensor([0, -(1 << (15 if it is torch.int16 else 31)), 1, 2, 3, 4, 5, 6]).to(it)
+    v = bits.cuda().view(dt)
+    k = torch.zeros_like(v)
+    c = empty_cache(11, "bf16" if dt is torch.bfloat16 else "f32", 16, 1, 2, 16, 2, 64)
+    ssd.ssd_attn_paged_append(None, k, v, c["k"], c["v"], dev(c["table"]), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                              cu_seqlens=[0, 30])
+    _, back = ssd.ssd_attn_paged_gather(c["k"], c["v"], dev(c["table"]), [0, 30])
+    assert torch.equal(back.view(it).cpu(), bits)
+
+
 def test_four_bit_rows_of_special_values():
     """Constant rows, values past half precision's range, tiny values, one outlier."""
     D, page = 64, 16
