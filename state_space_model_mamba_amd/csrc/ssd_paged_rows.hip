@@ -127,12 +127,14 @@ enum { kNoPages, kPages, kPages4 };
 // are formed once per token and wave, one or two angles to a lane (each lane its own four
 // took 8 us more in 138).
 //
-// Bound by memory: 32768 tokens of 32 + 8 heads of 128 in bf16 take 130 us, 5.2 TB/s (a large
-// copy 5.08); with the append of 21150 tokens 105 us, 4.9 TB/s.  Into 4 bits 116 us for 12%
-// fewer bytes: the vector units are 71% busy, and rows of 64 bytes are written one by one.
+// Bound by memory: 32768 tokens of 32 + 8 heads of 128 in bf16 take 128 us, 5.2 TB/s (a large
+// copy 5.08); with the append of 21150 tokens 105 us, 4.9 TB/s.  Into 4 bits 110 us for 12%
+// fewer bytes, the vector units 63% busy and rows of 64 bytes written one by one.  Five waves per SIMD in bf16, 96
+// registers each: with the four of the compiler's own choice for the 4-bit append, 102, it and
+// the reading back take 142 us, with five 138, with six, which spill, 154.
 // One token takes 4.6 us, most of it the look-ups, one after the other.
 template <typename T, int D, int kKind>
-__global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnArgs args_in_kernarg)
 {
     constexpr int LPH = D / 8, HW = 64 / LPH; // lanes of a head, heads at once
     constexpr int U = 4;                      // head groups of a round; the next round's loads are in flight
@@ -209,7 +211,12 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
 #pragma unroll
             for (int n = 0; n < NA; ++n) {
                 const double turns = (double)pos * freq[n];
-                sincospif((float)(2.0 * (turns - __builtin_rint(turns))), &s1[n], &c1[n]);
+                const double half = 2.0 * (turns - __builtin_rint(turns));
+                const float hi = (float)half, lo = 3.14159265f * (float)(half - (double)hi);
+                float s0, c0;
+                sincospif(hi, &s0, &c0);
+                s1[n] = __builtin_fmaf(c0, lo, s0);   // (and what fp32 left of the angle)
+                c1[n] = __builtin_fmaf(-s0, lo, c0);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -311,12 +318,18 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs args_in_kernarg)
                     const _Float16 least = (_Float16)fminf(fmaxf(lo, -kHalfMax), kHalfMax);
                     const _Float16 step = (_Float16)fminf((hi - lo) / 15.f, kHalfMax);
                     const float fl = (float)least, fs = (float)step;
-                    unsigned codes = 0;
+                    // The quotients, rounded as a division rounds them (its last steps, with one
+                    // reciprocal for all) and to whole numbers by adding 3 2^22, whose low bits
+                    // they become: its own bits, eight times shifted, add up to 0x3f400000.  (A step
+                    // of 0: all codes 0.)
+                    const float est = __builtin_amdgcn_rcpf(fs), top = 15.f * fs;
+                    const float inv = fs > 0.f ? __builtin_fmaf(__builtin_fmaf(-fs, est, 1.f), est, est) : 0.f;
+                    unsigned codes = 0u - 0x3f400000u;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float q = __builtin_rintf((y[e] - fl) / fs);   // (a step of 0: all codes 0)
-                        const unsigned code = fs > 0.f ? (unsigned)fminf(fmaxf(q, 0.f), 15.f) : 0u;
-                        codes |= code << (4 * e);
+                        const float n = __builtin_amdgcn_fmed3f(y[e] - fl, 0.f, top), q = n * inv;
+                        const float r = __builtin_fmaf(__builtin_fmaf(-q, fs, n), inv, q) + 12582912.f;
+                        codes += __float_as_uint(r) << (4 * e);
                     }
                     if (live && !isq) {
                         const int64_t at = line + ((int64_t)(isv ? h - Hq - Hkv : h - Hq) << a->c.shift);
