@@ -534,8 +534,9 @@ ssd_status ssd_attn_paged_gather(const ssd_paged_dims *dims, const int64_t *cu_s
  *   q, o [B, Hq, D] io_dtype; q_stride: elements between rows of q
  * The work is shared out on the device by the lengths, so the width of the table does
  * not matter, and results depend on the batch only by rounding (deterministic for the
- * same lengths).  An infinity or NaN in a value row reaches its own sequence only.  With n = kv_heads * (32-head tiles of a key head's queries): batch n < 2^24,
- * and n, and batch, times max_pages page_size + 32 at most 2^35.
+ * same lengths).  An infinity or NaN in a value row reaches its own sequence only.
+ * With n = kv_heads * (32-head tiles of a key head's queries): batch n < 2^24, and n,
+ * and batch, times max_pages page_size + 32 at most 2^35.
  * workspace: >= ssd_attn_paged_decode_workspace_size bytes, which do not depend on
  * the lengths, 16-byte aligned; one per call that may run at the same time (also per
  * captured graph that may).  o and the workspace overlap no input and not each other.

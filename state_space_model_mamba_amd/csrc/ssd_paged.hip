@@ -8,9 +8,9 @@
 // Work.  The host knows neither the lengths nor, therefore, the work: the launch has a
 // fixed number of work-groups W, and each takes an equal share of the units of all
 // (sequence, key head, 16 or 32 query heads) items laid end to end, a unit being kNW
-// tiles of kKT keys or the start of an item.  A share may end inside an item; what a work-group has of an item
-// that others continue goes to the workspace, and a second small kernel joins those.
-// So tables much wider than the sequences are long cost nothing, and sequences of any
+// tiles of kKT keys or the start of an item.  A share may end inside an item; what a
+// work-group has of an item that others continue goes to the workspace, and a second small
+// kernel joins those.  So tables much wider than the sequences are long cost nothing, and sequences of any
 // mix of lengths spread evenly.
 //
 // Scores are formed transposed (keys x query heads, 16 x 16 blocks): lane c + 16 g holds
@@ -56,8 +56,8 @@ struct PagedArgs {
     float2 *ml;                               // [2 W][rows] (m, l)
     int4 *rec;                                // (sequence or -1, item of it, first and last work-group) of what is
                                               // to be joined: [B HR] by item where that is no more than W
-    int spare;                                // bytes of a wave's sums beside its tiles, 0: in their place
     int by_item;                              // .. else [W] by the work-group that began it
+    int spare;                                // bytes of a wave's sums beside its tiles, 0: in their place
     int64_t q_stride;
     int64_t B, cap;                           // sequences; rows that a table has pages for
     int Hq, Hkv, grp, rtiles, logw;
@@ -360,9 +360,9 @@ template <typename T_, int D, int CB> struct WideTile {
 // Pages of 4-bit codes
 // ---------------------------------------------------------------------------
 // A value costs one instruction to unpack where a bf16 page costs none, so the work around it
-// is kept off the vector units.  Two codes n, n' of a dword's halves become the bf16 pair (16 + n, 16 + n') with a shift
-// and an and-or, and that is the products' operand: with step s and least value m of the
-// 64 values of group G,
+// is kept off the vector units.  Two codes n, n' of a dword's halves become the bf16 pair
+// (16 + n, 16 + n') with a shift and an and-or, and that is the products' operand: with step s
+// and least value m of the 64 values of group G,
 //     q . k_G = s (sum q (16 + n)) + (m - 16 s) sum q        (the 16s: the product's initial value)
 //     sum_t p_t v_t = sum_t (p_t s_t) (16 + n_t) + sum_t p_t (m_t - 16 s_t)
 // so that scales cost one multiply-add per score or probability and group instead of one

@@ -129,9 +129,9 @@ enum { kNoPages, kPages, kPages4 };
 //
 // Bound by memory: 32768 tokens of 32 + 8 heads of 128 in bf16 take 128 us, 5.2 TB/s (a large
 // copy 5.08); with the append of 21150 tokens 105 us, 4.9 TB/s.  Into 4 bits 110 us for 12%
-// fewer bytes, the vector units 63% busy and rows of 64 bytes written one by one.  Five waves per SIMD in bf16, 96
-// registers each: with the four of the compiler's own choice for the 4-bit append, 102, it and
-// the reading back take 142 us, with five 138, with six, which spill, 154.
+// fewer bytes, the vector units 63% busy and rows of 64 bytes written one by one.  Five waves
+// per SIMD in bf16, 96 registers each: with four (102, the compiler's own choice for the 4-bit
+// append) it and the reading back take 142 us, with five 138, with six, which spill, 154.
 // One token takes 4.6 us, most of it the look-ups, one after the other.
 template <typename T, int D, int kKind>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnArgs args_in_kernarg)

@@ -290,6 +290,30 @@ def test_four_bit_rows_of_special_values():
     assert torch.equal(k[0], t[0]) and torch.equal(k[5], t[5]) and (k[3] - t[3]).abs().max() <= 2.0 ** -24
 
 
+def test_four_bit_codes_beside_ties():
+    """Values in the middle between two codes go to the even one, and four fp32 steps beside it
+    (further than a rounded quotient is off) to the nearer; steps of every size, tiny ones too."""
+    D, rows = 64, 200
+    rng = np.random.default_rng(3)
+    s = (2.0 ** rng.uniform(-24, 11.9, rows)).astype(np.float16)
+    s[:4] = 2.0 ** -24, 3 * 2.0 ** -24, 2.0 ** -14, 4096
+    tie = (np.arange(15, dtype=np.float64) + 0.5) * s.astype(np.float64)[:, None]
+    tie = tie.astype(np.float32)                                      # (exact: 11 + 5 bits)
+    step = 4 * np.spacing(tie)
+    x = np.zeros((rows, 1, D), dtype=np.float32)
+    x[:, 0, 1], x[:, 0, 2:17], x[:, 0, 20:35], x[:, 0, 40:55] = 15 * s.astype(np.float32), tie, tie - step, tie + step
+    c = empty_cache(8, "f32", 4, 1, 16, 16, 1, D)
+    t = torch.from_numpy(x).cuda()
+    ssd.ssd_attn_paged_append(None, t, t, c["k"], c["v"], dev(c["table"]), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                              cu_seqlens=[0, rows], k_scales=c["ks"], v_scales=c["vs"])
+    for r in range(rows):
+        page, line = int(c["table"][0, r // 16]), r % 16
+        wc, ws = orc.store4(x[r, 0].astype(np.float64))
+        for name in ("k", "v"):
+            codes, sc = c[name][page, 0, line].cpu().numpy(), c[name + "s"][page, 0, line].cpu().numpy()
+            assert np.array_equal(sc.view(np.int16), ws.view(np.int16)) and np.array_equal(codes, wc), (name, r, s[r])
+
+
 # --------------------------------------------------------------------------
 # Reading back
 # --------------------------------------------------------------------------
