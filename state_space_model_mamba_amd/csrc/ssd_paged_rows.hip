@@ -72,6 +72,50 @@ template <int kLanes, typename Op> __device__ __forceinline__ float across(float
     return v;
 }
 
+// The sum of four squares, each rounded: a head's fours are then added in pairs of neighbours,
+// whatever the rotation's pairs, which is as near as fp32 sums come and, for D = 128, the order
+// of torch's mean.  4-bit codes depend on the last bits where a value lies between two: with
+// sums in another order, the hardware's reciprocal root and sincospif 17 - 28 of 21.7 million
+// differed from those of the formula written in torch, now none to two (for 3 us in 138).
+__device__ __forceinline__ float four_squares(const float *x)
+{
+#pragma clang fp contract(off)
+    return x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+}
+
+// 1 / sqrt(z), the hardware's estimate and a Newton step whose residual 1 - z y^2 is exact to
+// second order.  (0 and infinity: as the estimate; its residual would be NaN.)
+__device__ __forceinline__ float rsqrt_near(float z)
+{
+    const float y = rsqrtf(z), t = z * y;
+    const float e = __builtin_fmaf(-__builtin_fmaf(z, y, -t), y, __builtin_fmaf(-t, y, 1.f));
+    return fabsf(e) < 1.f ? __builtin_fmaf(0.5f * y, e, y) : y;
+}
+
+// Sine and cosine of x turns, |x| <= 1/2: the Taylor series about the nearest quarter turn, with
+// the leading terms as sums of two fp32 numbers, so that only their last addition rounds.  (All
+// in fp64 the constants' registers make the appends spill: 117 us instead of 106 for 21150 tokens.)
+__device__ __forceinline__ void sincos_turns(double x, float &sine, float &cosine)
+{
+    const double q = __builtin_rint(4.0 * x), ud = 6.283185307179586 * __builtin_fma(-0.25, q, x);
+    const float u = (float)ud, ul = (float)(ud - (double)u);
+    const float v = u * u, vl = __builtin_fmaf(2.f * u, ul, __builtin_fmaf(u, u, -v));
+    float s = __builtin_fmaf(v, -1.f / 39916800, 1.f / 362880);
+    s = __builtin_fmaf(v, s, -1.f / 5040);
+    s = __builtin_fmaf(v, s, 1.f / 120);
+    s = __builtin_fmaf(v, s, -1.f / 6);
+    s = u + __builtin_fmaf(u * v, s, ul);
+    float c = __builtin_fmaf(v, -1.f / 3628800, 1.f / 40320);
+    c = __builtin_fmaf(v, c, -1.f / 720);
+    c = __builtin_fmaf(v, c, 1.f / 24);
+    const float h = __builtin_fmaf(-0.5f, v, 1.f), hl = __builtin_fmaf(-0.5f, v, 1.f - h);
+    c = h + __builtin_fmaf(v * v, c, __builtin_fmaf(-0.5f, vl, hl));
+    const int k = (int)q;
+    const float a = k & 1 ? c : s, b = k & 1 ? s : c;
+    sine = k & 2 ? -a : a;
+    cosine = (k + 1) & 2 ? -b : b;
+}
+
 // Four values of T.
 template <typename T> struct Four;
 template <> struct Four<__bf16> {
@@ -127,9 +171,9 @@ enum { kNoPages, kPages, kPages4 };
 // are formed once per token and wave, one or two angles to a lane (each lane its own four
 // took 8 us more in 138).
 //
-// Bound by memory: 32768 tokens of 32 + 8 heads of 128 in bf16 take 128 us, 5.2 TB/s (a large
-// copy 5.08); with the append of 21150 tokens 105 us, 4.9 TB/s.  Into 4 bits 110 us for 12%
-// fewer bytes, the vector units 63% busy and rows of 64 bytes written one by one.  Five waves
+// Bound by memory: 32768 tokens of 32 + 8 heads of 128 in bf16 take 130 us, 5.2 TB/s (a large
+// copy 5.08); with the append of 21150 tokens 107 us, 4.8 TB/s.  Into 4 bits 114 us for 12%
+// fewer bytes, the vector units 68% busy and rows of 64 bytes written one by one.  Five waves
 // per SIMD in bf16, 96 registers each: with four (102, the compiler's own choice for the 4-bit
 // append) it and the reading back take 142 us, with five 138, with six, which spill, 154.
 // One token takes 4.6 us, most of it the look-ups, one after the other.
@@ -149,6 +193,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnA
     const int NH = Hq + (kKind == kNoPages ? Hkv : 2 * Hkv);
     const int rot = a->turn.rot;
     const bool next = a->turn.next != 0, turned = j < rot / 8;
+    const bool apart = !next && rot == D;     // a lane's fours lie half a head apart: no neighbours
     const int oa = !next && turned ? 4 * j : 8 * j, ob = !next && turned ? rot / 2 + 4 * j : 8 * j + 4;
 
     const float *qw = a->turn.q_weight, *kw = a->turn.k_weight;
@@ -211,12 +256,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnA
 #pragma unroll
             for (int n = 0; n < NA; ++n) {
                 const double turns = (double)pos * freq[n];
-                const double half = 2.0 * (turns - __builtin_rint(turns));
-                const float hi = (float)half, lo = 3.14159265f * (float)(half - (double)hi);
-                float s0, c0;
-                sincospif(hi, &s0, &c0);
-                s1[n] = __builtin_fmaf(c0, lo, s0);   // (and what fp32 left of the angle)
-                c1[n] = __builtin_fmaf(-s0, lo, c0);
+                sincos_turns(turns - __builtin_rint(turns), s1[n], c1[n]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -250,17 +290,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnA
                 F::open(now[u][0], x);
                 F::open(now[u][1], x + 4);
                 if (live ? (isq ? qw : isv ? nullptr : kw) != nullptr : false) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        ss = __builtin_fmaf(x[e], x[e], ss);
-                    ss = across<LPH>(ss, [](float p, float q) { return p + q; });
-                    const float rs = rsqrtf(ss * (1.f / D) + eps);
+                    const auto add = [](float p, float q) { return p + q; };
+                    float ss = four_squares(x);
+                    const float s4 = four_squares(x + 4);
+                    ss = apart ? across<LPH>(ss, add) + across<LPH>(s4, add) : across<LPH>(ss + s4, add);
+                    const float rs = rsqrt_near(ss * (1.f / D) + eps);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         x[e] = x[e] * rs * (isq ? wq[e] : wk[e]);
                 }
                 if (turned && !isv) {
+#pragma clang fp contract(off)                // (each product rounded: both of a pair alike)
                     if (next) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -316,7 +356,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnA
                     lo = across<8>(lo, [](float p, float q) { return fminf(p, q); });
                     hi = across<8>(hi, [](float p, float q) { return fmaxf(p, q); });
                     const _Float16 least = (_Float16)fminf(fmaxf(lo, -kHalfMax), kHalfMax);
-                    const _Float16 step = (_Float16)fminf((hi - lo) / 15.f, kHalfMax);
+                    const _Float16 step = (_Float16)fminf((hi - lo) * (1.f / 15), kHalfMax);
                     const float fl = (float)least, fs = (float)step;
                     // The quotients, rounded as a division rounds them (its last steps, with one
                     // reciprocal for all) and to whole numbers by adding 3 2^22, whose low bits
