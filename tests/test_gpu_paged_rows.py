@@ -51,6 +51,29 @@ def test_norm_rope(io, D, R, inter, which, T, Hq, Hkv, sliced):
         within(got, out, turn_bound(io, out, size, pos), what)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_sines_and_cosines(inter):
+    """Pairs (1, 0) become (cos, sin).  Off by the last addition's half a step, and by what goes
+    into it: 2^-24 of its smaller term (at most half the result) from each of about three roundings,
+    less than a step altogether; the angle's own error in fp64 stands in front of its zeros."""
+    D, T = 128, 4096
+    rng = np.random.default_rng(5)
+    pos = rng.integers(-2 ** 17, 2 ** 17, T).astype(np.int32)
+    pos[:4] = 0, 1, -1, 131071
+    f = (1e6 ** (-np.arange(D // 2) / (D // 2))).astype(np.float32)
+    f[1], f[2] = 0.0, np.float32(np.pi / 2)                           # no turn, and almost quarter turns
+    x = np.zeros((T, 1, D), dtype=np.float32)
+    x[..., slice(0, None, 2) if inter else slice(0, D // 2)] = 1
+    t = torch.from_numpy(x).cuda()
+    got = ssd.ssd_attn_qk_norm_rope(t, t, dev(pos), torch.from_numpy(f).cuda(), interleaved=inter)[0].cpu().numpy()[:, 0]
+    cos, sin = (got[:, 0::2], got[:, 1::2]) if inter else (got[:, :D // 2], got[:, D // 2:])
+    angle = pos.astype(np.longdouble)[:, None] * f.astype(np.longdouble)
+    for y, want in ((cos, np.cos(angle)), (sin, np.sin(angle))):
+        size = np.spacing(np.abs(want).astype(np.float32)).astype(np.float64)
+        # (an angle of up to 2^17 2 radians in fp64 turns: two roundings of 2^-53 of it)
+        assert (np.abs(y - want) <= size + 2.0 ** -53 * 4 * np.abs(angle)).all()
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_far_and_negative_positions(io):
     pos = np.array([2 ** 31 - 1, -(2 ** 31), -5, 0, 1, 131071, 1 << 24], dtype=np.int32)
