@@ -34,7 +34,7 @@ def test_loads_wait_for_scalar_operands(name):
         assert states is None or states >= 5, f"{name}:{line}: {states} wait states ahead of the load"
 
 
-def test_checker():
+def test_the_scan_finds_what_it_should():
     assert wait_states(r"s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds") == 2
     assert wait_states(r"s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2") == 6
     assert wait_states(r"s_waitcnt vmcnt(%0)") is None
