@@ -943,17 +943,21 @@ __device__ __forceinline__ u32x4 tile_words(const void *base, int64_t rows, unsi
 // dst + 16 l (4 l).  They are written out here so that the compiler does not
 // insert its own waits for them (it cannot tell the ring slots apart and
 // would wait for every one in flight); their reader waits with wait_vmcnt and
-// a barrier.  Nothing is written to registers.
+// a barrier.  Nothing is written to registers.  The wait states that the
+// compiler does not see to inside a statement are in it: one between writing
+// m0 and the load, five between a vector instruction that writes a scalar
+// register (the descriptors' readfirstlane, ahead of the statement) and the
+// load that reads it.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_load16(unsigned dst, u32x4 rsrc, unsigned voff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :: "s"(dst), "v"(voff), "s"(rsrc) : "memory", "m0");
 }
 __device__ __forceinline__ void lds_load4(unsigned dst, u32x4 rsrc, unsigned voff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :: "s"(dst), "v"(voff), "s"(rsrc) : "memory", "m0");
 }
 #pragma clang diagnostic pop
