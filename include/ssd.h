@@ -441,7 +441,9 @@ ssd_status ssd_attn_decode_step(const ssd_attn_dims *dims, const void *q, const 
  *                   Written as m = half(min), s = half((max - min) / 15), both held
  *                   within +-65504, code = round((x - m) / s) within 0 .. 15 (ties to
  *                   even; 0 where s is 0).  Values within +-65504 are off by half a step
- *                   at most, beside the roundings of m and s.
+ *                   at most, beside the roundings of m and s.  64 values with a NaN among
+ *                   them, or of infinities of one sign alone, have a step of NaN and
+ *                   come back as NaN, all of them.
  * Supported: D in {64, 128, 256}, page_size a power of two from 16 to 1024,
  * max_pages * page_size < 2^31 - 4096, row strides up to 2^22.
  *

@@ -12,7 +12,9 @@
 // 4-bit rows.  Every 64 values of a row have a least value m = f16(min) and a step
 // s = f16((max - min) / 15); code = round((x - m) / s) in 0 .. 15, value = code s + m.
 // Half precision holds the pair in a dword and is an operand of the mixed-precision
-// multiply-add as it stands; its 11 bits keep the codes' range within 1% of a step.
+// multiply-add as it stands; its 11 bits keep the codes' range within 1% of a step.  A NaN
+// among the values makes both NaN, infinities of one sign alone the step (inf - inf): the
+// group comes back as NaN, as it would by the formula.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -70,6 +72,16 @@ template <int kLanes, typename Op> __device__ __forceinline__ float across(float
     if constexpr (kLanes > 16)                // lane ^ 16
         v = op(v, __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v), 0x401f)));
     return v;
+}
+
+// The lesser and the greater of two numbers, NaN if either is.
+__device__ __forceinline__ float least_of(float p, float q)
+{
+    return __builtin_elementwise_minimum(p, q);
+}
+__device__ __forceinline__ float most_of(float p, float q)
+{
+    return __builtin_elementwise_maximum(p, q);
 }
 
 // The sum of four squares, each rounded: a head's fours are then added in pairs of neighbours,
@@ -350,20 +362,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnA
                     float lo = y[0], hi = y[0];
 #pragma unroll
                     for (int e = 1; e < 8; ++e) {
-                        lo = fminf(lo, y[e]);
-                        hi = fmaxf(hi, y[e]);
+                        lo = least_of(lo, y[e]);
+                        hi = most_of(hi, y[e]);
                     }
-                    lo = across<8>(lo, [](float p, float q) { return fminf(p, q); });
-                    hi = across<8>(hi, [](float p, float q) { return fmaxf(p, q); });
-                    const _Float16 least = (_Float16)fminf(fmaxf(lo, -kHalfMax), kHalfMax);
-                    const _Float16 step = (_Float16)fminf((hi - lo) * (1.f / 15), kHalfMax);
+                    lo = across<8>(lo, least_of);
+                    hi = across<8>(hi, most_of);
+                    const _Float16 least = (_Float16)least_of(most_of(lo, -kHalfMax), kHalfMax);
+                    const _Float16 step = (_Float16)least_of((hi - lo) * (1.f / 15), kHalfMax);
                     const float fl = (float)least, fs = (float)step;
                     // The quotients, rounded as a division rounds them (its last steps, with one
                     // reciprocal for all) and to whole numbers by adding 3 2^22, whose low bits
                     // they become: its own bits, eight times shifted, add up to 0x3f400000.  (A step
-                    // of 0: all codes 0.)
+                    // of 0 or NaN: all codes 0.)
                     const float est = __builtin_amdgcn_rcpf(fs), top = 15.f * fs;
-                    const float inv = fs > 0.f ? __builtin_fmaf(__builtin_fmaf(-fs, est, 1.f), est, est) : 0.f;
+                    const float inv = __builtin_fmaf(__builtin_fmaf(-fs, est, 1.f), est, est);
                     unsigned codes = 0u - 0x3f400000u;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -371,6 +383,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnA
                         const float r = __builtin_fmaf(__builtin_fmaf(-q, fs, n), inv, q) + 12582912.f;
                         codes += __float_as_uint(r) << (4 * e);
                     }
+                    codes = fs > 0.f ? codes : 0u;
                     if (live && !isq) {
                         const int64_t at = line + ((int64_t)(isv ? h - Hq - Hkv : h - Hq) << a->c.shift);
                         reinterpret_cast<uint32_t *>(isv ? a->c.v : a->c.k)[at * (D / 8) + j] = codes;
