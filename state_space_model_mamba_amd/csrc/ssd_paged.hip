@@ -209,9 +209,15 @@ __device__ __forceinline__ void hide(f32x4 (&s)[CB][KB], int see, unsigned bad, 
     }
 }
 
-// x as kTerms bf16 numbers, the first its rounding and the others that of what is left.
+// x as kTerms bf16 numbers, the first its rounding and the others that of what is left: x - t,
+// exact, as a dot product with (-1, 0) or (0, -1), one instruction where taking the half out and
+// subtracting would be two.  (The pairs are kept in registers: the compiler would write (-1, 0)
+// as the inline constant -1.0, whose -1 the hardware has in the upper half.)
 template <int kTerms> __device__ __forceinline__ void terms_of(const float (&x)[8], bf16x8 (&t)[kTerms])
 {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    unsigned lo = 0x0000bf80u, hi = 0xbf800000u;
+    asm("" : "+s"(lo), "+s"(hi));
     float r[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -223,8 +229,9 @@ template <int kTerms> __device__ __forceinline__ void terms_of(const float (&x)[
         for (int e = 0; e < 4; ++e) {
             u[e] = opaque(pack_bf16(r[2 * e], r[2 * e + 1]));
             if (n + 1 < kTerms) {
-                r[2 * e] -= __uint_as_float(u[e] << 16);
-                r[2 * e + 1] -= __uint_as_float(u[e] & 0xffff0000u);
+                const bf16x2 two = __builtin_bit_cast(bf16x2, (unsigned)u[e]);
+                r[2 * e] = __builtin_amdgcn_fdot2_f32_bf16(two, __builtin_bit_cast(bf16x2, lo), r[2 * e], false);
+                r[2 * e + 1] = __builtin_amdgcn_fdot2_f32_bf16(two, __builtin_bit_cast(bf16x2, hi), r[2 * e + 1], false);
             }
         }
         t[n] = __builtin_bit_cast(bf16x8, u);
@@ -360,20 +367,26 @@ template <typename T_, int D, int CB> struct WideTile {
 // Pages of 4-bit codes
 // ---------------------------------------------------------------------------
 // A value costs one instruction to unpack where a bf16 page costs none, so the work around it
-// is kept off the vector units.  Two codes n, n' of a dword's halves become the bf16 pair
-// (16 + n, 16 + n') with a shift and an and-or, and that is the products' operand: with step s
-// and least value m of the 64 values of group G,
-//     q . k_G = s (sum q (16 + n)) + (m - 16 s) sum q        (the 16s: the product's initial value)
-//     sum_t p_t v_t = sum_t (p_t s_t) (16 + n_t) + sum_t p_t (m_t - 16 s_t)
+// is kept off the vector units.  A byte n < 16 taken as an fp8 number (e4m3) is n 2^-9, so a
+// dword's codes, four to a masked dword, become bf16 numbers n by conversions from fp8 with a
+// scale of 2^9, two each, and those are the products' operand: with step s and least value m of
+// the 64 values of group G,
+//     q . k_G = s (sum q n) + m sum q
+//     sum_t p_t v_t = sum_t (p_t s_t) n_t + sum_t p_t m_t
 // so that scales cost one multiply-add per score or probability and group instead of one
-// per value.  Keys are read as stored; values through the 4-bit transpose read, 16 keys
-// of one column at a time.  p s enters as two bf16 numbers.  Where queries are fp32 both
-// enter as three, and codes as (n - 8) / 16 with m + 8 s for m - 16 s: the two sums, which
-// nearly cancel, are then a few times smaller (3.6e-6 off against 64 bits otherwise), for
-// 2.5 instructions a value instead of one.
+// per value.  The second line's two sums grow with the number of keys where their sum need not
+// (values about 0), and their roundings with them.  So two of every four keys count from the top,
+//     p v = -(p s) (15 - n) + p (m + 15 s),
+// whose sums run the other way; the complement is part of the mask.  p s enters as three bf16
+// numbers, which hold all of an fp32 number.  (With codes as 16 + n, all keys alike and two
+// terms, 0.4 - 1.6% of the outputs differed from the rounded formula, now 0.01 - 0.07% as of
+// fp32 products; 78 -> 82 us for 64 sequences of 100 - 8190 rows.)  Where queries are fp32 both
+// enter as three terms, and codes as (n - 8) / 16 with m + 8 s for m: 2.5 instructions a value.
+// Keys are read as stored; values through the 4-bit transpose read, 16 keys of one column at a
+// time.
 //
 // Tiles of 64 keys, or 32 where one is 5 KB and more (shorter chains in front of a wave's
-// first result and fewer registers; 131000 keys of 128: 43 -> 40 us): [keys][D / 2] bytes
+// first result and fewer registers; 131000 keys of 128: 46 -> 42 us): [keys][D / 2] bytes
 // of keys, the same of values, then the scales [part][group][16 keys] of both.  Rows are not
 // padded; their 16-byte chunks are permuted by an XOR with swz(row), so that reads of 16
 // rows cover the banks evenly.
@@ -384,36 +397,47 @@ template <typename T_, int D, int CB> struct CodeTile {
     static constexpr int kRow = D / 2, kPart = 16 * kRow, kSide = kParts * kPart, kScales = kKT * 4 * G;
     static constexpr int kBuf = 2 * kSide + 2 * kScales;
     static constexpr int kNW = 4;
-    // Work-groups of a CU: 256 registers a wave, or 512 where two blocks of columns of wide heads
-    // or fp32 queries of 256 need them.  With fewer the kernels spill: 32 sequences of 8000, 60
-    // heads over 3 of 128, take 77 us instead of 64; 16 of them, 16 heads over 4 of 256 in fp32,
-    // 91 instead of 78; 64 of 100 - 8190, 32 heads over one of 64, 55 instead of 25 at 128.
+    // Work-groups of a CU: two at 256 registers a wave, or one at 512 where two blocks of columns
+    // of wide heads, or fp32 queries of 256, take more (with bf16 queries 292 at 128, 476 at 256).
+    // 16 sequences of 8000 rows in fp32: 16 heads over 4 of 256 77 us, with two 90; 32 heads over
+    // one of 128 27, with two 47.  In bf16 64 of 100 - 8190 rows, 32 heads over one of 128, 36 and
+    // 38, but 32 of 8000, 60 heads over 3, 66 and 62.  Registers that spill all the same: six of
+    // fp32 queries of 64 and 127 of those of 256, both with two blocks of columns.
     static constexpr int kMost = (CB == 2 && D > 64) || (D == 256 && sizeof(T) == 4) ? 1 : 2;
     // Work-groups of a CU raise their priority in every other tile, in turn: the older one would
-    // otherwise finish first and leave the other alone (2 - 5% of the time; the reverse with two
-    // blocks of columns).
+    // otherwise finish first and leave the other alone (2 - 5% of the time; with two blocks of
+    // columns no difference).
     static constexpr bool kTurns = CB == 1;
     static constexpr int kPer = kPart > 1024 ? kPart / 1024 : 1;          // loads of a part's codes
     static constexpr int kLoads = kParts * (2 * kPer + 2);
-    static constexpr int kQ = sizeof(T) == 2 ? 1 : 3, kP = sizeof(T) == 2 ? 2 : 3;
+    static constexpr int kQ = sizeof(T) == 2 ? 1 : 3, kP = 3;
     static constexpr bool kCentred = sizeof(T) == 4;
 
-    // (constants kept in registers: as literals they would split and-or into two instructions)
-    unsigned mask, sixteen, low, hundred;
+    // (constants kept in registers: as literals they would be part of every instruction)
+    unsigned low, top;                        // codes of a dword in its bytes; which of them count from the top
     float zero;
     bf16x8 qf[CB][D / 32][kQ];                // queries, in the order of opened()
-    float qs[CB][G], qb[CB][G];               // their sums over a group, as they are and times the keys' biases
-    float rest[CB][G];                        // sum of p m (centred: p (m + 8 s))
-    f32x4 over[kCentred ? 1 : CB][kCentred ? 1 : G];   // the values' biases times p s, summed
+    float qs[CB][G];                          // their sums over a group
+    float rest[CB][G];                        // sum of p m or p (m + 15 s) (centred: p (m + 8 s))
 
     static __device__ __forceinline__ int swz(int row)
     {
         return D == 64 ? 0 : D == 128 ? (row >> 2) & 3 : (row >> 1) & 7;
     }
 
-    // Codes 0 .. 7 of a dword as 16 + code (centred: (code - 8) / 16), in the order 0, 4, 1,
-    // 5, 2, 6, 3, 7.  kKey: the first two as 128 + code, which saves a shift; sums over values
-    // keep to 16, their biases being part of a sum over all rows.
+    // The code that element e of opened() is.
+    static __host__ __device__ constexpr int code_of(int e)
+    {
+        return kCentred ? (e >> 1) + 4 * (e & 1) : e < 4 ? 2 * e : 2 * e - 7;
+    }
+    // Whether a value's code counts from the top there.
+    static __host__ __device__ constexpr bool from_top(int code)
+    {
+        return !kCentred && ((code & 3) == 1 || (code & 3) == 2);
+    }
+
+    // Codes 0 .. 7 of a dword, keys' as they are and some of the values' from the top; centred:
+    // (code - 8) / 16.
     template <bool kKey> __device__ __forceinline__ bf16x8 opened(unsigned w) const
     {
         u32x4 v;
@@ -425,11 +449,18 @@ template <typename T_, int D, int CB> struct CodeTile {
                                  __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * i + 16))));
             return __builtin_bit_cast(bf16x8, v);
         }
-        v[0] = kKey ? (w & low) | hundred : ((w << 3) & mask) | sixteen;
-        v[1] = ((w >> 1) & mask) | sixteen;
-        v[2] = ((w >> 5) & mask) | sixteen;
-        v[3] = ((w >> 9) & mask) | sixteen;
+        const unsigned even = (kKey ? w : w ^ top) & low, odd = (kKey ? w >> 4 : (w >> 4) ^ ~top) & low;
+        v[0] = pair<false>(even);
+        v[1] = pair<true>(even);
+        v[2] = pair<false>(odd);
+        v[3] = pair<true>(odd);
         return __builtin_bit_cast(bf16x8, v);
+    }
+
+    // Two bytes below 16 of a dword's lower or upper half as bf16 numbers.
+    template <bool kUpper> static __device__ __forceinline__ unsigned pair(unsigned bytes)
+    {
+        return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, 512.f, kUpper));
     }
 
     __device__ __forceinline__ void begin(const PagedArgs &a, unsigned at, int lane)
@@ -437,18 +468,16 @@ template <typename T_, int D, int CB> struct CodeTile {
         typedef Tile<T, D> TL;
         constexpr int kRaw = sizeof(T) == 2 ? 1 : 2;             // 16-byte pieces of eight queries
         const int c = lane & 15, g = lane >> 4;
-        mask = 0x00780078u;
-        sixteen = 0x41804180u;
-        low = 0x000f000fu;
-        hundred = 0x43004300u;                // 128
+        low = 0x0f0f0f0fu;
+        top = 0xff00ff00u;                    // codes 2 and 6 of the even ones, and the others of the odd ones: 1 and 5
         zero = 0.f;
-        asm volatile("" : "+s"(mask), "+v"(sixteen), "+s"(low), "+v"(hundred), "+v"(zero));
+        asm volatile("" : "+s"(low), "+s"(top), "+v"(zero));
         const unsigned sign = a.neg ? 0x80000000u : 0u;
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int s = 0; s < G; ++s) {
-                float sum = 0.f, first = 0.f;
+                float sum = 0.f;
 #pragma unroll
                 for (int p = 2 * s; p < 2 * s + 2; ++p) {
                     float x[8], y[8];
@@ -464,17 +493,13 @@ template <typename T_, int D, int CB> struct CodeTile {
                         x[e] = __uint_as_float(u ^ sign);
                         sum += x[e];
                     }
-                    first += x[0] + x[4];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        y[e] = x[(e >> 1) + 4 * (e & 1)];
+                        y[e] = x[code_of(e)];
                     terms_of<kQ>(y, qf[cb][p]);
                 }
                 qs[cb][s] = quad_sum(sum);
-                qb[cb][s] = kCentred ? 0.f : __builtin_fmaf(-112.f, quad_sum(first), -16.f * qs[cb][s]);
                 rest[cb][s] = 0.f;
-                if constexpr (!kCentred)
-                    over[cb][s] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
     }
 
@@ -575,7 +600,7 @@ template <typename T_, int D, int CB> struct CodeTile {
                 const u32x4 ws = scales(buf + 2 * kSide + (unsigned)(kb * 64 * G + s * 64 + 16 * g));
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb) {
-                    f32x4 d = {qb[cb][s], qb[cb][s], qb[cb][s], qb[cb][s]};
+                    f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int n = 0; n < kQ; ++n) {
                         d = mma16(k0, qf[cb][2 * s][n], d);
@@ -595,11 +620,8 @@ template <typename T_, int D, int CB> struct CodeTile {
             hide(sc, see, bad, g);
         soften<D, CB, kParts>(sc, c, st, [&](int cb, float al) {
 #pragma unroll
-            for (int s = 0; s < G; ++s) {
+            for (int s = 0; s < G; ++s)
                 rest[cb][s] *= al;
-                if constexpr (!kCentred)
-                    over[cb][s] *= al;
-            }
         });
         // within 16 lanes, lane r addresses the row of key 16 (r / 4) + 4 g + r % 4 (of tiles of 32
         // keys: r % 8, and the upper eight lanes the next 16 columns)
@@ -618,21 +640,16 @@ template <typename T_, int D, int CB> struct CodeTile {
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const f16x2 h = __builtin_bit_cast(f16x2, (unsigned)(e & 1 ? w1 : w0)[e >> 1]);
-                        const float p = sc[cb][kb + (e & 1)][e >> 1];
-                        if constexpr (kCentred) {
-                            x[e] = p * (16.f * (float)h[0]);
-                            rest[cb][s] = __builtin_fmaf(p, __builtin_fmaf(8.f, (float)h[0], (float)h[1]), rest[cb][s]);
-                        } else {
-                            x[e] = __builtin_fmaf(p, (float)h[0], zero);
-                            rest[cb][s] = __builtin_fmaf(p, (float)h[1], rest[cb][s]);
-                        }
+                        const int code = code_of(e);             // (of eight keys: four of block kb, four of the next)
+                        const f16x2 h = __builtin_bit_cast(f16x2, (unsigned)(code >> 2 ? w1 : w0)[code & 3]);
+                        const float p = sc[cb][kb + (code >> 2)][code & 3];
+                        const float base = kCentred ? __builtin_fmaf(8.f, (float)h[0], (float)h[1])
+                                         : from_top(code) ? __builtin_fmaf(15.f, (float)h[0], (float)h[1]) : (float)h[1];
+                        rest[cb][s] = __builtin_fmaf(p, base, rest[cb][s]);
+                        x[e] = kCentred ? p * (16.f * (float)h[0])
+                                        : __builtin_fmaf(from_top(code) ? -p : p, (float)h[0], zero);
                     }
                     terms_of<kP>(x, pt[cb][kb / 2]);
-                    if constexpr (!kCentred)
-#pragma unroll
-                        for (int n = 0; n < kP; ++n)
-                            over[cb][s] = mma16(opened<false>(0u), pt[cb][kb / 2][n], over[cb][s]);
                 }
             }
 #pragma unroll
@@ -660,9 +677,7 @@ template <typename T_, int D, int CB> struct CodeTile {
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int s = 0; s < G; ++s) {
-                float r = quad_sum(rest[cb][s]);
-                if constexpr (!kCentred)
-                    r -= over[cb][s][0];          // (all rows of it are alike)
+                const float r = quad_sum(rest[cb][s]);
 #pragma unroll
                 for (int d = 4 * s; d < 4 * s + 4; ++d)
 #pragma unroll
