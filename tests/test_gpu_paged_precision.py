@@ -1,4 +1,4 @@
-"""One-token attention over 4-bit pages in bf16 is as near its formula as fp32 sums and
+"""One-token attention over paged caches in bf16 is as near its formula as fp32 sums and
 probabilities are, beside the output's one rounding.
 
 F = 2^-24.  Two kinds of inputs make errors visible that the output's rounding hides elsewhere:
@@ -42,7 +42,7 @@ def ints(x):
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("grp", [1, 20])
-@pytest.mark.parametrize("bits", [4])
+@pytest.mark.parametrize("bits", [4, 16])
 def test_probabilities_of_values_that_cancel(bits, D, grp):
     B, Hkv, page = 48, 2, 16
     rng = np.random.default_rng(D + grp + bits)
