@@ -84,11 +84,12 @@ __device__ __forceinline__ float most_of(float p, float q)
     return __builtin_elementwise_maximum(p, q);
 }
 
-// The sum of four squares, each rounded: a head's fours are then added in pairs of neighbours,
-// whatever the rotation's pairs, which is as near as fp32 sums come and, for D = 128, the order
-// of torch's mean.  4-bit codes depend on the last bits where a value lies between two: with
-// sums in another order, the hardware's reciprocal root and sincospif 17 - 28 of 21.7 million
-// differed from those of the formula written in torch, now none to two (for 3 us in 138).
+// The sum of four squares, each rounded.  A head's fours are then added in pairs, of neighbours
+// but where half pairs turn a part of the head: a turned lane's two, R / 2 apart there, come
+// first.  With neighbours that is the order of torch's mean for D = 128.  4-bit codes depend on
+// the last bits where a value lies between two: with sums in another order, the hardware's
+// reciprocal root and sincospif 17 - 28 of 21.7 million (heads turned whole) differed from those
+// of the formula written in torch, now none to two (for 3 us in 138).
 __device__ __forceinline__ float four_squares(const float *x)
 {
 #pragma clang fp contract(off)
