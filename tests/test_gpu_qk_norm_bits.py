@@ -31,7 +31,7 @@ def turn(D, part):
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("part,inter", TURNS)
 def test_reciprocal_roots(D, part, inter):
-    T, H = 512, 6
+    T, H = 500, 5
     rng = np.random.default_rng(D)
     x = rng.integers(-30, 31, (T, H, D)).astype(np.float32)
     x[..., 1:] *= rng.random((T, H, 1)) < 0.9                    # (some heads of one value)
