@@ -438,7 +438,9 @@ ssd_status ssd_attn_decode_step(const ssd_attn_dims *dims, const void *q, const 
  *                   of byte i and 2 i + 1 in the high half, and k_scales, v_scales
  *                   [num_pages, Hkv, page_size, D / 64, 2] in IEEE half precision: for
  *                   every 64 values a step s and a least value m, value = code s + m.
- *                   Written as m = half(min), s = half((max - min) / 15), both held
+ *                   Written as m = half(min), s = half((max - min) / 15), the fifteenth
+ *                   as a product with 1/15 in fp32 (of 11000 steps one is thus the
+ *                   neighbour of the rounded quotient), both held
  *                   within +-65504, code = round((x - m) / s) within 0 .. 15 (ties to
  *                   even; 0 where s is 0).  Values within +-65504 are off by half a step
  *                   at most, beside the roundings of m and s.  64 values with a NaN among

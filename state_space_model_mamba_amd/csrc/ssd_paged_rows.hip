@@ -10,7 +10,8 @@
 // Results are rounded once, to the output type.
 //
 // 4-bit rows.  Every 64 values of a row have a least value m = f16(min) and a step
-// s = f16((max - min) / 15); code = round((x - m) / s) in 0 .. 15, value = code s + m.
+// s = f16((max - min) / 15), the fifteenth as a product with 1/15 in fp32 (as torch divides by
+// a number); code = round((x - m) / s) in 0 .. 15, value = code s + m.
 // Half precision holds the pair in a dword and is an operand of the mixed-precision
 // multiply-add as it stands; its 11 bits keep the codes' range within 1% of a step.  A NaN
 // among the values makes both NaN, infinities of one sign alone the step (inf - inf): the
