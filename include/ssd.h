@@ -521,7 +521,8 @@ ssd_status ssd_attn_paged_append(const ssd_paged_dims *dims, const ssd_qk_rope *
  * ..) become the packed rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 of k and v
  * [rows, Hkv, D] in io_dtype, 4-bit values rounded to it.  What ssd_attn_prefill
  * attends for the next part of a prompt.  starts and cu_seqlens are HOST arrays; rows
- * past the table are SSD_ERR_SHAPE, rows on no page are 0.
+ * past the table are SSD_ERR_SHAPE, rows on no page are 0.  Pages are read in blocks of
+ * 16 lines (16 i ..); lines outside the rows asked for are dropped.
  */
 ssd_status ssd_attn_paged_gather(const ssd_paged_dims *dims, const int64_t *cu_seqlens,
                                  const int64_t *starts, const void *k_pages,
@@ -533,8 +534,9 @@ ssd_status ssd_attn_paged_gather(const ssd_paged_dims *dims, const int64_t *cu_s
  * ssd_attn_paged_decode_step -- ssd_attn_decode_step's attention over pages, after an
  * ssd_attn_paged_append of one token per sequence with the same lengths: q[b] attends
  * rows 0 .. lengths[b].  A length outside [0, max_pages page_size) marks an unused slot:
- * o[b] = 0.  Rows on no page are not attended, and other rows than those are not read;
- * o[b] is 0 also where no row is attended or all scores are -infinity.
+ * o[b] = 0.  Rows on no page are not attended; o[b] is 0 also where no row is attended or
+ * all scores are -infinity.  Of the pages only the attended rows are read, and lines of
+ * page 0 in place of rows on no page: those are read and dropped, whatever they hold.
  *   q, o [B, Hq, D] io_dtype; q_stride: elements between rows of q
  * The work is shared out on the device by the lengths, so the width of the table does
  * not matter, and results depend on the batch only by rounding (deterministic for the
