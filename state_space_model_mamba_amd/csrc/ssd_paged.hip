@@ -21,12 +21,12 @@
 //
 // Bound by memory over pages of the input type: one sequence of 131000 rows, 32 heads over
 // 8 of 128 in bf16, 98 us and the join's 5 (537 MB at 5.5 TB/s; a large copy reaches 5.08
-// on the same card); 64 of 100 - 8190 rows 193 with the append in front.  Over 4-bit pages
-// the instructions of a tile take about as long as its bytes: vector units 48% busy, matrix
-// units 15%, 33 us for the long sequence's 151 MB (4.5 TB/s) and 4 for the join, 70 and 5 for
-// the 64.  Small calls take 6 - 12 us: the look-ups in front of the first tile, a tile, and
-// the join's launch.  Tried and no better: twice and four times as many work-groups (8 and 25
-// us more: each starts with look-ups and an empty pipeline), a second round of small
+// on the same card); 64 of 100 - 8190 rows 193 - 211 with the append in front, by the lengths.
+// Over 4-bit pages a tile's instructions and waits take longer than its bytes: vector units 47%
+// busy, matrix units 16%, 38 us for the long sequence's 151 MB (4.0 TB/s) and 5 for the join,
+// 74 and 5 for the 64.  Small calls take 6 - 12 us: the look-ups in front of the first tile, a
+// tile, and the join's launch.  Tried and no better: twice and four times as many work-groups
+// (8 and 25 us more: each starts with look-ups and an empty pipeline), a second round of small
 // work-groups for the end (4 - 8 us more for even batches).
 #include <hip/hip_runtime.h>
 
@@ -716,10 +716,10 @@ void paged_decode_kernel(PagedArgs a)
 
     // This work-group's units [u0, u1) of all, and the sequence b that u0 lies in with the
     // units before it.  Beginning an item takes about as long as a unit (`extra`, its first unit
-    // then: without it work-groups with many short sequences end last, 88 us instead of 77 for 64
+    // then: without it work-groups with many short sequences end last, 94 us instead of 82 for 64
     // sequences of 100 - 8190 rows in 4 bits).  Up to 64 sequences of the same number of units do
-    // without: their items divide evenly more often (16 of 8000 rows, 32 heads over one of 256: 40
-    // us, 46 with).  Where there are no more units than work-groups each gets one, so that every
+    // without: their items divide evenly more often (16 of 8000 rows, 32 heads over one of 256: 36
+    // us, 43 with).  Where there are no more units than work-groups each gets one, so that every
     // work-group of an item has a piece of it.  Up to 64 sequences: every wave finds its share from
     // its own lanes.
     int before = 0, found, mylen = 0, extra;

@@ -189,7 +189,8 @@ enum { kNoPages, kPages, kPages4 };
 // copy 5.08); with the append of 21150 tokens 107 us, 4.8 TB/s.  Into 4 bits 114 us for 12%
 // fewer bytes, the vector units 68% busy and rows of 64 bytes written one by one.  Five waves
 // per SIMD in bf16, 96 registers each: with four (102, the compiler's own choice for the 4-bit
-// append) it and the reading back take 142 us, with five 138, with six, which spill, 154.
+// append) it and the reading back took 142 us, with five 138 (now 139, and one register of it
+// spills), with six, which spill more, 154.
 // One token takes 4.6 us, most of it the look-ups, one after the other.
 template <typename T, int D, int kKind>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnArgs args_in_kernarg)
@@ -372,10 +373,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 1) void turn_kernel(TurnA
                     const _Float16 least = (_Float16)least_of(most_of(lo, -kHalfMax), kHalfMax);
                     const _Float16 step = (_Float16)least_of((hi - lo) * (1.f / 15), kHalfMax);
                     const float fl = (float)least, fs = (float)step;
-                    // The quotients, rounded as a division rounds them (its last steps, with one
-                    // reciprocal for all) and to whole numbers by adding 3 2^22, whose low bits
-                    // they become: its own bits, eight times shifted, add up to 0x3f400000.  (A step
-                    // of 0 or NaN: all codes 0.)
+                    // The quotients, rounded as a division rounds them (Markstein's correction: the
+                    // residual n - q s, exact, times the refined reciprocal, which is one for all)
+                    // and to whole numbers by adding 3 2^22, whose low bits they become: its own
+                    // bits, eight times shifted, add up to 0x3f400000.  (A step of 0 or NaN: all
+                    // codes 0.)
                     const float est = __builtin_amdgcn_rcpf(fs), top = 15.f * fs;
                     const float inv = __builtin_fmaf(__builtin_fmaf(-fs, est, 1.f), est, est);
                     unsigned codes = 0u - 0x3f400000u;
