@@ -53,10 +53,10 @@ def quantise(x):
     """64 values: (codes, step, least)."""
     x = np.asarray(x, dtype=np.float64)
     lo, hi = x.min(), x.max()
-    with np.errstate(over="ignore"):
+    with np.errstate(over="ignore", invalid="ignore"):
         least = float(np.float16(np.clip(lo, -65504, 65504)))
         step = float(np.float16(min((hi - lo) / 15, 65504)))
-    code = np.zeros(len(x)) if step == 0 else np.clip(np.rint((x - least) / step), 0, 15)
+    code = np.clip(np.rint((x - least) / step), 0, 15) if step > 0 else np.zeros(len(x))   # (0 or NaN: 0)
     return code.astype(np.uint8), step, least
 
 
