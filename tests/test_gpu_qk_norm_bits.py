@@ -10,7 +10,10 @@ estimate alone exceeds half a unit for many z.)
 
 Whole heads, bounds for what the kernel does: every square rounded, F = 2^-24, and 3 additions
 to a sum of four, one to eight, log2(D / 8) to all: 5 + log2(D / 8) F of the sum, half of that of
-its root; the addition of eps, F / 2; the root, F; two products, F each."""
+its root; the addition of eps, F / 2; the root, F; two products, F each.  (With the rotation's
+sines and cosines, off by one unit in their last place at most, 2 F, its products and its sum,
+12.5 F of a pair's sizes: paged_cases.turn_bound takes 24 F, which it derives for sums in another
+order and for sines and cosines from the library.)"""
 import numpy as np
 import pytest
 import torch
